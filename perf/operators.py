@@ -151,7 +151,7 @@ def _cache(case, held, rows, spare, gen, layers):
     ref[order[:total].long()] = 1
     free = torch.full((num_pages,), -1, dtype=torch.int32, device=device)
     free[:spare] = order[total:]
-    control = torch.zeros(64, dtype=torch.int32, device=device)
+    control = torch.zeros(64 + 2 * 1024, dtype=torch.int32, device=device)
     control[1] = spare
     dtype = DTYPES[case["dtype"]]
     pool = torch.empty(layers, 2, num_pages, case["kv_heads"], case["page"], case["dim"], dtype=dtype, device=device)
