@@ -18,6 +18,8 @@ from ._lib import BF16, F32, DsparkError  # noqa: F401
 __all__ = ["draft_block", "draft_block_per_request", "draft_block_noalloc",
            "draft_block_profile", "draft_block_timeline", "sample_temperature",
            "draft_block_host", "HostWorkspace", "verify_standard", "verify_block",
+           "PagedCache", "TreeWorkspace", "cache_reserve", "cache_release",
+           "cache_fork", "cache_accept", "cache_append", "tree_attention",
            "noise_words", "workspace_bytes", "read_device_error",
            "DraftWorkspace", "DsparkError", "F32", "BF16", "version"]
 
@@ -400,6 +402,11 @@ def sample_temperature(logits, seed, offset, *, T: float = 1.0,
     return tokens, probs
 
 
+from .cache import (PagedCache, TreeWorkspace, cache_accept,  # noqa: E402
+                    cache_append, cache_fork, cache_release, cache_reserve,
+                    tree_attention)
+
+
 def noise_words(seed: int, offset: int, k: int, stream_id: int, n: int,
                 device=None, with_gumbel: bool = True, stream=None,
                 folded: bool = False):
@@ -418,8 +425,9 @@ def noise_words(seed: int, offset: int, k: int, stream_id: int, n: int,
     return out, g
 
 
-def read_device_error(workspace: DraftWorkspace, stream=None) -> int:
-    """Reads and clears the workspace's device error word (synchronises)."""
+def read_device_error(workspace, stream=None) -> int:
+    """Reads and clears the device error word of a DraftWorkspace or a
+    PagedCache (synchronises)."""
     code = ctypes.c_int(0)
     st = _lib.load().dspark_read_device_error(
         _ptr(workspace.buffer), ctypes.byref(code), _stream(stream))

@@ -38,12 +38,32 @@ EXPORTED = (
     "dspark_sample_workspace_bytes",
     "dspark_sample_temperature",
     "dspark_verify_block",
+    "dspark_cache_init",
+    "dspark_cache_reserve",
+    "dspark_cache_release",
+    "dspark_cache_fork",
+    "dspark_cache_accept",
+    "dspark_cache_append",
+    "dspark_tree_workspace_bytes",
+    "dspark_tree_attention",
     "dspark_noise_words",
     "dspark_noise_words_folded",
     "dspark_read_device_error",
     "dspark_status_string",
     "dspark_version",
 )
+
+
+class CacheStruct(ctypes.Structure):
+    """dspark_cache of include/dspark.h."""
+
+    _fields_ = [("pool", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("layers", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("max_seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("page_count", ctypes.c_void_p), ("ref_count", ctypes.c_void_p),
+                ("free_list", ctypes.c_void_p), ("control", ctypes.c_void_p)]
 
 
 class DsparkError(RuntimeError):
@@ -105,6 +125,23 @@ def load() -> ctypes.CDLL:
         lib.dspark_sample_temperature.argtypes = [
             P, P, ctypes.c_float, P, P, P, P, I, I, P, P, P, ctypes.c_size_t, P]
         lib.dspark_sample_temperature.restype = I
+        C, I64, F = ctypes.POINTER(CacheStruct), ctypes.c_int64, ctypes.c_float
+        lib.dspark_cache_init.argtypes = [C, P]
+        lib.dspark_cache_reserve.argtypes = [C, P, P, I, I, P]
+        lib.dspark_cache_release.argtypes = [C, P, I, P]
+        lib.dspark_cache_fork.argtypes = [C, P, P, P, I, P]
+        lib.dspark_cache_accept.argtypes = [C, P, P, P, P, I, I, I, I, P, P]
+        lib.dspark_cache_append.argtypes = [
+            C, I, P, P, P, P, I64, P, I64, P, I64, P, P, F, P, I, I, I, P, I,
+            I, I, P, P]
+        lib.dspark_tree_attention.argtypes = [
+            C, I, P, P, P, P, P, I64, P, I, F, I, I, I, P, P, P,
+            ctypes.c_size_t, P]
+        for name in ("init", "reserve", "release", "fork", "accept", "append"):
+            getattr(lib, "dspark_cache_" + name).restype = I
+        lib.dspark_tree_attention.restype = I
+        lib.dspark_tree_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.dspark_tree_workspace_bytes.restype = ctypes.c_size_t
         lib.dspark_noise_words.argtypes = [U64, U64, I, I, I, P, P, P]
         lib.dspark_noise_words.restype = I
         lib.dspark_noise_words_folded.argtypes = [U64, U64, I, I, I, P, P, P]

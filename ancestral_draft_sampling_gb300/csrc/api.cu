@@ -9,7 +9,6 @@
 // after every FFMA position, and one proposal writer for all positions.  No
 // host synchronisation, so the whole call can be captured in a CUDA graph.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -17,6 +16,7 @@
 #include <vector>
 
 #include "dspark_common.cuh"
+#include "host_util.cuh"
 
 namespace dspark {
 int generic_chunks_used(int V, int n_chunks);
@@ -26,34 +26,12 @@ namespace {
 
 using namespace dspark;
 
-bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
+bool aligned16(const void* p) { return aligned_to(p, 16); }
 
 bool sizes_supported(int B, int K, int V, int r) {
   return B >= 1 && B <= DSPARK_MAX_B && K >= 1 && K <= DSPARK_MAX_K &&
          V >= 1 && V <= DSPARK_MAX_V && r >= 16 && r <= DSPARK_MAX_R &&
          r % 16 == 0;
-}
-
-// Streaming multiprocessors of the current device (cached per device).
-int sm_count() {
-  static std::atomic<int> cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  int n = cache[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
-            cudaSuccess ||
-        n <= 0)
-      n = 1;
-    cache[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-dspark_status from_cuda(cudaError_t e) {
-  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 // Checks the arguments of dspark_draft_block and fills the kernel arguments.

@@ -1,0 +1,302 @@
+// cache_append.cu -- queries and keys normalised for each head and rotated by
+// their positions, and keys and values stored to the pages, in one pass.
+//
+// For a head's row x of D values: r = 1 / sqrt(mean(x^2) + eps), y = x r w,
+// then the pairs (a, b) of the first rot_dim values turn by the position's
+// angle: (a c - b s, b c + a s).  Everything is float32 and rounded once.
+// Every value is read once and written once, so the pass is bound by HBM for
+// prompts and by one launch's latency for single tokens.
+//
+// Vector kernel: a group of D * size / 16 lanes holds a row, 16 bytes a lane,
+// so a warp's load is 512 contiguous bytes; the mean is a butterfly over the
+// group, and the other half of a pair sits in the lane rot_dim / 2 values
+// away (or in the same lane, for neighbouring pairs).  A warp stays on one
+// token and loads kPer times before it stores, so the rotation's cosines are
+// loaded once for all its heads.  Rows that do not split that way (head_dim
+// not 16 bytes times a power of two up to 32 lanes, or halves that end inside
+// a lane's words) take the row kernel: a warp for each row, through shared
+// memory.
+#include "cache.cuh"
+#include "host_util.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr int kThreads = 128;
+
+template <typename T>
+struct Word;  // 16 bytes of T as float32
+template <>
+struct Word<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void load(const uint4& w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 store(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                      __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void load(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 store(const float (&x)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Where a token goes.  page < 0: its keys and values are not stored.
+struct Token {
+  int b, t, page, slot, position;
+  bool there;
+};
+
+__device__ __forceinline__ Token find_token(const AppendArgs& a, int i, bool report) {
+  Token k;
+  k.b = i / a.T;
+  k.t = i - k.b * a.T;
+  k.page = -1;
+  k.slot = 0;
+  k.position = a.position[i];
+  const int s = cache_seq(a.c, a.seq, k.b);
+  k.there = s >= 0 && (a.count == nullptr || k.t < a.count[k.b]);
+  if (s < 0 && report) cache_error(a.c, kCacheErrSeq);
+  if (!k.there) return k;
+  const long long at = (long long)a.length[k.b] + k.t;
+  if (at >= k.t && at < (long long)cache_held(a.c, s) * a.c.page_size) {
+    k.page = cache_page(a.c, s, (int)(at / a.c.page_size), a.c.max_pages);
+    k.slot = (int)(at % a.c.page_size);
+  }
+  if (k.page < 0 && report) cache_error(a.c, kCacheErrPage);
+  if (k.position < 0 || k.position >= a.max_position) {
+    k.position = -1;
+    if (report) cache_error(a.c, kCacheErrPosition);
+  }
+  return k;
+}
+
+// Row `h` of token k: queries, then keys, then values.  Null if there is no
+// such row, or nothing to store it to.
+struct Row {
+  const char* src;
+  char* dst;
+  const float* weight;
+  bool rotate;
+};
+
+__device__ __forceinline__ Row find_row(const AppendArgs& a, const Token& k, int h) {
+  const int Hq = a.heads, Hk = a.c.kv_heads;
+  const size_t elt = dtype_bytes(a.c.dtype), row = a.c.head_dim * elt;
+  const size_t token = (size_t)k.b * a.T + k.t;
+  Row r{nullptr, nullptr, nullptr, false};
+  if (h < Hq) {
+    r.src = a.q + token * a.q_stride * elt + h * row;
+    r.dst = a.q_out + (token * Hq + h) * row;
+    r.weight = a.q_weight;
+    r.rotate = true;
+  } else if (h < Hq + 2 * Hk && k.page >= 0) {
+    const bool key = h < Hq + Hk;
+    const int g = h - Hq - (key ? 0 : Hk);
+    r.src = key ? a.k + token * a.k_stride * elt + g * row
+                : a.v + token * a.v_stride * elt + g * row;
+    r.dst = static_cast<char*>(a.c.pool) +
+            cache_row(a.c, 2 * a.layer + (key ? 0 : 1), k.page, g, k.slot);
+    r.weight = key ? a.k_weight : nullptr;
+    r.rotate = key;
+  }
+  return r;
+}
+
+template <typename T, int kPer>
+__global__ void __launch_bounds__(kThreads)
+    append_kernel(AppendArgs a, int lanes, int splits) {
+  constexpr int N = Word<T>::n;
+  const int lane = threadIdx.x & 31;
+  const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int token = w / splits, split = w - token * splits;
+  if (token >= a.B * a.T) return;
+  const Token k = find_token(a, token, lane == 0 && split == 0);
+  if (!k.there) return;
+  const int sub = lane & (lanes - 1), per_warp = 32 / lanes;
+  const int d0 = sub * N, half = a.rot >> 1;
+  const int h0 = split * kPer * per_warp + lane / lanes;
+
+  uint4 word[kPer];
+  Row row[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    row[i] = find_row(a, k, h0 + i * per_warp);
+    word[i] = make_uint4(0, 0, 0, 0);
+    if (row[i].src) word[i] = *reinterpret_cast<const uint4*>(row[i].src + 16 * sub);
+  }
+  // the angle of each of the lane's values; the sine carries the sign
+  float cs[N], sn[N];
+  int partner = lane;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    cs[e] = 1.0f;
+    sn[e] = 0.0f;
+  }
+  if (k.position >= 0) {
+    const float* table = a.cos_sin + (size_t)k.position * a.rot;
+    if (!a.interleaved && d0 < a.rot) {
+      const bool low = d0 < half;  // half is a multiple of N: all N or none
+      partner = low ? lane + half / N : lane - half / N;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int i = low ? d0 + e : d0 + e - half;
+        cs[e] = table[i];
+        sn[e] = low ? -table[half + i] : table[half + i];
+      }
+    } else if (a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (d0 + e < a.rot) {
+          const int i = (d0 + e) >> 1;
+          cs[e] = table[i];
+          sn[e] = e & 1 ? table[half + i] : -table[half + i];
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    float x[N];
+    Word<T>::load(word[i], x);
+    if (a.q_weight || a.k_weight) {  // the butterfly is the whole warp's
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum = fmaf(x[e], x[e], sum);
+      for (int m = lanes >> 1; m > 0; m >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      if (row[i].weight) {
+        const float r = rsqrtf(sum / (float)a.c.head_dim + a.eps);
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = x[e] * r * row[i].weight[d0 + e];
+      }
+    }
+    float y[N];
+    if (a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = x[e ^ 1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
+    }
+    if (!row[i].dst) continue;
+    if (row[i].rotate) {
+      // a value that is not turned keeps its bits (0 * infinity is no 0)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (k.position >= 0 && d0 + e < a.rot) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
+      word[i] = Word<T>::store(x);
+    }
+    *reinterpret_cast<uint4*>(row[i].dst + 16 * sub) = word[i];
+  }
+}
+
+// A warp for each row, any head_dim and rot_dim.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_row_kernel(AppendArgs a) {
+  __shared__ float buf[kThreads / 32][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = a.heads + 2 * a.c.kv_heads, D = a.c.head_dim;
+  const long long w = (long long)blockIdx.x * (kThreads / 32) + warp;
+  const int token = (int)(w / rows), h = (int)(w - (long long)token * rows);
+  if (token >= a.B * a.T) return;
+  const Token k = find_token(a, token, lane == 0 && h == 0);
+  if (!k.there) return;
+  const Row r = find_row(a, k, h);
+  if (!r.src) return;
+  const T* src = reinterpret_cast<const T*>(r.src);
+  T* dst = reinterpret_cast<T*>(r.dst);
+  if (!r.rotate) {  // values: the bits
+    for (int d = lane; d < D; d += 32) dst[d] = src[d];
+    return;
+  }
+  float sum = 0.0f;
+  for (int d = lane; d < D; d += 32) {
+    const float x = to_float(src[d]);
+    buf[warp][d] = x;
+    sum = fmaf(x, x, sum);
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  const float rs = r.weight ? rsqrtf(sum / (float)D + a.eps) : 1.0f;
+  __syncwarp();
+  const int half = a.rot >> 1;
+  const float* table = a.cos_sin + (size_t)(k.position < 0 ? 0 : k.position) * a.rot;
+  for (int d = lane; d < D; d += 32) {
+    float x = buf[warp][d];
+    if (r.weight) x = x * rs * r.weight[d];
+    if (k.position >= 0 && d < a.rot) {
+      const int i = a.interleaved ? d >> 1 : d < half ? d : d - half;
+      const bool low = a.interleaved ? !(d & 1) : d < half;
+      const int o = a.interleaved ? d ^ 1 : low ? d + half : d - half;
+      float y = buf[warp][o];
+      if (r.weight) y = y * rs * r.weight[o];
+      const float sn = table[half + i];
+      x = fmaf(x, table[i], low ? -y * sn : y * sn);
+    }
+    put(dst + d, x);
+  }
+}
+
+template <typename T>
+cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
+  constexpr int N = Word<T>::n;
+  const int D = a.c.head_dim, lanes = D / N;
+  const int rows = a.heads + 2 * a.c.kv_heads;
+  const long long tokens = (long long)a.B * a.T;
+  const bool whole = D % N == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0 &&
+                     (a.interleaved || (a.rot >> 1) % N == 0);
+  if (!whole) {
+    const long long blocks = (tokens * rows + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    append_row_kernel<T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  // rows of a warp's load, and loads of a token
+  const int per_warp = 32 / lanes, loads = (rows + per_warp - 1) / per_warp;
+  // four loads a warp where that still leaves every multiprocessor 16 warps,
+  // else one: fewer tokens than that are bound by latency
+  const bool many = tokens * loads / 4 >= 16LL * sm_count();
+  const int splits = many ? (loads + 3) / 4 : loads;
+  const long long blocks = (tokens * splits + kThreads / 32 - 1) / (kThreads / 32);
+  if (tokens * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (many)
+    append_kernel<T, 4><<<(unsigned)blocks, kThreads, 0, stream>>>(a, lanes, splits);
+  else
+    append_kernel<T, 1><<<(unsigned)blocks, kThreads, 0, stream>>>(a, lanes, splits);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
+  return a.c.dtype == DSPARK_F32 ? launch<float>(a, stream)
+                                 : launch<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace dspark

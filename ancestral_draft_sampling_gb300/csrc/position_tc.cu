@@ -53,12 +53,11 @@
 // Every mbarrier wait is bounded; on a timeout the kernel records an error
 // in the workspace control word, stops issuing work, waits (bounded) for
 // its in-flight copies and MMAs, frees its TMEM and returns.
-#include <cudaTypedefs.h>
-
 #include <cstdlib>
 #include <mutex>
 
 #include "dspark_common.cuh"
+#include "host_util.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dspark {
@@ -1004,20 +1003,6 @@ bool stall_first_wait_requested() {
   return env != nullptr && env[0] == '1';
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 struct Layout {
   int bpad, stages, stage_bufs;
   uint32_t u_off, tile_off, stage_off, rows_off, rstate_off, bar_off;
@@ -1069,7 +1054,7 @@ CUresult encode_position_map(CUtensorMap* map, CUtensorMapDataType dt,
   const cuuint32_t estr[2] = {1, 1};
   void* addr = const_cast<char*>(static_cast<const char*>(base)) +
                (size_t)k * V * elt;
-  return encode_fn()(map, dt, 2, addr, dims, strides, box, estr,
+  return tensor_map_encoder()(map, dt, 2, addr, dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1118,7 +1103,7 @@ bool position_tc_supported(const DraftArgs& a) {
   return a.w_dtype == DSPARK_BF16 && a.r % 16 == 0 && a.r <= 256 &&
          a.V % 8 == 0 && per_group <= kMaxBpad &&
          make_layout(per_group, a.r, elt).stages >= kMinStages &&
-         encode_fn() != nullptr;
+         tensor_map_encoder() != nullptr;
 }
 
 // CTAs of the tensor-core kernel: one per SM, at most one per vocab tile.
@@ -1130,7 +1115,7 @@ int position_tc_chunks(int V, int sm_count) {
 
 cudaError_t launch_position_tc(const DraftArgs& a, int k, int n_chunks,
                                cudaStream_t stream) {
-  if (!encode_fn()) return cudaErrorNotSupported;
+  if (!tensor_map_encoder()) return cudaErrorNotSupported;
   if (a.B > kMaxBpad) return cudaErrorInvalidValue;  // a request group at most
   const int elt = a.base_dtype == DSPARK_F32 ? 4 : 2;
   const Layout L = make_layout(a.B, a.r, elt);
@@ -1140,7 +1125,7 @@ cudaError_t launch_position_tc(const DraftArgs& a, int k, int n_chunks,
     const cuuint64_t strides[1] = {(cuuint64_t)a.V * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)kKChunk};
     const cuuint32_t estr[2] = {1, 1};
-    if (encode_fn()(&wb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+    if (tensor_map_encoder()(&wb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                     const_cast<void*>(a.Wb), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -394,6 +394,217 @@ DSPARK_API dspark_status dspark_sample_temperature(
     const int32_t* position, int R, int V, int32_t* tokens, float* probs,
     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------ the paged key/value cache
+ *
+ * The steps around the draft block that read and write a model's (or a
+ * drafter's) key/value cache: room for a step's tokens is reserved, each
+ * layer's queries and keys are normalised and rotated and the keys and
+ * values stored, the drafted tokens attend over the cache, and after
+ * verification the accepted path is moved together and the pages behind it
+ * are freed.  A sequence can be forked: its full pages are shared.
+ *
+ * The caller owns every array.  A cache of S = max_seqs sequences:
+ *   pool         [layers][2][num_pages][kv_heads][page_size][head_dim] dtype,
+ *                keys in plane 0 of a layer and values in plane 1; 16-byte
+ *                aligned.
+ *   block_table  [max_seqs][max_pages] int32: entry i of a row is the page of
+ *                tokens i * page_size .. of that sequence; -1 behind the held
+ *                pages.
+ *   page_count   [max_seqs] int32: pages that a sequence holds.
+ *   ref_count    [num_pages] int32: sequences that hold a page.
+ *   free_list    [num_pages] int32: a stack of the free pages; pages are
+ *                taken from its top.
+ *   control      [DSPARK_CACHE_CONTROL_WORDS] int32, 16-byte aligned: [0] the
+ *                device error word (dspark_read_device_error reads and clears
+ *                it; calls on a cache set it and never clear it), [1] the
+ *                number of free pages, [2] a counter that every call leaves
+ *                at 0; scratch from word 64 on.
+ * Lengths are the caller's: `length` [B] int32 is the number of committed
+ * tokens of each sequence of a call.  `seq` [B] int32 (or NULL: 0..B-1)
+ * names the sequences, each at most once in a call.
+ * Limits: 1 <= layers <= 1024, page_size <= 4096, head_dim a multiple of 8
+ * up to 256, kv_heads <= 1024, max_seqs * max_pages < 2^31, num_pages < 2^31,
+ * max_pages * page_size < 2^31, B <= 1024.  The pool is addressed in 64 bits.
+ *
+ * Sequences, pages, positions and paths that are out of range are seen on
+ * the device: the entry is skipped as its call says and the error word is
+ * set (6: a seq outside [0, max_seqs); 7: a length or page outside what the
+ * sequence holds; 8: no free page left, or more pages than a table row has;
+ * 9: an accepted path or length that is not one; 10: a position outside the
+ * rotation table; 11: a fork whose child is a parent, or twice a child).
+ * Calls on one cache must follow one another (one stream, or ordered by the
+ * caller); calls on different caches are independent. */
+typedef struct {
+  void* pool;
+  dspark_dtype dtype;
+  int layers, num_pages, kv_heads, page_size, head_dim;
+  int max_seqs, max_pages;
+  int32_t* block_table;
+  int32_t* page_count;
+  int32_t* ref_count;
+  int32_t* free_list;
+  int32_t* control;
+} dspark_cache;
+
+#define DSPARK_CACHE_MAX_B 1024
+#define DSPARK_CACHE_CONTROL_WORDS (64 + 2 * DSPARK_CACHE_MAX_B)
+#define DSPARK_TREE_MAX_TOKENS 64
+#define DSPARK_TREE_MAX_GROUP 32
+
+/*
+ * dspark_cache_init -- an empty cache: no sequence holds a page, every page
+ * is free (page 0 on top of the stack), the error word is 0.  The pool is
+ * left as it is.  One launch, graph capturable.
+ */
+DSPARK_API dspark_status dspark_cache_init(const dspark_cache* cache,
+                                           cudaStream_t stream);
+
+/*
+ * dspark_cache_reserve -- pages for `tokens` (>= 0) more tokens of each of B
+ * sequences: afterwards sequence seq[b] holds at least
+ * ceil((length[b] + tokens) / page_size) pages.  Pages are taken in the order
+ * of b and, within a sequence, of its tokens.  A sequence whose table row is
+ * too short, or for which too few pages are free, gets none (error 8), and
+ * the others are served.  One launch.
+ */
+DSPARK_API dspark_status dspark_cache_reserve(const dspark_cache* cache,
+                                              const int32_t* seq,
+                                              const int32_t* length,
+                                              int tokens, int B,
+                                              cudaStream_t stream);
+
+/*
+ * dspark_cache_release -- the B sequences give up all their pages.  Pages
+ * that no sequence holds any more go back on the stack, the last one first
+ * (so reserving and releasing the same sequences leaves the stack as it
+ * was).  One launch.
+ */
+DSPARK_API dspark_status dspark_cache_release(const dspark_cache* cache,
+                                              const int32_t* seq, int B,
+                                              cudaStream_t stream);
+
+/*
+ * dspark_cache_fork -- sequence child[b] becomes a copy of the first
+ * length[b] tokens of sequence parent[b], in every layer: the full pages are
+ * shared, and the tokens of a page that is partly filled are copied to a page
+ * of the child's own.  Pages that the child held before are given up first.
+ * Several children may have the same parent; a child that is also a parent
+ * of the call, or is named twice, makes the whole call do nothing (error 11).
+ * A child whose parent holds fewer than length[b] tokens (error 7), or for
+ * which no page is free (error 8), ends up empty.  Two launches.
+ */
+DSPARK_API dspark_status dspark_cache_fork(const dspark_cache* cache,
+                                           const int32_t* parent,
+                                           const int32_t* child,
+                                           const int32_t* length, int B,
+                                           cudaStream_t stream);
+
+/*
+ * dspark_cache_accept -- keeps the accepted ones of the `tokens` tokens that
+ * follow the committed ones: n = accepted_len[b] + extra of them stay (none
+ * if accepted_len[b] < 0, verification's report of a bad request).
+ *
+ *   path         [B, path_width] int32 or NULL: the i-th kept token is the
+ *                one at length[b] + path[b][i], strictly increasing in i and
+ *                below `tokens`; it moves to length[b] + i, keys and values,
+ *                in every layer.  NULL: the kept tokens are the first n.
+ *   accepted_len [B] int32, as the verification calls write it.
+ *   extra        tokens kept besides the accepted drafts (1 when the tokens
+ *                start with the last emitted one).
+ *   new_length   [B] int32 out (may be `length`): length[b] + n.
+ * Pages behind the kept tokens are given up as dspark_cache_release does.  A
+ * path that is not one, or n > path_width or tokens, keeps nothing (error 9).
+ * One launch.
+ */
+DSPARK_API dspark_status dspark_cache_accept(
+    const dspark_cache* cache, const int32_t* seq, const int32_t* length,
+    const int32_t* accepted_len, const int32_t* path, int path_width,
+    int extra, int tokens, int B, int32_t* new_length, cudaStream_t stream);
+
+/*
+ * dspark_cache_append -- the queries and keys of T new tokens of each of B
+ * sequences, normalised for each head and rotated by their positions, in one
+ * pass; keys and values go to the cache of `layer`, token t of sequence b to
+ * place length[b] + t (whose page must be held: dspark_cache_reserve).
+ *
+ *   q            [B,T,heads,D], k and v [B,T,kv_heads,D], the cache's dtype,
+ *                D = head_dim; a token's heads are dense, and consecutive
+ *                tokens lie q_stride, k_stride, v_stride elements apart (so
+ *                the three may be parts of one projection's output).
+ *                16-byte aligned, strides multiples of 8 elements.
+ *   q_weight, k_weight  [D] float32 or NULL: y = x / sqrt(mean(x^2) + eps) * w
+ *                over each head (NULL: no normalisation).
+ *   cos_sin      [max_position][rot_dim] float32: rot_dim / 2 cosines, then
+ *                the sines.  The first rot_dim (even, <= D) dims are rotated:
+ *                pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) when
+ *                `interleaved`: (a, b) -> (a c - b s, b c + a s).
+ *   position     [B,T] int32 rows of cos_sin.
+ *   token_count  [B] int32 or NULL (T): tokens of sequence b; later rows of
+ *                q_out and later places of the cache are left as they are.
+ *   q_out        [B,T,heads,D] dense (may be q when that is dense).
+ * Everything runs in float32 and is rounded once; values are copied.  A token
+ * whose page is not held is not stored (error 7); one with a position outside
+ * the table is not rotated (error 10).  One launch, B * T < 2^24.
+ */
+DSPARK_API dspark_status dspark_cache_append(
+    const dspark_cache* cache, int layer, const int32_t* seq,
+    const int32_t* length, const int32_t* token_count, const void* q,
+    int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const float* q_weight, const float* k_weight, float eps,
+    const float* cos_sin, int max_position, int rot_dim, int interleaved,
+    const int32_t* position, int B, int T, int heads, void* q_out,
+    cudaStream_t stream);
+
+/* Device workspace of dspark_tree_attention (0 if unsupported). */
+DSPARK_API size_t dspark_tree_workspace_bytes(int B, int T, int heads,
+                                              int kv_heads, int head_dim);
+
+/*
+ * dspark_tree_attention -- attention of T drafted tokens of each of B
+ * sequences over the cache of `layer`, the drafted tokens' own keys and values
+ * included (they lie behind the committed ones, see dspark_cache_append).
+ *
+ *   q            [B,T,heads,D] dense, the cache's dtype, 16-byte aligned.
+ *                heads = group * kv_heads; query head h reads key head
+ *                h / group.
+ *   mask         uint64 words or NULL: bit j of word t says that token t sees
+ *                drafted token j: the ancestors of t in a tree of drafts and
+ *                t itself, all tokens in a block that sees itself whole.
+ *                mask_stride words lie between two sequences (0: one tree for
+ *                all).  NULL: token t sees tokens 0..t.
+ *   token_count  [B] int32 or NULL (T): drafted tokens of sequence b.  Later
+ *                rows of out and lse are left as they are, later keys are not
+ *                read.
+ *   window       0, or the number of positions that a token sees: token t
+ *                sees committed token j if position[b][t] - j < window.  The
+ *                mask alone rules the drafted tokens.
+ *   position     [B,T] int32 or NULL (length[b] + t), used with a window; a
+ *                position below length[b] counts as length[b].
+ *   scale        of the scores q.k, finite.
+ *   out          [B,T,heads,D] dense: sum_j p_j v_j, p = softmax(scale q.k)
+ *                over the visible tokens; zeros for a token that sees none.
+ *   lse          [B,T,heads] float32 or NULL: log(sum_j exp(scale q.k_j)),
+ *                -inf for a token that sees none.
+ *   workspace    dspark_tree_workspace_bytes(...) bytes, 256-byte aligned; its
+ *                contents need not be initialised.  Two calls in flight at
+ *                the same time must not share it.
+ * Scores, softmax statistics and sums are float32; bfloat16 inputs multiply
+ * weights rounded to bfloat16 (relative error 2^-9 each).  Keys and values of
+ * places that a token does not see never reach its result, whatever they
+ * hold.  A sequence whose length or pages are out of range is not computed
+ * (error 6 or 7; its rows are left as they are); a table entry that names no
+ * page reads as zeros (error 7).
+ * 1 <= T <= 64, group <= 32.  bfloat16 with head_dim 64 or 128 and a page size
+ * that is a power of two from 8 on runs on the tensor cores, everything else
+ * on the FFMA kernel.  Two launches, graph capturable, no synchronisation.
+ */
+DSPARK_API dspark_status dspark_tree_attention(
+    const dspark_cache* cache, int layer, const int32_t* seq,
+    const int32_t* length, const int32_t* token_count, const void* q,
+    const uint64_t* mask, int64_t mask_stride, const int32_t* position,
+    int window, float scale, int B, int T, int heads, void* out, float* lse,
+    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * dspark_noise_words -- diagnostic: writes the n raw Philox words the
  * sampler uses for elements 0..n-1 of (seed, offset, position k, stream),
