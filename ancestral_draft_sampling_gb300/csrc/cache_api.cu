@@ -28,7 +28,7 @@ dspark_status check_cache(const dspark_cache* c) {
   if (c->layers > 1024 || c->page_size > 4096 || c->kv_heads > 1024 ||
       c->head_dim > 256 || c->head_dim % 8 != 0 ||
       (long long)c->max_seqs * c->max_pages >= (1LL << 31) ||
-      (long long)c->max_pages * c->page_size >= (1LL << 31))
+      (long long)c->max_pages * c->page_size > (1LL << 30))
     return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
 }
@@ -227,7 +227,8 @@ dspark_status dspark_tree_attention(
   a.lse = lse;
   a.prefix = static_cast<long long*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.part);
-  cudaError_t e = launch_tree_ffma(a, sm_count(), stream);
+  cudaError_t e = tree_tc_supported(a) ? launch_tree_tc(a, sm_count(), stream)
+                                       : launch_tree_ffma(a, sm_count(), stream);
   if (e == cudaSuccess) e = launch_tree_merge(a, stream);
   return from_cuda(e);
 }

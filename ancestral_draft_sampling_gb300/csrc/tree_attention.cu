@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (lane < n) {
       const int c = cb + lane;
       const float* st = tree_part_stats(a, c == c0 ? slot0 : 2 * c) + 2 * r;
-      wt = st[0] == M ? 1.0f : expf(st[0] - M);  // parts that saw nothing: 0
+      wt = st[0] == M ? 1.0f : exp2f((st[0] - M) * a.stat_log2);  // saw nothing: 0
       if (M == -INFINITY) wt = 0.0f;
       lw = wt * st[1];
     }
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       put4(static_cast<T*>(a.out) + row * D + d,
            make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
   }
-  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M + logf(L);
+  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * a.stat_ln + logf(L);
 }
 
 // Dynamic shared memory a block may have beside its few static words.
@@ -322,6 +322,8 @@ cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
   a.row_tokens = kRows / a.group;
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
   a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
+  a.stat_log2 = 1.4426950408889634f;
+  a.stat_ln = 1.0f;
   const size_t smem = sizeof(float) * ((size_t)(kRows + kTile) * (D + 4) +
                                        (size_t)kTile * D + kWarps * kTile * 4);
   // two blocks a multiprocessor where shared memory allows it (D <= 128)

@@ -35,6 +35,7 @@ struct TreeArgs {
   int row_tokens;  // drafted tokens of a row tile
   int row_tiles;   // of T tokens
   int slot_rows;   // rows of a partial result
+  float stat_log2, stat_ln;  // a partial maximum's unit in log2 and in ln units
   long long* prefix;  // [B + 1] first tile of each sequence in the line
   float* part;        // [2 G][slot_rows][D] sums, then [2 G][slot_rows][2]
 };

@@ -1,0 +1,662 @@
+// tree_attention_tc.cu -- attention of drafted tokens over the paged cache on
+// the 5th-generation tensor cores (tcgen05), bfloat16, head_dim 64 or 128.
+//
+// For a unit's row tile of 128 rows (drafted tokens times query heads) and
+// each tile of 128 keys: S = Q K^T into tensor memory, weights
+// P = 2^(c S - m) (c = scale log2 e) from one thread for each row back into
+// tensor memory over S, O += P V.  m is the row's reference: the running
+// maximum, but raised only when a tile's maximum passes it by more than 8
+// (weights stay below 2^8, sums far inside float32), so O, which lives in
+// tensor memory for the whole unit, is seldom rescaled.  The sum l is taken of
+// the float32 weights; the product reads them rounded to bfloat16, which is
+// what the tensor cores multiply.
+//
+// Bound by HBM while rows * 4 flops for each key element stay below the
+// tensor cores' rate, that is up to about 285 rows a key head; the layout
+// follows from that: one block a multiprocessor, keys and values in a ring of
+// 32 KB (16 KB) tiles that TMA fills straight from the pages, 192 KB in
+// flight, which covers the latency of HBM several times over.
+//   warp 0      fills the ring: each lane copies one page's rows of one half
+//               of the head (64 values, 128-byte swizzle), and looks up its
+//               page of the next tile meanwhile.
+//   warp 1      one thread issues the products: S of tile n + 1 before O of
+//               tile n, so the softmax of a tile overlaps the next product.
+//   warp 2      loads a unit's queries (TMA, rows (token, head) of the key
+//               head), once the last unit's scores are done.
+//   warps 4..7  softmax: warp w holds rows 32 (w - 4) .. + 31.
+// Tiles that some rows see and others do not (the drafted tokens, a window's
+// edge, the sequence's end) may hold NaN or infinities in places that weigh
+// nothing, and 0 * NaN would reach every row.  Their values are looked
+// through first; entries that are not finite are added to the rows that see
+// them by hand and cleared.
+//
+// Every wait is bounded; where one runs out the kernel sets the error word,
+// waits (bounded) for its copies and products, frees its tensor memory and
+// returns.
+#include "dspark_common.cuh"
+#include "host_util.cuh"
+#include "sm100_ptx.cuh"
+#include "tree_attention.cuh"
+
+namespace dspark {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;             // keys of a tile
+constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 bfloat16
+constexpr uint32_t kSpin = 1u << 22;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kRaise = 8.0f;         // log2 units that a weight may exceed 1
+
+template <int D>
+struct Shape {
+  static constexpr int halves = D / 64;
+  static constexpr int tile_bytes = halves * kHalfBytes;
+  static constexpr int slots = D == 128 ? 6 : 12;
+  static constexpr uint32_t s_col(uint32_t i) { return 128 * i; }
+  static constexpr uint32_t o_col(uint32_t i) { return 256 + D * i; }
+};
+
+struct Control {  // shared memory behind the tiles
+  uint64_t kv_full[12], kv_empty[12];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done, o_free[2], v_sync, drain;
+  long long sums[34];
+  uint32_t bad[2][4];   // rows of a value tile that hold NaN or infinities
+  uint32_t add_first[2];  // the unit's first product adds to O
+  uint32_t tmem;
+  int failed;
+};
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)(1 + Shape<D>::slots) * Shape<D>::tile_bytes + sizeof(Control);
+}
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, kSpin);
+}
+
+// The same for a whole warp: either all its lanes go on or none does.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(bar, parity));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                       int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                       int x, int y, int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define R8(b) "=r"(r[b]), "=r"(r[b + 1]), "=r"(r[b + 2]), "=r"(r[b + 3]), "=r"(r[b + 4]), \
+              "=r"(r[b + 5]), "=r"(r[b + 6]), "=r"(r[b + 7])
+#define I8(b) "r"(r[b]), "r"(r[b + 1]), "r"(r[b + 2]), "r"(r[b + 3]), "r"(r[b + 4]), \
+              "r"(r[b + 5]), "r"(r[b + 6]), "r"(r[b + 7])
+
+// 32 lanes x 32 columns, one lane of tensor memory a thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : R8(0), R8(8), R8(16), R8(24)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::I8(0),
+      I8(8), I8(16), I8(24), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t at) {
+  uint32_t x;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ void tmem_st1(uint32_t at, uint32_t x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(x), "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Which of the keys j .. j + 31 a row sees: committed ones lo .. len - 1, and
+// drafted ones by their bits.
+__device__ __forceinline__ uint32_t seen32(int j, int lo, int len, uint64_t bits) {
+  const int a = lo - j, e = len - j;
+  const uint32_t below = e <= 0 ? 0u : e >= 32 ? ~0u : (1u << e) - 1;
+  const uint32_t under = a <= 0 ? 0u : a >= 32 ? ~0u : (1u << a) - 1;
+  uint32_t m = below & ~under;
+  if (e <= 0) {
+    if (e > -64) m |= (uint32_t)(bits >> -e);
+  } else if (e < 32) {
+    m |= (uint32_t)(bits << e);
+  }
+  return m;
+}
+
+struct TcArgs {
+  TreeArgs a;
+  int page_rows;  // rows of a copy: of one page, at most a tile
+  int pages;      // copies of half a tile
+  int q_tokens;   // drafted tokens of a query copy
+};
+
+// Position in the ring of tile n's keys and values, of N tiles: the order in
+// which the products use them (keys of tile n + 1 before values of tile n).
+__device__ __forceinline__ int k_at(int n) { return n == 0 ? 0 : 2 * n - 1; }
+__device__ __forceinline__ int v_at(int n, int N) { return n == N - 1 ? 2 * n + 1 : 2 * n + 2; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v) {
+  using S = Shape<D>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* q_tile = smem;
+  uint8_t* ring = smem + S::tile_bytes;
+  Control& sh = *reinterpret_cast<Control*>(ring + S::slots * S::tile_bytes);
+  const TreeArgs& a = P.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::slots; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], 4);
+      mbar_init(&sh.o_free[i], 4);
+      sh.add_first[i] = 0;
+    }
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.v_sync, 4);
+    mbar_init(&sh.drain, 1);
+    sh.failed = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 3) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  TreeWalk w = tree_start(a, sh.sums);  // synchronises the block
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int N = (int)(w.end - w.pos);  // tiles of this block
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------- keys and values
+    const int half = lane / P.pages, part = lane - half * P.pages;
+    const bool mine = half < S::halves;
+    int at = 0;                 // entries of the ring filled so far
+    struct Where { int h, id, y; } cur{0, 0, 0}, prev{0, 0, 0};
+    // the lane's page of the tile that starts with key j
+    auto look_up = [&](int j) {
+      j += part * P.page_rows;
+      Where t{w.h, a.c.num_pages, j % a.c.page_size};
+      if (mine && j < w.q.len + w.q.cnt) {
+        const int id = cache_page(a.c, w.q.s, j / a.c.page_size, a.c.max_pages);
+        if (id >= 0) t.id = id;
+        else cache_error(a.c, kCacheErrPage);
+      }
+      return t;  // no page: a place behind the pool, which reads as zeros
+    };
+    auto fill = [&](const CUtensorMap* map, const Where& t) {
+      const int s = at % S::slots;
+      if (at >= S::slots) ok = wait_warp(&sh.kv_empty[s], ((at / S::slots) - 1) & 1);
+      if (!ok) return;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[s], S::tile_bytes);
+      __syncwarp();
+      if (mine)
+        tma_4d(ring + s * S::tile_bytes + half * kHalfBytes + part * P.page_rows * 128, map,
+               &sh.kv_full[s], half * 64, t.y, t.h, t.id);
+      ++at;
+    };
+    bool some = w.next(a);
+    int i = 0;
+    Where ahead{0, 0, 0};
+    if (some) ahead = look_up((w.q.lo + w.first) * kTile);
+    for (int n = 0; n < N && ok; ++n) {
+      prev = cur;
+      cur = ahead;
+      // the next tile's page, before this tile's copies wait for room
+      if (++i >= w.n) {
+        i = 0;
+        some = w.next(a);
+      }
+      if (some) ahead = look_up((w.q.lo + w.first + i) * kTile);
+      fill(&map_k, cur);
+      if (n > 0 && ok) fill(&map_v, prev);
+    }
+    if (N > 0 && ok) fill(&map_v, cur);
+    if (!ok) {  // copies that nobody waited for land before the block ends
+      for (int e = at > S::slots ? at - S::slots : 0; e < at; ++e)
+        mbar_wait(&sh.kv_full[e % S::slots], (e / S::slots) & 1, kSpin >> 4);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+      const uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
+      const uint32_t q_base = smem_u32(q_tile), ring_base = smem_u32(ring);
+      int unit = -1, left = 0;       // of tile n
+      int o_unit = 0;                // of tile n - 1
+      bool o_first = false, first = false;
+      for (int n = 0; n <= N && ok; ++n) {
+        const int before = unit;
+        const bool before_first = first;
+        if (n < N) {
+          first = left == 0;
+          if (first) {
+            w.next(a);
+            left = w.n;
+            ++unit;
+            ok = wait(&sh.q_full, unit & 1);
+          }
+          --left;
+          const int e = k_at(n), s = e % S::slots;
+          ok = ok && wait(&sh.kv_full[s], (e / S::slots) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_base = ring_base + s * S::tile_bytes;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
+            mma_bf16(tmem + S::s_col(n & 1), smem_desc_sw128(q_base + off, 16, 1024),
+                     smem_desc_sw128(k_base + off, 16, 1024), idesc_s, k != 0);
+          }
+          mma_commit(&sh.s_full[n & 1]);
+          mma_commit(&sh.kv_empty[s]);
+          if (left == 0) mma_commit(&sh.q_empty);
+        }
+        if (n > 0) {
+          const int m = n - 1, e = v_at(m, N), s = e % S::slots;
+          o_unit = before;
+          o_first = before_first;
+          if (o_first) ok = wait(&sh.o_free[o_unit & 1], ((o_unit >> 1) & 1) ^ 1);
+          ok = ok && wait(&sh.kv_full[s], (e / S::slots) & 1);
+          ok = ok && wait(&sh.p_ready[m & 1], (m >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const bool add = !o_first || *(volatile uint32_t*)&sh.add_first[m & 1];
+          const uint32_t v_base = ring_base + s * S::tile_bytes;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_bf16_ta(tmem + S::o_col(o_unit & 1), tmem + S::s_col(m & 1) + 8 * k,
+                        smem_desc_sw128(v_base + k * 2048, kHalfBytes, 1024), idesc_o,
+                        add || k != 0);
+          mma_commit(&sh.pv_done);
+          mma_commit(&sh.kv_empty[s]);
+        }
+      }
+      if (!ok) {
+        mma_commit(&sh.drain);
+        mbar_wait(&sh.drain, 0, kSpin >> 4);
+      }
+    }
+  } else if (warp == 2) {
+    // --------------------------------------------------------- queries
+    if (lane == 0) {
+      const uint32_t bytes = S::halves * P.q_tokens * a.group * 128;
+      int unit = 0;
+      for (; ok && w.next(a); ++unit) {
+        if (unit > 0) ok = wait(&sh.q_empty, (unit - 1) & 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&sh.q_full, bytes);
+        for (int i = 0; i < S::halves; ++i)
+          tma_5d(q_tile + i * kHalfBytes, &map_q, &sh.q_full, i * 64, 0, w.h,
+                 w.rt * a.row_tokens, w.b);
+      }
+      if (!ok && unit > 0) mbar_wait(&sh.q_full, (unit - 1) & 1, kSpin >> 4);
+    }
+  } else if (warp >= 4) {
+    // --------------------------------------------------------- softmax
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float c = a.scale * kLog2e;
+    int n = 0, unit = 0, syncs = 0;
+    bool is_first = true;  // the block's first unit
+    for (; ok && w.next(a); ++unit) {
+      const int t0 = w.rt * a.row_tokens;
+      const int tokens = w.q.cnt - t0 < a.row_tokens ? w.q.cnt - t0 : a.row_tokens;
+      const int rows = tokens * a.group;
+      const int t = t0 + r / a.group;
+      const bool valid = r < rows, any = quarter * 32 < rows;
+      const uint64_t bits = valid ? tree_mask(a, w.b, t, w.q.cnt) : 0;
+      const int len = w.q.len;
+      int lo = valid ? tree_window_lo(a, w.b, t, len) : 0;
+      int lo_most = 0;  // committed keys below this are hidden from some row
+      if (a.window > 0) {
+        for (int i = lane; i < tokens; i += 32) {
+          const int x = tree_window_lo(a, w.b, t0 + i, len);
+          lo_most = x > lo_most ? x : lo_most;
+        }
+        lo_most = __reduce_max_sync(0xffffffffu, lo_most);
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int tile = 0; tile < w.n && ok; ++tile, ++n) {
+        const int j0 = (w.q.lo + w.first + tile) * kTile;
+        const bool masked = j0 + kTile > len || j0 < lo_most;
+        const uint32_t s_at = lanes + S::s_col(n & 1), o_at = lanes + S::o_col(unit & 1);
+        ok = wait_warp(&sh.s_full[n & 1], (n >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        if (any) {
+          float x[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x) + 32 * i);
+          tmem_ld_wait();
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) see[i] = seen32(j0 + 32 * i, lo, len, bits);
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) {
+              x[i] *= c;
+              if ((see[i / 32] >> (i % 32)) & 1) top[i & 3] = fmaxf(top[i & 3], x[i]);
+              else x[i] = -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) {
+              x[i] *= c;
+              top[i & 3] = fmaxf(top[i & 3], x[i]);
+            }
+          }
+          const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          const bool raise = valid && best > m + kRaise;  // m = -inf: any maximum
+          if (__any_sync(0xffffffffu, raise)) {
+            const float now = raise ? best : m;
+            const float f = raise ? ex2(m - now) : 1.0f;
+            if (tile > 0) {
+              ok = wait_warp(&sh.pv_done, (n - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+                uint32_t o[32];
+                tmem_ld32(o_at + 32 * i, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(o_at + 32 * i, o);
+              }
+            }
+            l *= f;
+            m = now;
+          }
+          const float base = m == -INFINITY ? 0.0f : m;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t p[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const int e = 64 * i + 2 * k;
+              const float p0 = ex2(x[e] - base), p1 = ex2(x[e + 1] - base);
+              sum[(2 * k) & 3] += p0;
+              sum[(2 * k + 1) & 3] += p1;
+              p[k] = pack_bf16(p0, p1);
+            }
+            tmem_st32(s_at + 32 * i, p);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        uint32_t found = 0;
+        if (masked) {
+          // the tile's values: this thread looks through key j0 + r's
+          const int e = v_at(n, N), slot = e % S::slots;
+          uint8_t* v = ring + slot * S::tile_bytes;
+          ok = wait_warp(&sh.kv_full[slot], (e / S::slots) & 1);
+          if (!ok) break;
+          uint32_t worst = 0;
+#pragma unroll
+          for (int i = 0; i < S::halves * 8; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(
+                v + (i >> 3) * kHalfBytes + r * 128 + (((i & 7) ^ (r & 7)) << 4));
+            const uint32_t k[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {  // an exponent of ones carries past it
+              worst |= (k[d] & 0x7f807f80u) + 0x00800080u;
+            }
+          }
+          const uint32_t b = __ballot_sync(0xffffffffu, (worst & 0x80008000u) != 0);
+          if (lane == 0) {
+            sh.bad[n & 1][quarter] = b;
+            mbar_arrive(&sh.v_sync);
+          }
+          ok = wait_warp(&sh.v_sync, syncs++ & 1);
+          if (!ok) break;
+          uint32_t rows_bad[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            rows_bad[i] = *(volatile uint32_t*)&sh.bad[n & 1][i];
+            found |= rows_bad[i];
+          }
+          if (found) {
+            if (any) {
+              if (tile > 0) {
+                ok = wait_warp(&sh.pv_done, (n - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+              } else {  // O starts from what is added here
+                for (int d = 0; d < D; ++d) tmem_st1(o_at + d, 0);
+                tmem_st_wait();
+              }
+              for (int j = 0; j < kTile; ++j) {
+                if (!((rows_bad[j >> 5] >> (j & 31)) & 1)) continue;
+                const uint32_t pp = tmem_ld1(s_at + (j >> 1));
+                tmem_ld_wait();
+                const float p = __uint_as_float(j & 1 ? pp & 0xffff0000u : pp << 16);
+                const uint32_t word = j < 64 ? (j < 32 ? see[0] : see[1]) : (j < 96 ? see[2] : see[3]);
+                const bool sees = (word >> (j & 31)) & 1;
+                for (int d = 0; d < D; ++d) {
+                  const uint16_t u = *reinterpret_cast<const uint16_t*>(
+                      v + (d >> 6) * kHalfBytes + j * 128 + ((((d & 63) >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
+                  if ((u & 0x7f80u) != 0x7f80u) continue;
+                  const float o = __uint_as_float(tmem_ld1(o_at + d));
+                  tmem_ld_wait();
+                  tmem_st1(o_at + d, __float_as_uint(sees ? fmaf(p, bf16_bits_to_float(u), o) : o));
+                  tmem_st_wait();
+                }
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.v_sync);
+            ok = wait_warp(&sh.v_sync, syncs++ & 1);
+            if (!ok) break;
+            if ((rows_bad[quarter] >> lane) & 1) {
+              for (int d = 0; d < D; ++d) {
+                uint16_t* u = reinterpret_cast<uint16_t*>(
+                    v + (d >> 6) * kHalfBytes + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2);
+                if ((*u & 0x7f80u) == 0x7f80u) *u = 0;
+              }
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        if (threadIdx.x == 128) *(volatile uint32_t*)&sh.add_first[n & 1] = found != 0;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[n & 1]);
+      }
+      if (!ok) break;
+      // the unit's rows
+      ok = wait_warp(&sh.pv_done, (n - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
+      is_first = false;
+      if (any) {
+        const uint32_t o_at = lanes + S::o_col(unit & 1);
+        const size_t row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r % a.group;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(o_at + 32 * i, o);
+          tmem_ld_wait();
+          if (valid && w.whole) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t p[4];
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+                p[d] = pack_bf16(__uint_as_float(o[8 * k + 2 * d]) * inv,
+                                 __uint_as_float(o[8 * k + 2 * d + 1]) * inv);
+              to[k] = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          } else if (valid) {
+            uint4* to = reinterpret_cast<uint4*>(tree_part(a, slot) + (size_t)r * D + 32 * i);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        if (valid) {
+          if (!w.whole) {
+            float* st = tree_part_stats(a, slot) + 2 * r;
+            st[0] = m;
+            st[1] = l;
+          } else if (a.lse) {
+            a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.o_free[unit & 1]);
+    }
+  }
+  if (!ok) sh.failed = 1;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && sh.failed) cache_error(a.c, kDevErrTimeout);
+}
+
+bool is_power_of_two(int x) { return (x & (x - 1)) == 0; }
+
+template <int D>
+cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [] {
+    cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)smem_bytes<D>());
+  });
+  const auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  TcArgs P{};
+  P.a = a;
+  P.page_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
+  P.pages = kTile / P.page_rows;
+  P.q_tokens = a.T < a.row_tokens ? a.T : a.row_tokens;
+  CUtensorMap mq, mk, mv;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  {
+    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.c.kv_heads,
+                                (cuuint64_t)a.T, (cuuint64_t)a.B};
+    const cuuint64_t row = (cuuint64_t)D * 2;
+    const cuuint64_t strides[4] = {row, row * a.group, row * a.heads, row * a.heads * a.T};
+    const cuuint32_t box[5] = {64, (cuuint32_t)a.group, 1, (cuuint32_t)P.q_tokens, 1};
+    if (encode(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(a.q), dims, strides,
+               box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  for (int i = 0; i < 2; ++i) {
+    char* base = static_cast<char*>(a.c.pool) + cache_row(a.c, 2 * a.layer + i, 0, 0, 0);
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.c.page_size,
+                                (cuuint64_t)a.c.kv_heads, (cuuint64_t)a.c.num_pages};
+    const cuuint64_t row = (cuuint64_t)D * 2;
+    const cuuint64_t strides[3] = {row, row * a.c.page_size, row * a.c.page_size * a.c.kv_heads};
+    const cuuint32_t box[4] = {64, (cuuint32_t)P.page_rows, 1, 1};
+    if (encode(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  tree_tc_kernel<D><<<a.blocks, kThreads, smem_bytes<D>(), stream>>>(P, mq, mk, mv);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tree_tc_supported(const TreeArgs& a) {
+  return a.c.dtype == DSPARK_BF16 && (a.c.head_dim == 64 || a.c.head_dim == 128) &&
+         a.c.page_size >= 8 && is_power_of_two(a.c.page_size);
+}
+
+cudaError_t launch_tree_tc(TreeArgs& a, int sms, cudaStream_t stream) {
+  a.tile = kTile;
+  a.row_tokens = kTreeRows / a.group;
+  a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
+  a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
+  a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
+  a.stat_log2 = 1.0f;
+  a.stat_ln = kLn2;
+  return a.c.head_dim == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace dspark

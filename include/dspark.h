@@ -424,7 +424,7 @@ DSPARK_API dspark_status dspark_sample_temperature(
  * names the sequences, each at most once in a call.
  * Limits: 1 <= layers <= 1024, page_size <= 4096, head_dim a multiple of 8
  * up to 256, kv_heads <= 1024, max_seqs * max_pages < 2^31, num_pages < 2^31,
- * max_pages * page_size < 2^31, B <= 1024.  The pool is addressed in 64 bits.
+ * max_pages * page_size <= 2^30, B <= 1024.  The pool is addressed in 64 bits.
  *
  * Sequences, pages, positions and paths that are out of range are seen on
  * the device: the entry is skipped as its call says and the error word is
