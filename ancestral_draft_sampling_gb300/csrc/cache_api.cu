@@ -43,17 +43,17 @@ dspark_status check_heads(int heads, int kv_heads) {
   return DSPARK_OK;
 }
 
-// The workspace of the attention: the first tile of each sequence, then the
-// partial results.  The tensor-core tile's rows bound the FFMA kernel's two
-// blocks of 32 rows a multiprocessor, too.
+// The workspace of the attention: what the merge has to do, then the partial
+// results.  The FFMA kernel runs two blocks of 32 rows a
+// multiprocessor.
 struct TreeLayout {
   size_t part, total;
 };
 
-TreeLayout tree_layout(int B, int T, int group, int D) {
+TreeLayout tree_layout(int T, int group, int D) {
   TreeLayout L;
-  L.part = align_up((size_t)(B + 1) * sizeof(long long), 256);
-  const int fit = kTreeRows / group;  // drafted tokens of a tensor-core tile
+  L.part = align_up((size_t)2 * kTreeMaxBlocks * sizeof(TreeJoin), 256);
+  const int fit = 2 * (kTreeRows / group);  // drafted tokens of a tensor-core unit
   size_t rows = (size_t)(T < fit ? T : fit) * group * 2 * kTreeMaxBlocks;
   const int fit32 = 32 / group;
   const size_t rows32 = (size_t)(T < fit32 ? T : fit32) * group * 4 * kTreeMaxBlocks;
@@ -182,7 +182,7 @@ dspark_status dspark_cache_append(
 
 size_t dspark_tree_workspace_bytes(int B, int T, int heads, int kv_heads, int head_dim) {
   if (!tree_sizes(B, T, heads, kv_heads, head_dim)) return 0;
-  return tree_layout(B, T, heads / kv_heads, head_dim).total;
+  return tree_layout(T, heads / kv_heads, head_dim).total;
 }
 
 dspark_status dspark_tree_attention(
@@ -204,7 +204,7 @@ dspark_status dspark_tree_attention(
     if (!is4(p)) return DSPARK_ERR_INVALID_ARG;
   if (!tree_sizes(B, T, heads, cache->kv_heads, cache->head_dim)) return DSPARK_ERR_UNSUPPORTED;
   const int group = heads / cache->kv_heads;
-  const TreeLayout L = tree_layout(B, T, group, cache->head_dim);
+  const TreeLayout L = tree_layout(T, group, cache->head_dim);
   if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
     return DSPARK_ERR_WORKSPACE;
   TreeArgs a{};
@@ -225,7 +225,7 @@ dspark_status dspark_tree_attention(
   a.q = q;
   a.out = out;
   a.lse = lse;
-  a.prefix = static_cast<long long*>(workspace);
+  a.join = static_cast<TreeJoin*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.part);
   cudaError_t e = tree_tc_supported(a) ? launch_tree_tc(a, sm_count(), stream)
                                        : launch_tree_ffma(a, sm_count(), stream);

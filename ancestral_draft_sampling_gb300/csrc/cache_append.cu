@@ -12,9 +12,9 @@
 // group, and the other half of a pair sits in the lane rot_dim / 2 values
 // away (or in the same lane, for neighbouring pairs).  A warp stays on one
 // token and loads kPer times before it stores, so the rotation's cosines are
-// loaded once for all its heads.  Rows that do not split that way (head_dim
-// not 16 bytes times a power of two up to 32 lanes, or halves that end inside
-// a lane's words) take the row kernel: a warp for each row, through shared
+// loaded once for all its heads.  Rows that do not split that way (other head
+// dims than 8, 16 or 32 lanes hold, rotations that end inside a lane's words,
+// unaligned tables) take the row kernel: a warp for each row, through shared
 // memory.
 #include "cache.cuh"
 #include "host_util.cuh"
@@ -129,27 +129,52 @@ __device__ __forceinline__ Row find_row(const AppendArgs& a, const Token& k, int
   return r;
 }
 
-template <typename T, int kPer>
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(AppendArgs a, int lanes, int splits) {
-  constexpr int N = Word<T>::n;
+// n floats from p, 16 (n a multiple of 4) or 8 bytes at a time.
+template <int n>
+__device__ __forceinline__ void load_floats(const float* p, float* x) {
+  if (n % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < n / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(p)[i];
+      x[4 * i] = v.x;
+      x[4 * i + 1] = v.y;
+      x[4 * i + 2] = v.z;
+      x[4 * i + 3] = v.w;
+    }
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+  }
+}
+
+// kLanes lanes hold a row, kPer loads a warp.  The table and the weights are
+// read 16 bytes at a time (one value at a time the loads of angles and
+// weights, not HBM, bound the pass: 119 us for two prompts of 13k tokens).
+template <typename T, int kLanes, int kPer, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int splits) {
+  constexpr int N = Word<T>::n, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31;
   const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int token = w / splits, split = w - token * splits;
   if (token >= a.B * a.T) return;
   const Token k = find_token(a, token, lane == 0 && split == 0);
   if (!k.there) return;
-  const int sub = lane & (lanes - 1), per_warp = 32 / lanes;
+  const int sub = lane & (kLanes - 1);
   const int d0 = sub * N, half = a.rot >> 1;
-  const int h0 = split * kPer * per_warp + lane / lanes;
-
+  const int h0 = split * kPer * kRows + lane / kLanes;
+  const int Hq = a.heads, Hk = a.c.kv_heads;
+  constexpr int elt = sizeof(T), row = kLanes * 16;
+  const char* q = a.q + (size_t)token * a.q_stride * elt + 16 * sub;
+  const char* kk = a.k + (size_t)token * a.k_stride * elt + 16 * sub;
+  const char* v = a.v + (size_t)token * a.v_stride * elt + 16 * sub;
   uint4 word[kPer];
-  Row row[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    row[i] = find_row(a, k, h0 + i * per_warp);
+    const int h = h0 + i * kRows;
+    const char* src = h < Hq ? q + h * row : h < Hq + Hk ? kk + (h - Hq) * row : v + (h - Hq - Hk) * row;
     word[i] = make_uint4(0, 0, 0, 0);
-    if (row[i].src) word[i] = *reinterpret_cast<const uint4*>(row[i].src + 16 * sub);
+    if (h < Hq + 2 * Hk) word[i] = *reinterpret_cast<const uint4*>(src);
   }
   // the angle of each of the lane's values; the sine carries the sign
   float cs[N], sn[N];
@@ -159,60 +184,73 @@ __global__ void __launch_bounds__(kThreads)
     cs[e] = 1.0f;
     sn[e] = 0.0f;
   }
-  if (k.position >= 0) {
+  const bool turn = k.position >= 0 && d0 < a.rot;  // all the lane's values or none
+  if (turn) {
     const float* table = a.cos_sin + (size_t)k.position * a.rot;
-    if (!a.interleaved && d0 < a.rot) {
-      const bool low = d0 < half;  // half is a multiple of N: all N or none
+    if (!kInterleaved) {
+      const bool low = d0 < half;
       partner = low ? lane + half / N : lane - half / N;
+      load_floats<N>(table + (low ? d0 : d0 - half), cs);
+      load_floats<N>(table + (low ? d0 + half : d0), sn);
+      if (low)
+#pragma unroll
+        for (int e = 0; e < N; ++e) sn[e] = -sn[e];
+    } else {
+      float c2[N / 2], s2[N / 2];
+      load_floats<N / 2>(table + (d0 >> 1), c2);
+      load_floats<N / 2>(table + half + (d0 >> 1), s2);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int i = low ? d0 + e : d0 + e - half;
-        cs[e] = table[i];
-        sn[e] = low ? -table[half + i] : table[half + i];
+        cs[e] = c2[e >> 1];
+        sn[e] = e & 1 ? s2[e >> 1] : -s2[e >> 1];
       }
-    } else if (a.interleaved) {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (d0 + e < a.rot) {
-          const int i = (d0 + e) >> 1;
-          cs[e] = table[i];
-          sn[e] = e & 1 ? table[half + i] : -table[half + i];
-        }
     }
   }
+  const bool norm = a.q_weight || a.k_weight;
+  float wq[N], wk[N];
+  if (a.q_weight) load_floats<N>(a.q_weight + d0, wq);
+  if (a.k_weight) load_floats<N>(a.k_weight + d0, wk);
+  char* q_out = a.q_out + (size_t)token * Hq * row + 16 * sub;
+  const size_t step = (size_t)a.c.page_size * row;  // between a page's heads
+  char* k_out = static_cast<char*>(a.c.pool) +
+                cache_row(a.c, 2 * a.layer, k.page < 0 ? 0 : k.page, 0, k.slot) + 16 * sub;
+  char* v_out = k_out + cache_row(a.c, 1, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    float x[N];
+    const int h = h0 + i * kRows;
+    const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hk;
+    float x[N], y[N];
     Word<T>::load(word[i], x);
-    if (a.q_weight || a.k_weight) {  // the butterfly is the whole warp's
+    if (norm) {  // the butterfly is the whole warp's
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < N; ++e) sum = fmaf(x[e], x[e], sum);
-      for (int m = lanes >> 1; m > 0; m >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      if (row[i].weight) {
-        const float r = rsqrtf(sum / (float)a.c.head_dim + a.eps);
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = x[e] * r * row[i].weight[d0 + e];
+      for (int m = kLanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      const float r = rsqrtf(sum * (1.0f / (kLanes * N)) + a.eps);
+      if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
       }
     }
-    float y[N];
-    if (a.interleaved) {
+    if (kInterleaved) {
 #pragma unroll
       for (int e = 0; e < N; ++e) y[e] = x[e ^ 1];
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
     }
-    if (!row[i].dst) continue;
-    if (row[i].rotate) {
-      // a value that is not turned keeps its bits (0 * infinity is no 0)
+    // a value that is not turned keeps its bits (0 * infinity is no 0)
+    if (turn) {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (k.position >= 0 && d0 + e < a.rot) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
-      word[i] = Word<T>::store(x);
+      for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
     }
-    *reinterpret_cast<uint4*>(row[i].dst + 16 * sub) = word[i];
+    if (is_q) {
+      *reinterpret_cast<uint4*>(q_out + h * row) = Word<T>::store(x);
+    } else if (k.page >= 0) {
+      if (is_k) *reinterpret_cast<uint4*>(k_out + (h - Hq) * step) = Word<T>::store(x);
+      else if (h < Hq + 2 * Hk) *reinterpret_cast<uint4*>(v_out + (h - Hq - Hk) * step) = word[i];
+    }
   }
 }
 
@@ -263,32 +301,43 @@ __global__ void __launch_bounds__(kThreads) append_row_kernel(AppendArgs a) {
   }
 }
 
-template <typename T>
-cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
-  constexpr int N = Word<T>::n;
-  const int D = a.c.head_dim, lanes = D / N;
+template <typename T, int kLanes>
+cudaError_t launch_lanes(const AppendArgs& a, cudaStream_t stream) {
   const int rows = a.heads + 2 * a.c.kv_heads;
   const long long tokens = (long long)a.B * a.T;
-  const bool whole = D % N == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0 &&
-                     (a.interleaved || (a.rot >> 1) % N == 0);
-  if (!whole) {
-    const long long blocks = (tokens * rows + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    append_row_kernel<T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
-  }
   // rows of a warp's load, and loads of a token
-  const int per_warp = 32 / lanes, loads = (rows + per_warp - 1) / per_warp;
+  const int per_warp = 32 / kLanes, loads = (rows + per_warp - 1) / per_warp;
   // four loads a warp where that still leaves every multiprocessor 16 warps,
   // else one: fewer tokens than that are bound by latency
   const bool many = tokens * loads / 4 >= 16LL * sm_count();
   const int splits = many ? (loads + 3) / 4 : loads;
-  const long long blocks = (tokens * splits + kThreads / 32 - 1) / (kThreads / 32);
   if (tokens * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (many)
-    append_kernel<T, 4><<<(unsigned)blocks, kThreads, 0, stream>>>(a, lanes, splits);
+  const unsigned blocks = (unsigned)((tokens * splits + kThreads / 32 - 1) / (kThreads / 32));
+  if (many && a.interleaved)
+    append_kernel<T, kLanes, 4, true><<<blocks, kThreads, 0, stream>>>(a, splits);
+  else if (many)
+    append_kernel<T, kLanes, 4, false><<<blocks, kThreads, 0, stream>>>(a, splits);
+  else if (a.interleaved)
+    append_kernel<T, kLanes, 1, true><<<blocks, kThreads, 0, stream>>>(a, splits);
   else
-    append_kernel<T, 1><<<(unsigned)blocks, kThreads, 0, stream>>>(a, lanes, splits);
+    append_kernel<T, kLanes, 1, false><<<blocks, kThreads, 0, stream>>>(a, splits);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
+  constexpr int N = Word<T>::n;
+  // a lane's values turn together and read whole words of the table
+  const bool whole =
+      (a.interleaved ? a.rot % N == 0 && (a.rot >> 1) % (N / 2) == 0 : (a.rot >> 1) % N == 0) &&
+      aligned_to(a.cos_sin, 16) && aligned_to(a.q_weight, 16) && aligned_to(a.k_weight, 16);
+  if (whole && a.c.head_dim == 8 * N) return launch_lanes<T, 8>(a, stream);
+  if (whole && a.c.head_dim == 16 * N) return launch_lanes<T, 16>(a, stream);
+  if (whole && a.c.head_dim == 32 * N) return launch_lanes<T, 32>(a, stream);
+  const long long blocks =
+      ((long long)a.B * a.T * (a.heads + 2 * a.c.kv_heads) + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  append_row_kernel<T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -286,10 +286,11 @@ __global__ void __launch_bounds__(kBlock, 1)
   }
 }
 
-// Fork, the copy: block (x, b) copies its share of the 16-byte words of the
-// filled rows of every plane and head.  Bound by HBM: the rows are read once
-// for each child, from L2 when several children share a parent.
-constexpr int kCopyThreads = 256, kCopyBatch = 4;
+// Fork, the copy: a warp for each (plane, head) of child b copies the filled
+// rows, which are contiguous there, eight 16-byte words a lane in flight.
+// Bound by HBM: each child's rows are written once; they are read from L2 when
+// several children share a parent.
+constexpr int kCopyThreads = 256, kCopyBatch = 8;
 
 __global__ void __launch_bounds__(kCopyThreads)
     fork_copy_kernel(dspark_cache c, const int32_t* length) {
@@ -298,29 +299,23 @@ __global__ void __launch_bounds__(kCopyThreads)
   const int from = __ldcg(&c.control[kCtlScratch + 2 * b]);
   const int to = __ldcg(&c.control[kCtlScratch + 2 * b + 1]);
   if (to < 0) return;
-  const int rows = length[b] % c.page_size;
-  const int words = c.head_dim * dtype_bytes(c.dtype) / 16;
-  const unsigned per_head = (unsigned)rows * words;
-  const unsigned items = 2u * c.layers * c.kv_heads;  // (plane, head)
-  const uint64_t total = (uint64_t)items * per_head;
-  const uint64_t step = (uint64_t)gridDim.x * kCopyThreads;
+  const int words = length[b] % c.page_size * (c.head_dim * dtype_bytes(c.dtype) / 16);
+  const int lane = threadIdx.x & 31, items = 2 * c.layers * c.kv_heads;
   char* pool = static_cast<char*>(c.pool);
-  for (uint64_t i = (uint64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < total;
-       i += kCopyBatch * step) {
-    uint4 v[kCopyBatch];
-    size_t dst[kCopyBatch];
+  for (int item = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); item < items;
+       item += gridDim.x * (kCopyThreads / 32)) {
+    const int plane = item / c.kv_heads, head = item - plane * c.kv_heads;
+    const uint4* src = reinterpret_cast<const uint4*>(pool + cache_row(c, plane, from, head, 0));
+    uint4* dst = reinterpret_cast<uint4*>(pool + cache_row(c, plane, to, head, 0));
+    for (int i = lane; i < words; i += 32 * kCopyBatch) {
+      uint4 v[kCopyBatch];
 #pragma unroll
-    for (int k = 0; k < kCopyBatch; ++k) {
-      const uint64_t j = i + k * step;
-      if (j >= total) break;
-      const unsigned item = (unsigned)(j / per_head), w = (unsigned)(j % per_head);
-      const int plane = item / c.kv_heads, head = item % c.kv_heads;
-      v[k] = *reinterpret_cast<const uint4*>(pool + cache_row(c, plane, from, head, 0) + 16 * (size_t)w);
-      dst[k] = cache_row(c, plane, to, head, 0) + 16 * (size_t)w;
+      for (int k = 0; k < kCopyBatch; ++k)
+        if (i + 32 * k < words) v[k] = src[i + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kCopyBatch; ++k)
+        if (i + 32 * k < words) dst[i + 32 * k] = v[k];
     }
-#pragma unroll
-    for (int k = 0; k < kCopyBatch; ++k)
-      if (i + k * step < total) *reinterpret_cast<uint4*>(pool + dst[k]) = v[k];
   }
 }
 
@@ -458,12 +453,10 @@ cudaError_t launch_cache_fork(const dspark_cache& c, const int32_t* parent,
   fork_kernel<<<1, kBlock, 0, stream>>>(c, parent, child, length, B);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // blocks for a full page's rows: what is not filled ends at once
-  const size_t words = cache_row(c, 0, 0, 1, 0) / 16 * 2 * c.layers * c.kv_heads;
-  const size_t each = (words + (size_t)kCopyThreads * kCopyBatch - 1) /
-                      ((size_t)kCopyThreads * kCopyBatch);
+  const int items = 2 * c.layers * c.kv_heads;
+  const int blocks = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(each < 1024 ? each : 1024), B);
+  cfg.gridDim = dim3(blocks, B);
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
   float* pw = ps + warp * kTile * 4;
   sm100::launch_dependents();
   TreeWalk w = tree_start(a, sums);
+  if (threadIdx.x == kThreads - 1) tree_describe(a, w);
   bool is_first = true;
   while (w.next(a)) {
     const int t0 = w.rt * a.row_tokens;
@@ -230,24 +231,11 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   sm100::grid_dependency_wait();
-  const int unit = blockIdx.x;
-  const int rt = unit % a.row_tiles, bh = unit / a.row_tiles;
-  const int h = bh % a.c.kv_heads, b = bh / a.c.kv_heads;
-  const long long W = a.prefix[a.B], base = a.prefix[b];
-  if (a.prefix[b + 1] == base) return;
-  const TreeSeq q = tree_seq(a, b, false);
-  if (rt >= q.row_tiles) return;
-  const int G = W < a.blocks ? (int)W : a.blocks;
-  const long long us = base + (long long)(h * q.row_tiles + rt) * q.tiles;
-  const int c0 = tree_block_of(W, G, us), c1 = tree_block_of(W, G, us + q.tiles - 1);
-  if (c0 == c1) return;
-  const int t0 = rt * a.row_tokens;
-  const int rows = (q.cnt - t0 < a.row_tokens ? q.cnt - t0 : a.row_tokens) * a.group;
+  const TreeJoin j = a.join[blockIdx.x + 1];  // nothing cuts the line's start
   const int lane = threadIdx.x & 31, D = a.c.head_dim;
   const int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  // block c0's part is its first unit only if the block starts with it
-  const int slot0 = 2 * c0 + (tree_first(W, G, c0) >= us ? 0 : 1);
+  if (r >= j.rows) return;
+  const int c0 = j.first, c1 = j.last, slot0 = j.slot;
   float M = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32)
     M = fmaxf(M, tree_part_stats(a, c == c0 ? slot0 : 2 * c)[2 * r]);
@@ -283,7 +271,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       }
     }
   }
-  const size_t row = ((size_t)b * a.T + t0 + r / a.group) * a.heads + h * a.group + r % a.group;
+  const size_t row =
+      ((size_t)j.b * a.T + j.t0 + r / a.group) * a.heads + j.h * a.group + r % a.group;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -337,10 +326,9 @@ cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
 }
 
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream) {
-  const int rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
+  if (a.blocks < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.c.kv_heads * a.row_tiles),
-                     (rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.gridDim = dim3(a.blocks - 1, (a.slot_rows + kMergeWarps - 1) / kMergeWarps);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};

@@ -10,12 +10,24 @@
 // whose tiles lie in one block is finished there; the others leave partial
 // results (unnormalised sums, the maximum and the sum of each row), at most
 // two a block (its first and its last unit), which the merge kernel joins in
-// the blocks' order, so results do not depend on timing.
+// the blocks' order, so results do not depend on timing.  Only G - 1 places of
+// the line can lie inside a unit, so block c of the merge looks after the unit
+// that the start of share c cuts first, which block c describes to it (a merge
+// block for each unit, each finding its own parts, took 45 us of 150 for 256
+// units of 128 rows).
 #pragma once
 
 #include "cache.cuh"
 
 namespace dspark {
+
+// Partial results to join: those of blocks first .. last (first's in `slot`,
+// the others' in their slot 0) of drafted tokens t0 .. t0 + rows / group - 1.
+// rows = 0: nothing.
+struct TreeJoin {
+  int b, h, t0, rows;
+  int first, last, slot, unused;
+};
 
 struct TreeArgs {
   dspark_cache c;
@@ -36,7 +48,7 @@ struct TreeArgs {
   int row_tiles;   // of T tokens
   int slot_rows;   // rows of a partial result
   float stat_log2, stat_ln;  // a partial maximum's unit in log2 and in ln units
-  long long* prefix;  // [B + 1] first tile of each sequence in the line
+  struct TreeJoin* join;  // [G] what block c of the merge has to do
   float* part;        // [2 G][slot_rows][D] sums, then [2 G][slot_rows][2]
 };
 
@@ -114,6 +126,7 @@ struct TreeWalk {
   int first, n;        // its tiles here: first .. first + n - 1, counted from
                        // the unit's own first tile
   bool whole;          // all of the unit's tiles are here
+  long long W;         // tiles of the line
 
   __device__ __forceinline__ bool next(const TreeArgs& a) {
     if (pos >= end) return false;
@@ -140,8 +153,7 @@ struct TreeWalk {
 
 // Every thread of the block calls this (blockDim.x a multiple of 32, all of
 // `threads` of them): sums the work of the sequences and finds where this
-// block's share starts.  Block 0 leaves the sums for the merge.  `sums` is
-// shared memory of 34 long longs.
+// block's share starts.  `sums` is shared memory of 34 long longs.
 __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, long long* sums) {
   const int n = blockDim.x, t = threadIdx.x;
   const int per = (a.B + n - 1) / n;
@@ -163,14 +175,6 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, long long* sum
     W += sums[i];
   }
   before += x - mine;
-  if (blockIdx.x == 0) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      a.prefix[b] = at;
-      at += tree_work(a, tree_seq(a, b, false));
-    }
-    if (t == 0) a.prefix[a.B] = W;
-  }
   __syncthreads();
   const int G = W < a.blocks ? (int)W : a.blocks;
   TreeWalk w;
@@ -179,6 +183,7 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, long long* sum
   w.b = 0;
   w.h = w.rt = w.first = w.n = 0;
   w.whole = false;
+  w.W = W;
   if ((int)blockIdx.x < G) {
     w.pos = tree_first(W, G, blockIdx.x);
     w.end = tree_first(W, G, blockIdx.x + 1);
@@ -202,6 +207,31 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, long long* sum
     w.q = tree_seq(a, w.b, false);
   }
   return w;
+}
+
+// One thread of every block, with a walk of its own that has not begun: what
+// this block of the merge has to do.  The share's start cuts a unit when the
+// first unit does not begin there; the unit is this block's to join when the
+// share before it holds the unit's beginning.
+__device__ __forceinline__ void tree_describe(const TreeArgs& a, TreeWalk w) {
+  TreeJoin j{};
+  const int c = blockIdx.x;
+  const long long start = w.pos;
+  if (w.next(a) && w.first > 0) {
+    const int G = w.W < a.blocks ? (int)w.W : a.blocks;
+    const long long us = start - w.first, before = tree_first(w.W, G, c - 1);
+    if (before <= us) {
+      j.b = w.b;
+      j.h = w.h;
+      j.t0 = w.rt * a.row_tokens;
+      const int tokens = w.q.cnt - j.t0 < a.row_tokens ? w.q.cnt - j.t0 : a.row_tokens;
+      j.rows = tokens * a.group;
+      j.first = c - 1;
+      j.slot = 2 * (c - 1) + (before == us ? 0 : 1);
+      j.last = tree_block_of(w.W, G, us + w.q.tiles - 1);
+    }
+  }
+  a.join[c] = j;
 }
 
 // The drafted tokens that token t of sequence b sees.

@@ -1,29 +1,34 @@
 // tree_attention_tc.cu -- attention of drafted tokens over the paged cache on
 // the 5th-generation tensor cores (tcgen05), bfloat16, head_dim 64 or 128.
 //
-// For a unit's row tile of 128 rows (drafted tokens times query heads) and
-// each tile of 128 keys: S = Q K^T into tensor memory, weights
-// P = 2^(c S - m) (c = scale log2 e) from one thread for each row back into
-// tensor memory over S, O += P V.  m is the row's reference: the running
-// maximum, but raised only when a tile's maximum passes it by more than 8
-// (weights stay below 2^8, sums far inside float32), so O, which lives in
-// tensor memory for the whole unit, is seldom rescaled.  The sum l is taken of
-// the float32 weights; the product reads them rounded to bfloat16, which is
-// what the tensor cores multiply.
+// For 128 rows (drafted tokens times query heads) and each tile of 128 keys:
+// S = Q K^T into tensor memory, weights P = 2^(c S - m) (c = scale log2 e)
+// from one thread for each row back into tensor memory over S, O += P V.  m is
+// the row's reference: the running maximum, but raised only when a tile's
+// maximum passes it by more than 8 (weights stay below 2^8, sums far inside
+// float32), so O, which lives in tensor memory for the whole unit, is seldom
+// rescaled.  The sum l is taken of the float32 weights; the product reads them
+// rounded to bfloat16, which is what the tensor cores multiply.
+//
+// Two streams share a block, each with S, O and four softmax warps of its own,
+// so one stream's softmax runs under the other's products.  A unit of more
+// than 128 rows gives each stream half the rows, and both use every tile of
+// keys and values; a smaller unit gives each stream every other tile, and the
+// two results are joined at its end.
 //
 // Bound by HBM while rows * 4 flops for each key element stay below the
 // tensor cores' rate, that is up to about 285 rows a key head; the layout
 // follows from that: one block a multiprocessor, keys and values in a ring of
-// 32 KB (16 KB) tiles that TMA fills straight from the pages, 192 KB in
+// 32 KB (16 KB) tiles that TMA fills straight from the pages, up to 192 KB in
 // flight, which covers the latency of HBM several times over.
-//   warp 0      fills the ring: each lane copies one page's rows of one half
-//               of the head (64 values, 128-byte swizzle), and looks up its
-//               page of the next tile meanwhile.
-//   warp 1      one thread issues the products: S of tile n + 1 before O of
-//               tile n, so the softmax of a tile overlaps the next product.
-//   warp 2      loads a unit's queries (TMA, rows (token, head) of the key
-//               head), once the last unit's scores are done.
-//   warps 4..7  softmax: warp w holds rows 32 (w - 4) .. + 31.
+//   warp 0       fills the ring: each lane copies one page's rows of one half
+//                of the head (64 values, 128-byte swizzle), and looks up its
+//                page of the next tile meanwhile.
+//   warp 1       one thread issues the products.
+//   warp 2       loads a unit's queries (TMA, rows (token, head) of the key
+//                head), once the last unit's scores are done.
+//   warp 3       tells the merge what to do.
+//   warps 4..7, 8..11  the streams' softmax: rows 32 (w % 4) .. + 31.
 // Tiles that some rows see and others do not (the drafted tokens, a window's
 // edge, the sequence's end) may hold NaN or infinities in places that weigh
 // nothing, and 0 * NaN would reach every row.  Their values are looked
@@ -43,7 +48,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kTile = 128;             // keys of a tile
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 bfloat16
 constexpr uint32_t kSpin = 1u << 22;
@@ -54,25 +59,32 @@ template <int D>
 struct Shape {
   static constexpr int halves = D / 64;
   static constexpr int tile_bytes = halves * kHalfBytes;
-  static constexpr int slots = D == 128 ? 6 : 12;
+  static constexpr int tiles = D == 128 ? 7 : 13;  // queries (1 or 2) and ring
   static constexpr uint32_t s_col(uint32_t i) { return 128 * i; }
   static constexpr uint32_t o_col(uint32_t i) { return 256 + D * i; }
 };
 
 struct Control {  // shared memory behind the tiles
   uint64_t kv_full[12], kv_empty[12];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done, o_free[2], v_sync, drain;
+  uint64_t q_full, q_empty, drain, v_all, b_done;
+  uint64_t s_full[2], p_ready[2], pv_done[2], v_sync[2];  // of each stream
+  // sums have been read: by the first stream at the end of every unit (both
+  // streams' where it joins them), by the second where it has rows of its own.
+  // Nobody arrives without work in the unit, so no phase is run ahead of.
+  uint64_t o_free[2];
   long long sums[34];
-  uint32_t bad[2][4];   // rows of a value tile that hold NaN or infinities
+  uint32_t bad[2][4];     // rows of a value tile that hold NaN or infinities
   uint32_t add_first[2];  // the unit's first product adds to O
+  float2 b_stats[128];    // the second stream's maximum and sum of each row
   uint32_t tmem;
   int failed;
 };
 
 template <int D>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)(1 + Shape<D>::slots) * Shape<D>::tile_bytes + sizeof(Control);
+  return 1024 + (size_t)Shape<D>::tiles * Shape<D>::tile_bytes + sizeof(Control);
 }
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a block");
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, kSpin);
@@ -155,6 +167,28 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Two float32 operations in one instruction, on a pair in 64 bits.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -179,13 +213,80 @@ struct TcArgs {
   TreeArgs a;
   int page_rows;  // rows of a copy: of one page, at most a tile
   int pages;      // copies of half a tile
+  int fit;        // drafted tokens of a stream's 128 rows
   int q_tokens;   // drafted tokens of a query copy
+  int q_tiles;    // query tiles of a unit: 2 where units have more than 128 rows
+  int slots;      // tiles of the ring
 };
 
-// Position in the ring of tile n's keys and values, of N tiles: the order in
-// which the products use them (keys of tile n + 1 before values of tile n).
+// Position in the ring of tile n's keys and values, of N tiles: keys run two
+// tiles ahead of values.
 __device__ __forceinline__ int k_at(int n) { return n == 0 ? 0 : 2 * n - 1; }
-__device__ __forceinline__ int v_at(int n, int N) { return n == N - 1 ? 2 * n + 1 : 2 * n + 2; }
+__device__ __forceinline__ int v_at(int n, int N) { return (n + 2 < N ? n + 2 : N) + n; }
+
+// A role's view of the ring: the slot and the phase parity of an entry.
+struct Entry {
+  int slot;
+  uint32_t parity;
+};
+__device__ __forceinline__ Entry entry(int e, int slots) {
+  const int round = e / slots;
+  return {e - round * slots, (uint32_t)round & 1u};
+}
+
+// The largest (c >= 0) or smallest (c < 0) of n scores of the row that the
+// thread holds, from tensor memory; hidden ones (see) do not count.
+template <bool kMasked, bool kLeast>
+__device__ __forceinline__ float extreme(uint32_t at, const uint32_t (&see)[4]) {
+  float top[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top[i] = kLeast ? INFINITY : -INFINITY;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[64];
+    tmem_ld32(at + 64 * h, x);
+    tmem_ld32(at + 64 * h + 32, x + 32);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      float v = __uint_as_float(x[i]);
+      if (kMasked && !((see[2 * h + i / 32] >> (i % 32)) & 1)) v = kLeast ? INFINITY : -INFINITY;
+      top[i & 3] = kLeast ? fminf(top[i & 3], v) : fmaxf(top[i & 3], v);
+    }
+  }
+  return kLeast ? fminf(fminf(top[0], top[1]), fminf(top[2], top[3]))
+                : fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// Weights 2^(c s - base) over the scores, in bfloat16; their float32 sum.
+template <bool kMasked>
+__device__ __forceinline__ float weigh(uint32_t at, float c, float base, const uint32_t (&see)[4]) {
+  const uint64_t cc = pair(c, c), bb = pair(-base, -base);
+  uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[64];
+    tmem_ld32(at + 64 * h, x);
+    tmem_ld32(at + 64 * h + 32, x + 32);
+    tmem_ld_wait();
+    uint32_t p[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float2 y = unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, bb));
+      float p0 = ex2(y.x), p1 = ex2(y.y);
+      if (kMasked) {
+        const uint32_t w = see[2 * h + i / 16] >> (2 * i % 32);
+        p0 = w & 1 ? p0 : 0.0f;
+        p1 = w & 2 ? p1 : 0.0f;
+      }
+      sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+      p[i] = pack_bf16(p0, p1);
+    }
+    tmem_st32(at + 32 * h, p);  // over scores that have been read
+  }
+  const float2 t = unpair(add2(sum[0], sum[1]));
+  return t.x + t.y;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -194,30 +295,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap map_v) {
   using S = Shape<D>;
   extern __shared__ uint8_t raw[];
-  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint8_t* q_tile = smem;
-  uint8_t* ring = smem + S::tile_bytes;
-  Control& sh = *reinterpret_cast<Control*>(ring + S::slots * S::tile_bytes);
+  uint8_t* q_tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* ring = q_tile + P.q_tiles * S::tile_bytes;
+  Control& sh = *reinterpret_cast<Control*>(q_tile + S::tiles * S::tile_bytes);
   const TreeArgs& a = P.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slots = P.slots;
 
   launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::slots; ++i) {
+    for (int i = 0; i < slots; ++i) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.v_all, 8);
+    mbar_init(&sh.b_done, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_ready[i], 4);
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.v_sync[i], 4);
       mbar_init(&sh.o_free[i], 4);
       sh.add_first[i] = 0;
     }
-    mbar_init(&sh.pv_done, 1);
-    mbar_init(&sh.v_sync, 4);
-    mbar_init(&sh.drain, 1);
     sh.failed = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -238,8 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- keys and values
     const int half = lane / P.pages, part = lane - half * P.pages;
     const bool mine = half < S::halves;
-    int at = 0;                 // entries of the ring filled so far
-    struct Where { int h, id, y; } cur{0, 0, 0}, prev{0, 0, 0};
+    int at = 0, slot = 0;       // entries of the ring filled so far, the next one's slot
+    uint32_t parity = 1;        // of the phase that frees it: the first round passes
+    struct Where { int h, id, y; };
     // the lane's page of the tile that starts with key j
     auto look_up = [&](int j) {
       j += part * P.page_rows;
@@ -252,36 +355,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       return t;  // no page: a place behind the pool, which reads as zeros
     };
     auto fill = [&](const CUtensorMap* map, const Where& t) {
-      const int s = at % S::slots;
-      if (at >= S::slots) ok = wait_warp(&sh.kv_empty[s], ((at / S::slots) - 1) & 1);
+      ok = wait_warp(&sh.kv_empty[slot], parity);
       if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[s], S::tile_bytes);
+      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], S::tile_bytes);
       __syncwarp();
       if (mine)
-        tma_4d(ring + s * S::tile_bytes + half * kHalfBytes + part * P.page_rows * 128, map,
-               &sh.kv_full[s], half * 64, t.y, t.h, t.id);
+        tma_4d(ring + slot * S::tile_bytes + half * kHalfBytes + part * P.page_rows * 128, map,
+               &sh.kv_full[slot], half * 64, t.y, t.h, t.id);
       ++at;
+      if (++slot == slots) {
+        slot = 0;
+        parity ^= 1;
+      }
     };
     bool some = w.next(a);
     int i = 0;
-    Where ahead{0, 0, 0};
-    if (some) ahead = look_up((w.q.lo + w.first) * kTile);
+    Where t0{0, 0, 0}, t1{0, 0, 0}, t2{0, 0, 0};  // tiles n, n - 1 and the next
+    if (some) t2 = look_up((w.q.lo + w.first) * kTile);
+    // keys 0, 1, then values n - 2 (n >= 2) before keys n: v_at and k_at
     for (int n = 0; n < N && ok; ++n) {
-      prev = cur;
-      cur = ahead;
-      // the next tile's page, before this tile's copies wait for room
-      if (++i >= w.n) {
+      const Where old = t1;
+      t1 = t0;
+      t0 = t2;
+      if (++i >= w.n) {  // the next tile's page, before this one's copies wait
         i = 0;
         some = w.next(a);
       }
-      if (some) ahead = look_up((w.q.lo + w.first + i) * kTile);
-      fill(&map_k, cur);
-      if (n > 0 && ok) fill(&map_v, prev);
+      if (some) t2 = look_up((w.q.lo + w.first + i) * kTile);
+      if (n >= 2) fill(&map_v, old);
+      if (ok) fill(&map_k, t0);
     }
-    if (N > 0 && ok) fill(&map_v, cur);
+    if (N > 1 && ok) fill(&map_v, t1);
+    if (N > 0 && ok) fill(&map_v, t0);
     if (!ok) {  // copies that nobody waited for land before the block ends
-      for (int e = at > S::slots ? at - S::slots : 0; e < at; ++e)
-        mbar_wait(&sh.kv_full[e % S::slots], (e / S::slots) & 1, kSpin >> 4);
+      for (int e = at > slots ? at - slots : 0; e < at; ++e) {
+        const Entry f = entry(e, slots);
+        mbar_wait(&sh.kv_full[f.slot], f.parity, kSpin >> 4);
+      }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- products
@@ -289,54 +399,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
       const uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
       const uint32_t q_base = smem_u32(q_tile), ring_base = smem_u32(ring);
-      int unit = -1, left = 0;       // of tile n
-      int o_unit = 0;                // of tile n - 1
-      bool o_first = false, first = false;
-      for (int n = 0; n <= N && ok; ++n) {
-        const int before = unit;
-        const bool before_first = first;
-        if (n < N) {
-          first = left == 0;
-          if (first) {
-            w.next(a);
-            left = w.n;
-            ++unit;
-            ok = wait(&sh.q_full, unit & 1);
-          }
-          --left;
-          const int e = k_at(n), s = e % S::slots;
-          ok = ok && wait(&sh.kv_full[s], (e / S::slots) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t k_base = ring_base + s * S::tile_bytes;
+      int g = 0;                     // tiles of the units before
+      uint32_t halved = 0, freed = 0;  // units that gave each stream half the rows
+      uint32_t used[2] = {0, 0};     // tiles that a stream has weighed
+      Entry k{0, 0};
+      // scores of the keys in k for a stream, from its query tile
+      auto scores = [&](int st, int tile) {
+        const uint32_t k_base = ring_base + k.slot * S::tile_bytes;
+        const uint32_t q_at = q_base + tile * S::tile_bytes;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-            mma_bf16(tmem + S::s_col(n & 1), smem_desc_sw128(q_base + off, 16, 1024),
-                     smem_desc_sw128(k_base + off, 16, 1024), idesc_s, k != 0);
-          }
-          mma_commit(&sh.s_full[n & 1]);
-          mma_commit(&sh.kv_empty[s]);
-          if (left == 0) mma_commit(&sh.q_empty);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = (i >> 2) * kHalfBytes + (i & 3) * 32;
+          mma_bf16(tmem + S::s_col(st), smem_desc_sw128(q_at + off, 16, 1024),
+                   smem_desc_sw128(k_base + off, 16, 1024), idesc_s, i != 0);
         }
-        if (n > 0) {
-          const int m = n - 1, e = v_at(m, N), s = e % S::slots;
-          o_unit = before;
-          o_first = before_first;
-          if (o_first) ok = wait(&sh.o_free[o_unit & 1], ((o_unit >> 1) & 1) ^ 1);
-          ok = ok && wait(&sh.kv_full[s], (e / S::slots) & 1);
-          ok = ok && wait(&sh.p_ready[m & 1], (m >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const bool add = !o_first || *(volatile uint32_t*)&sh.add_first[m & 1];
-          const uint32_t v_base = ring_base + s * S::tile_bytes;
+        mma_commit(&sh.s_full[st]);
+      };
+      auto keys = [&](int n) {
+        k = entry(k_at(n), slots);
+        ok = ok && wait(&sh.kv_full[k.slot], k.parity);
+        tc_fence_after();
+      };
+      auto sums = [&](int st, const Entry& v, bool first) {
+        ok = ok && wait(&sh.p_ready[st], used[st]++ & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const bool add = !first || *(volatile uint32_t*)&sh.add_first[st];
+        const uint32_t v_base = ring_base + v.slot * S::tile_bytes;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16_ta(tmem + S::o_col(o_unit & 1), tmem + S::s_col(m & 1) + 8 * k,
-                        smem_desc_sw128(v_base + k * 2048, kHalfBytes, 1024), idesc_o,
-                        add || k != 0);
-          mma_commit(&sh.pv_done);
-          mma_commit(&sh.kv_empty[s]);
+        for (int i = 0; i < kTile / 16; ++i)
+          mma_bf16_ta(tmem + S::o_col(st), tmem + S::s_col(st) + 8 * i,
+                      smem_desc_sw128(v_base + i * 2048, kHalfBytes, 1024), idesc_o, add || i != 0);
+        mma_commit(&sh.pv_done[st]);
+      };
+      for (int unit = 0; ok && w.next(a); ++unit, g += w.n) {
+        ok = wait(&sh.q_full, unit & 1);
+        const bool both = w.q.cnt - w.rt * a.row_tokens > P.fit;
+        if (ok) keys(g);
+        if (!ok) break;
+        scores(0, 0);
+        if (both) scores(1, 1);
+        mma_commit(&sh.kv_empty[k.slot]);
+        if (!both && w.n > 1) {
+          keys(g + 1);
+          if (!ok) break;
+          scores(1, 0);
+          mma_commit(&sh.kv_empty[k.slot]);
+        }
+        if (w.n <= (both ? 1 : 2)) mma_commit(&sh.q_empty);
+        if (unit > 0) ok = wait(&sh.o_free[0], (unit - 1) & 1);
+        if (freed < halved) ok = ok && wait(&sh.o_free[1], freed++ & 1);
+        halved += both;
+        for (int i = 0; i < w.n && ok; ++i) {
+          const Entry v = entry(v_at(g + i, N), slots);
+          ok = wait(&sh.kv_full[v.slot], v.parity);
+          if (both) {
+            const bool more = i + 1 < w.n;
+            sums(0, v, i == 0);
+            if (more && ok) {
+              keys(g + i + 1);
+              if (ok) scores(0, 0);
+            }
+            if (ok) sums(1, v, i == 0);
+            if (!ok) break;
+            mma_commit(&sh.kv_empty[v.slot]);
+            if (more) {
+              scores(1, 1);
+              mma_commit(&sh.kv_empty[k.slot]);
+              if (i + 2 == w.n) mma_commit(&sh.q_empty);
+            }
+          } else {
+            if (ok) sums(i & 1, v, i < 2);
+            if (!ok) break;
+            mma_commit(&sh.kv_empty[v.slot]);
+            if (i + 2 < w.n) {
+              keys(g + i + 2);
+              if (!ok) break;
+              scores(i & 1, 0);
+              mma_commit(&sh.kv_empty[k.slot]);
+              if (i + 3 == w.n) mma_commit(&sh.q_empty);
+            }
+          }
         }
       }
       if (!ok) {
@@ -347,83 +490,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // --------------------------------------------------------- queries
     if (lane == 0) {
-      const uint32_t bytes = S::halves * P.q_tokens * a.group * 128;
       int unit = 0;
       for (; ok && w.next(a); ++unit) {
         if (unit > 0) ok = wait(&sh.q_empty, (unit - 1) & 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(&sh.q_full, bytes);
-        for (int i = 0; i < S::halves; ++i)
-          tma_5d(q_tile + i * kHalfBytes, &map_q, &sh.q_full, i * 64, 0, w.h,
-                 w.rt * a.row_tokens, w.b);
+        const int t0 = w.rt * a.row_tokens;
+        const int tiles = w.q.cnt - t0 > P.fit ? 2 : 1;
+        mbar_arrive_expect_tx(&sh.q_full, tiles * S::halves * P.q_tokens * a.group * 128);
+        for (int i = 0; i < tiles * S::halves; ++i) {
+          const int tile = i / S::halves, half = i - tile * S::halves;
+          tma_5d(q_tile + i * kHalfBytes, &map_q, &sh.q_full, half * 64, 0, w.h,
+                 t0 + tile * P.fit, w.b);
+        }
       }
       if (!ok && unit > 0) mbar_wait(&sh.q_full, (unit - 1) & 1, kSpin >> 4);
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    if (lane == 0) tree_describe(a, w);
+  } else {
     // --------------------------------------------------------- softmax
-    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const int st = warp >= 8, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_at = lanes + S::s_col(st), o_at = lanes + S::o_col(st);
     const float c = a.scale * kLog2e;
-    int n = 0, unit = 0, syncs = 0;
-    bool is_first = true;  // the block's first unit
-    for (; ok && w.next(a); ++unit) {
-      const int t0 = w.rt * a.row_tokens;
-      const int tokens = w.q.cnt - t0 < a.row_tokens ? w.q.cnt - t0 : a.row_tokens;
+    int g = 0;                       // tiles of the units before
+    uint32_t used = 0, syncs = 0, alls = 0, joins = 0;  // phases of the barriers
+    bool is_first = true;            // the block's first unit
+    for (; ok && w.next(a); g += w.n) {
+      const int t_unit = w.rt * a.row_tokens, left = w.q.cnt - t_unit;
+      const bool both = left > P.fit;             // half the rows each
+      const int t0 = t_unit + (both && st ? P.fit : 0);
+      const int more = w.q.cnt - t0, tokens = more < P.fit ? more : P.fit;
       const int rows = tokens * a.group;
       const int t = t0 + r / a.group;
       const bool valid = r < rows, any = quarter * 32 < rows;
       const uint64_t bits = valid ? tree_mask(a, w.b, t, w.q.cnt) : 0;
       const int len = w.q.len;
-      int lo = valid ? tree_window_lo(a, w.b, t, len) : 0;
+      const int lo = valid ? tree_window_lo(a, w.b, t, len) : 0;
       int lo_most = 0;  // committed keys below this are hidden from some row
       if (a.window > 0) {
-        for (int i = lane; i < tokens; i += 32) {
-          const int x = tree_window_lo(a, w.b, t0 + i, len);
+        for (int i = lane; i < left && i < a.row_tokens; i += 32) {
+          const int x = tree_window_lo(a, w.b, t_unit + i, len);
           lo_most = x > lo_most ? x : lo_most;
         }
         lo_most = __reduce_max_sync(0xffffffffu, lo_most);
       }
       float m = -INFINITY, l = 0.0f;
-      for (int tile = 0; tile < w.n && ok; ++tile, ++n) {
+      const int first = both ? 0 : st, step = both ? 1 : 2;
+      for (int tile = first; tile < w.n && ok; tile += step, ++used) {
         const int j0 = (w.q.lo + w.first + tile) * kTile;
         const bool masked = j0 + kTile > len || j0 < lo_most;
-        const uint32_t s_at = lanes + S::s_col(n & 1), o_at = lanes + S::o_col(unit & 1);
-        ok = wait_warp(&sh.s_full[n & 1], (n >> 1) & 1);
+        ok = wait_warp(&sh.s_full[st], used & 1);
         if (!ok) break;
         tc_fence_after();
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         if (any) {
-          float x[kTile];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x) + 32 * i);
-          tmem_ld_wait();
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float best;
           if (masked) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) see[i] = seen32(j0 + 32 * i, lo, len, bits);
-#pragma unroll
-            for (int i = 0; i < kTile; ++i) {
-              x[i] *= c;
-              if ((see[i / 32] >> (i % 32)) & 1) top[i & 3] = fmaxf(top[i & 3], x[i]);
-              else x[i] = -INFINITY;
-            }
+            best = c < 0.0f ? extreme<true, true>(s_at, see) : extreme<true, false>(s_at, see);
           } else {
-#pragma unroll
-            for (int i = 0; i < kTile; ++i) {
-              x[i] *= c;
-              top[i & 3] = fmaxf(top[i & 3], x[i]);
-            }
+            best = c < 0.0f ? extreme<false, true>(s_at, see) : extreme<false, false>(s_at, see);
           }
-          const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          best *= c;
           const bool raise = valid && best > m + kRaise;  // m = -inf: any maximum
           if (__any_sync(0xffffffffu, raise)) {
             const float now = raise ? best : m;
             const float f = raise ? ex2(m - now) : 1.0f;
-            if (tile > 0) {
-              ok = wait_warp(&sh.pv_done, (n - 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
+            if (tile > first) {  // the last product into O ended before these scores did
+#pragma unroll 1
               for (int i = 0; i < D / 32; ++i) {
                 uint32_t o[32];
                 tmem_ld32(o_at + 32 * i, o);
@@ -437,71 +573,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = now;
           }
           const float base = m == -INFINITY ? 0.0f : m;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t p[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int e = 64 * i + 2 * k;
-              const float p0 = ex2(x[e] - base), p1 = ex2(x[e + 1] - base);
-              sum[(2 * k) & 3] += p0;
-              sum[(2 * k + 1) & 3] += p1;
-              p[k] = pack_bf16(p0, p1);
-            }
-            tmem_st32(s_at + 32 * i, p);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += masked ? weigh<true>(s_at, c, base, see) : weigh<false>(s_at, c, base, see);
           tmem_st_wait();
         }
         uint32_t found = 0;
         if (masked) {
           // the tile's values: this thread looks through key j0 + r's
-          const int e = v_at(n, N), slot = e % S::slots;
-          uint8_t* v = ring + slot * S::tile_bytes;
-          ok = wait_warp(&sh.kv_full[slot], (e / S::slots) & 1);
+          const Entry e = entry(v_at(g + tile, N), slots);
+          uint8_t* v = ring + e.slot * S::tile_bytes;
+          ok = wait_warp(&sh.kv_full[e.slot], e.parity);
           if (!ok) break;
           uint32_t worst = 0;
 #pragma unroll
           for (int i = 0; i < S::halves * 8; ++i) {
             const uint4 u = *reinterpret_cast<const uint4*>(
                 v + (i >> 3) * kHalfBytes + r * 128 + (((i & 7) ^ (r & 7)) << 4));
-            const uint32_t k[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {  // an exponent of ones carries past it
-              worst |= (k[d] & 0x7f807f80u) + 0x00800080u;
-            }
+            // an exponent of ones carries past it
+            worst |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                     ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
           }
           const uint32_t b = __ballot_sync(0xffffffffu, (worst & 0x80008000u) != 0);
           if (lane == 0) {
-            sh.bad[n & 1][quarter] = b;
-            mbar_arrive(&sh.v_sync);
+            sh.bad[st][quarter] = b;
+            mbar_arrive(&sh.v_sync[st]);
           }
-          ok = wait_warp(&sh.v_sync, syncs++ & 1);
+          ok = wait_warp(&sh.v_sync[st], syncs++ & 1);
           if (!ok) break;
           uint32_t rows_bad[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            rows_bad[i] = *(volatile uint32_t*)&sh.bad[n & 1][i];
+            rows_bad[i] = *(volatile uint32_t*)&sh.bad[st][i];
             found |= rows_bad[i];
           }
           if (found) {
             if (any) {
-              if (tile > 0) {
-                ok = wait_warp(&sh.pv_done, (n - 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-              } else {  // O starts from what is added here
+              if (tile == first) {  // O starts from what is added here
                 for (int d = 0; d < D; ++d) tmem_st1(o_at + d, 0);
                 tmem_st_wait();
               }
               for (int j = 0; j < kTile; ++j) {
-                if (!((rows_bad[j >> 5] >> (j & 31)) & 1)) continue;
+                const uint32_t word = j < 64 ? (j < 32 ? rows_bad[0] : rows_bad[1])
+                                             : (j < 96 ? rows_bad[2] : rows_bad[3]);
+                if (!((word >> (j & 31)) & 1)) continue;
                 const uint32_t pp = tmem_ld1(s_at + (j >> 1));
                 tmem_ld_wait();
                 const float p = __uint_as_float(j & 1 ? pp & 0xffff0000u : pp << 16);
-                const uint32_t word = j < 64 ? (j < 32 ? see[0] : see[1]) : (j < 96 ? see[2] : see[3]);
-                const bool sees = (word >> (j & 31)) & 1;
+                const uint32_t sw = j < 64 ? (j < 32 ? see[0] : see[1]) : (j < 96 ? see[2] : see[3]);
+                const bool sees = (sw >> (j & 31)) & 1;
                 for (int d = 0; d < D; ++d) {
                   const uint16_t u = *reinterpret_cast<const uint16_t*>(
                       v + (d >> 6) * kHalfBytes + j * 128 + ((((d & 63) >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
@@ -513,11 +631,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            // cleared once every stream that uses the tile has read it, by one
+            // of them, and used only then
+            uint64_t* bar = both ? &sh.v_all : &sh.v_sync[st];
+            uint32_t& phase = both ? alls : syncs;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.v_sync);
-            ok = wait_warp(&sh.v_sync, syncs++ & 1);
+            if (lane == 0) mbar_arrive(bar);
+            ok = wait_warp(bar, phase++ & 1);
             if (!ok) break;
-            if ((rows_bad[quarter] >> lane) & 1) {
+            if ((!both || st == 0) && ((rows_bad[quarter] >> lane) & 1)) {
               for (int d = 0; d < D; ++d) {
                 uint16_t* u = reinterpret_cast<uint16_t*>(
                     v + (d >> 6) * kHalfBytes + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2);
@@ -525,61 +647,100 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             fence_proxy_async_smem();
+            if (both) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar);
+              ok = wait_warp(bar, phase++ & 1);
+              if (!ok) break;
+            }
           }
         }
-        if (threadIdx.x == 128) *(volatile uint32_t*)&sh.add_first[n & 1] = found != 0;
+        if (quarter == 0 && lane == 0) *(volatile uint32_t*)&sh.add_first[st] = found != 0;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[n & 1]);
+        if (lane == 0) mbar_arrive(&sh.p_ready[st]);
       }
       if (!ok) break;
-      // the unit's rows
-      ok = wait_warp(&sh.pv_done, (n - 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
+      const bool worked = first < w.n;  // the stream had a tile of this unit
+      if (worked) {
+        ok = wait_warp(&sh.pv_done[st], (used - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
       const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
       is_first = false;
-      if (any) {
-        const uint32_t o_at = lanes + S::o_col(unit & 1);
-        const size_t row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r % a.group;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
+      if (!both && st == 1) {
+        // the first stream joins the two
+        if (worked) {
+          sh.b_stats[r] = make_float2(m, l);
           __syncwarp();
-          tmem_ld32(o_at + 32 * i, o);
-          tmem_ld_wait();
-          if (valid && w.whole) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * i);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t p[4];
-#pragma unroll
-              for (int d = 0; d < 4; ++d)
-                p[d] = pack_bf16(__uint_as_float(o[8 * k + 2 * d]) * inv,
-                                 __uint_as_float(o[8 * k + 2 * d + 1]) * inv);
-              to[k] = make_uint4(p[0], p[1], p[2], p[3]);
-            }
-          } else if (valid) {
-            uint4* to = reinterpret_cast<uint4*>(tree_part(a, slot) + (size_t)r * D + 32 * i);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          }
+          if (lane == 0) mbar_arrive(&sh.b_done);
         }
-        if (valid) {
-          if (!w.whole) {
-            float* st = tree_part_stats(a, slot) + 2 * r;
-            st[0] = m;
-            st[1] = l;
-          } else if (a.lse) {
-            a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+      } else {
+        const bool join = !both && w.n > 1;
+        float fa = 1.0f, fb = 0.0f;
+        if (join) {
+          ok = wait_warp(&sh.b_done, joins++ & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 o = sh.b_stats[r];
+          const float now = fmaxf(m, o.x);
+          fa = m == now ? 1.0f : ex2(m - now);
+          fb = o.x == now ? 1.0f : ex2(o.x - now);
+          l = l * fa + o.y * fb;
+          m = now;
+        }
+        if (any) {
+          const size_t row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r % a.group;
+          const int part_row = (t0 - t_unit) * a.group + r;
+          const float inv = w.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(o_at + 32 * i, o);
+            if (join) {
+              uint32_t o2[32];
+              tmem_ld32(lanes + S::o_col(1) + 32 * i, o2);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * fa + __uint_as_float(o2[k]) * fb);
+            } else {
+              tmem_ld_wait();
+            }
+            if (valid && w.whole) {
+              uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * i);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t p[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                  p[d] = pack_bf16(__uint_as_float(o[8 * k + 2 * d]) * inv,
+                                   __uint_as_float(o[8 * k + 2 * d + 1]) * inv);
+                to[k] = make_uint4(p[0], p[1], p[2], p[3]);
+              }
+            } else if (valid) {
+              uint4* to = reinterpret_cast<uint4*>(tree_part(a, slot) + (size_t)part_row * D + 32 * i);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+          if (valid) {
+            if (!w.whole) {
+              float* stats = tree_part_stats(a, slot) + 2 * part_row;
+              stats[0] = m;
+              stats[1] = l;
+            } else if (a.lse) {
+              a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_free[unit & 1]);
+      if (lane == 0 && (both || st == 0)) mbar_arrive(&sh.o_free[st]);
     }
   }
   if (!ok) sh.failed = 1;
@@ -611,7 +772,10 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   P.a = a;
   P.page_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
   P.pages = kTile / P.page_rows;
-  P.q_tokens = a.T < a.row_tokens ? a.T : a.row_tokens;
+  P.fit = kTreeRows / a.group;
+  P.q_tokens = a.T < P.fit ? a.T : P.fit;
+  P.q_tiles = a.T > P.fit ? 2 : 1;
+  P.slots = Shape<D>::tiles - P.q_tiles;
   CUtensorMap mq, mk, mv;
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   {
@@ -650,7 +814,8 @@ bool tree_tc_supported(const TreeArgs& a) {
 
 cudaError_t launch_tree_tc(TreeArgs& a, int sms, cudaStream_t stream) {
   a.tile = kTile;
-  a.row_tokens = kTreeRows / a.group;
+  const int fit = kTreeRows / a.group;  // tokens of a stream's rows
+  a.row_tokens = a.T <= fit ? fit : 2 * fit;
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
   a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
   a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
