@@ -24,6 +24,20 @@ __all__ = ["draft_block", "draft_block_per_request", "draft_block_noalloc",
            "DraftWorkspace", "DsparkError", "F32", "BF16", "version"]
 
 
+_CACHE = ("PagedCache", "TreeWorkspace", "cache_reserve", "cache_release",
+          "cache_fork", "cache_accept", "cache_append", "tree_attention")
+
+
+def __getattr__(name):
+    """The paged cache (cache.py) is loaded, and torch with it, when it is
+    first asked for."""
+    if name in _CACHE:
+        from . import cache
+        globals().update({n: getattr(cache, n) for n in _CACHE})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 def _torch():
     import torch
     return torch
@@ -400,11 +414,6 @@ def sample_temperature(logits, seed, offset, *, T: float = 1.0,
         _ptr(workspace), workspace.numel(), _stream(stream))
     _lib.check("dspark_sample_temperature", st)
     return tokens, probs
-
-
-from .cache import (PagedCache, TreeWorkspace, cache_accept,  # noqa: E402
-                    cache_append, cache_fork, cache_release, cache_reserve,
-                    tree_attention)
 
 
 def noise_words(seed: int, offset: int, k: int, stream_id: int, n: int,

@@ -8,19 +8,12 @@ import ctypes
 import math
 from typing import Optional
 
+import torch
+
 from . import _lib
 from ._lib import BF16, F32, DsparkError
 
 CONTROL_WORDS = 64 + 2 * 1024  # DSPARK_CACHE_CONTROL_WORDS
-
-
-def _torch():
-    import torch
-    return torch
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 class PagedCache:
@@ -32,7 +25,6 @@ class PagedCache:
     def __init__(self, layers: int, num_pages: int, page_size: int, kv_heads: int,
                  head_dim: int, max_seqs: int, max_pages: int, dtype=None,
                  device=None, stream=None):
-        torch = _torch()
         device = device or "cuda"
         i32 = dict(dtype=torch.int32, device=device)
         self._set(torch.empty(layers, 2, num_pages, kv_heads, page_size, head_dim,
@@ -40,9 +32,7 @@ class PagedCache:
                   torch.empty(max_seqs, max_pages, **i32), torch.empty(max_seqs, **i32),
                   torch.empty(num_pages, **i32), torch.empty(num_pages, **i32),
                   torch.empty(CONTROL_WORDS, **i32))
-        with self._current():
-            _check("dspark_cache_init", _lib.load().dspark_cache_init(
-                self._ref, self._stream(stream)))
+        _call(self, "dspark_cache_init", stream)
 
     @classmethod
     def from_tensors(cls, pool, block_table, page_count, ref_count, free_list, control):
@@ -55,7 +45,6 @@ class PagedCache:
         return self
 
     def _set(self, pool, block_table, page_count, ref_count, free_list, control):
-        torch = _torch()
         if pool.dim() != 6 or pool.shape[1] != 2:
             raise ValueError("pool must be [layers, 2, num_pages, kv_heads, page_size, head_dim]")
         if pool.dtype not in (torch.float32, torch.bfloat16):
@@ -82,6 +71,7 @@ class PagedCache:
         self.page_size, self.head_dim = page_size, head_dim
         self.max_seqs, self.max_pages = max_seqs, max_pages
         self.device, self.dtype = pool.device, pool.dtype
+        self.index = pool.get_device()  # -1 on the host
         self.buffer = control  # the device error word (read_device_error)
         self._struct = _lib.CacheStruct(
             pool.data_ptr(), F32 if pool.dtype == torch.float32 else BF16, layers,
@@ -90,89 +80,77 @@ class PagedCache:
             free_list.data_ptr(), control.data_ptr())
         self._ref = ctypes.byref(self._struct)
 
-    def _current(self):
-        """Makes the cache's device the current one for a launch."""
-        torch = _torch()
-        if self.device.type != "cuda":
-            raise ValueError("the cache is not on a CUDA device")
-        if self.device.index in (None, torch.cuda.current_device()):
-            return _NOTHING
-        return torch.cuda.device(self.device)
 
-    def _stream(self, stream) -> int:
-        if stream is None:
-            stream = _torch().cuda.current_stream(self.device)
-        return stream.cuda_stream
-
-
-class _Nothing:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NOTHING = _Nothing()
-
-
-def _check(fn: str, status: int) -> None:
+def _call(cache, fn, stream, *args):
+    """Calls the library on the cache's device and on `stream` (None: that
+    device's current stream)."""
+    index = cache.index
+    if index < 0:
+        raise ValueError("the cache is not on a CUDA device")
+    if index == torch._C._cuda_getDevice():
+        handle = (torch._C._cuda_getCurrentRawStream(index) if stream is None
+                  else stream.cuda_stream)
+        status = getattr(_lib.load(), fn)(cache._ref, *args, handle)
+    else:
+        with torch.cuda.device(index):
+            handle = (torch._C._cuda_getCurrentRawStream(index) if stream is None
+                      else stream.cuda_stream)
+            status = getattr(_lib.load(), fn)(cache._ref, *args, handle)
     if status != 0:
         raise DsparkError(fn, status)
 
 
-def _ints(cache, **tensors):
-    """int32 vectors [B], contiguous, on the cache's device (None passes)."""
-    torch = _torch()
-    B = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if B is None:
-            B = t.shape[0] if t.dim() else 0
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B:
-            raise TypeError(f"{name} must be int32 [B]")
-        if not t.is_contiguous():
-            raise ValueError("all tensors must be contiguous")
-        if t.device != cache.device:
-            raise ValueError(f"{name} must be on the cache's device")
-    return B
-
-
-def _same(cache, name, t, shape, dtype):
-    if t.dtype != dtype or t.shape != shape:
-        raise TypeError(f"{name} must be {dtype} {list(shape)}")
+def _bad(cache, name, t, dtype, shape):
+    """Says what is wrong with a tensor that _fits refused."""
+    if t.dtype != dtype or t.shape != tuple(shape):
+        raise TypeError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
     if not t.is_contiguous():
-        raise ValueError("all tensors must be contiguous")
-    if t.device != cache.device:
-        raise ValueError(f"{name} must be on the cache's device")
+        raise ValueError(f"all tensors must be contiguous: {name} is not")
+    raise ValueError(f"{name} must be on the cache's device")
+
+
+def _fits(cache, t, dtype, shape) -> bool:
+    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == cache.index)
+
+
+def _ptr_of(cache, name, t, dtype, shape) -> Optional[int]:
+    """The address of a tensor of this dtype and shape, contiguous on the
+    cache's device; None stays None."""
+    if t is None:
+        return None
+    if not _fits(cache, t, dtype, shape):
+        _bad(cache, name, t, dtype, shape)
+    return t.data_ptr()
+
+
+def _batch(length) -> int:
+    if length.dim() != 1:
+        raise TypeError("the sequences of a call are int32 [B]")
+    return length.shape[0]
 
 
 def cache_reserve(cache: PagedCache, length, tokens: int, *, seq=None, stream=None) -> None:
     """Pages for ``tokens`` more tokens of each sequence: length [B] int32
     committed tokens, seq [B] int32 or None (sequences 0..B-1)."""
-    B = _ints(cache, length=length, seq=seq)
-    with cache._current():
-        _check("dspark_cache_reserve", _lib.load().dspark_cache_reserve(
-            cache._ref, _ptr(seq), length.data_ptr(), tokens, B, cache._stream(stream)))
+    i32, shape = torch.int32, (_batch(length),)
+    _call(cache, "dspark_cache_reserve", stream, _ptr_of(cache, "seq", seq, i32, shape),
+          _ptr_of(cache, "length", length, i32, shape), tokens, shape[0])
 
 
 def cache_release(cache: PagedCache, seq, *, stream=None) -> None:
     """The sequences seq [B] int32 give up all their pages."""
-    B = _ints(cache, seq=seq)
-    with cache._current():
-        _check("dspark_cache_release", _lib.load().dspark_cache_release(
-            cache._ref, seq.data_ptr(), B, cache._stream(stream)))
+    i32, shape = torch.int32, (_batch(seq),)
+    _call(cache, "dspark_cache_release", stream, _ptr_of(cache, "seq", seq, i32, shape), shape[0])
 
 
 def cache_fork(cache: PagedCache, parent, child, length, *, stream=None) -> None:
     """Sequence child[b] becomes a copy of the first length[b] tokens of
     parent[b]: full pages are shared, a partly filled one is copied."""
-    B = _ints(cache, parent=parent, child=child, length=length)
-    with cache._current():
-        _check("dspark_cache_fork", _lib.load().dspark_cache_fork(
-            cache._ref, parent.data_ptr(), child.data_ptr(), length.data_ptr(), B,
-            cache._stream(stream)))
+    i32, shape = torch.int32, (_batch(length),)
+    _call(cache, "dspark_cache_fork", stream, _ptr_of(cache, "parent", parent, i32, shape),
+          _ptr_of(cache, "child", child, i32, shape),
+          _ptr_of(cache, "length", length, i32, shape), shape[0])
 
 
 def cache_accept(cache: PagedCache, length, accepted_len, tokens: int, *, path=None,
@@ -180,20 +158,19 @@ def cache_accept(cache: PagedCache, length, accepted_len, tokens: int, *, path=N
     """Keeps accepted_len[b] + extra of the ``tokens`` tokens behind the
     committed ones (path [B, P] int32: which ones; None: the first) and gives
     up the pages behind them.  Returns new_length [B] int32."""
-    torch = _torch()
-    B = _ints(cache, length=length, accepted_len=accepted_len, seq=seq, new_length=new_length)
+    i32, shape = torch.int32, (_batch(length),)
     width = 0
     if path is not None:
         if path.dim() != 2:
             raise TypeError("path must be int32 [B, P]")
         width = path.shape[1]
-        _same(cache, "path", path, (B, width), torch.int32)
+    at = _ptr_of(cache, "length", length, i32, shape)
     if new_length is None:
-        new_length = torch.empty_like(length)
-    with cache._current():
-        _check("dspark_cache_accept", _lib.load().dspark_cache_accept(
-            cache._ref, _ptr(seq), length.data_ptr(), accepted_len.data_ptr(), _ptr(path),
-            width, extra, tokens, B, new_length.data_ptr(), cache._stream(stream)))
+        new_length = length.new_empty(shape)
+    _call(cache, "dspark_cache_accept", stream, _ptr_of(cache, "seq", seq, i32, shape), at,
+          _ptr_of(cache, "accepted_len", accepted_len, i32, shape),
+          _ptr_of(cache, "path", path, i32, (shape[0], width)), width, extra, tokens, shape[0],
+          _ptr_of(cache, "new_length", new_length, i32, shape))
     return new_length
 
 
@@ -218,40 +195,34 @@ def cache_append(cache: PagedCache, layer: int, q, k, v, length, *, position, co
     and v may be parts of one projection's output.  position [B, T] int32
     rows of cos_sin [max_position, rot_dim] float32 (cosines, then sines);
     q_weight and k_weight [D] float32 or None.  Returns q_out."""
-    torch = _torch()
     if q.dim() != 4:
         raise ValueError("q must be [B, T, heads, D]")
     B, T, heads, D = q.shape
     kv = (B, T, cache.kv_heads, cache.head_dim)
     if D != cache.head_dim or k.shape != kv or v.shape != kv:
         raise ValueError("q must be [B, T, heads, D], k and v [B, T, kv_heads, D]")
-    dtype, device = cache.dtype, cache.device
-    if q.dtype != dtype or k.dtype != dtype or v.dtype != dtype:
+    dtype, index = cache.dtype, cache.index
+    if not (q.dtype is dtype and k.dtype is dtype and v.dtype is dtype):
         raise TypeError("q, k and v must have the cache's dtype")
-    if q.device != device or k.device != device or v.device != device:
+    if not (q.get_device() == index and k.get_device() == index and v.get_device() == index):
         raise ValueError("q, k and v must be on the cache's device")
-    if _ints(cache, length=length, token_count=token_count, seq=seq) != B:
-        raise TypeError("length must be int32 [B]")
-    _same(cache, "position", position, (B, T), torch.int32)
     if cos_sin.dim() != 2:
         raise TypeError("cos_sin must be float32 [max_position, rot_dim]")
-    _same(cache, "cos_sin", cos_sin, cos_sin.shape, torch.float32)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _same(cache, name, w, (D,), torch.float32)
     if q_out is None:
-        q_out = torch.empty((B, T, heads, D), dtype=dtype, device=device)
-    else:
-        _same(cache, "q_out", q_out, (B, T, heads, D), dtype)
-    with cache._current():
-        _check("dspark_cache_append", _lib.load().dspark_cache_append(
-            cache._ref, layer, _ptr(seq), length.data_ptr(), _ptr(token_count),
-            q.data_ptr(), _token_stride("q", q, B, T, D),
-            k.data_ptr(), _token_stride("k", k, B, T, D),
-            v.data_ptr(), _token_stride("v", v, B, T, D),
-            _ptr(q_weight), _ptr(k_weight), eps, cos_sin.data_ptr(), cos_sin.shape[0],
-            cos_sin.shape[1], int(interleaved), position.data_ptr(), B, T, heads,
-            q_out.data_ptr(), cache._stream(stream)))
+        q_out = torch.empty((B, T, heads, D), dtype=dtype, device=cache.device)
+    i32, f32, shape = torch.int32, torch.float32, (B,)
+    _call(cache, "dspark_cache_append", stream, layer, _ptr_of(cache, "seq", seq, i32, shape),
+          _ptr_of(cache, "length", length, i32, shape),
+          _ptr_of(cache, "token_count", token_count, i32, shape),
+          q.data_ptr(), _token_stride("q", q, B, T, D),
+          k.data_ptr(), _token_stride("k", k, B, T, D),
+          v.data_ptr(), _token_stride("v", v, B, T, D),
+          _ptr_of(cache, "q_weight", q_weight, f32, (D,)),
+          _ptr_of(cache, "k_weight", k_weight, f32, (D,)), eps,
+          _ptr_of(cache, "cos_sin", cos_sin, f32, cos_sin.shape), cos_sin.shape[0],
+          cos_sin.shape[1], 1 if interleaved else 0,
+          _ptr_of(cache, "position", position, i32, (B, T)), B, T, heads,
+          _ptr_of(cache, "q_out", q_out, dtype, (B, T, heads, D)))
     return q_out
 
 
@@ -264,7 +235,7 @@ class TreeWorkspace:
         if n == 0:
             raise DsparkError("dspark_tree_workspace_bytes", 2)
         self.nbytes = n
-        self.buffer = _torch().empty(n, dtype=_torch().uint8, device=device or "cuda")
+        self.buffer = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
 def tree_attention(cache: PagedCache, layer: int, q, length, *, mask=None, token_count=None,
@@ -277,37 +248,31 @@ def tree_attention(cache: PagedCache, layer: int, q, length, *, mask=None, token
     tokens that mask allows: int64 words [B, T] or [T], bit j of word t says
     that token t sees drafted token j (None: tokens 0..t).  scale defaults to
     1 / sqrt(D).  Returns (out, lse); lse is None unless asked for."""
-    torch = _torch()
     if q.dim() != 4:
         raise ValueError("q must be [B, T, heads, D]")
     B, T, heads, D = q.shape
-    _same(cache, "q", q, (B, T, heads, cache.head_dim), cache.dtype)
-    if _ints(cache, length=length, token_count=token_count, seq=seq) != B:
-        raise TypeError("length must be int32 [B]")
+    full = (B, T, heads, cache.head_dim)
+    at = _ptr_of(cache, "q", q, cache.dtype, full)
     stride = 0
-    if mask is not None:
-        _same(cache, "mask", mask, (T,) if mask.dim() == 1 else (B, T), torch.int64)
-        stride = T if mask.dim() == 2 else 0
-    if position is not None:
-        _same(cache, "position", position, (B, T), torch.int32)
+    if mask is not None and mask.dim() == 2:
+        stride = T
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _same(cache, "out", out, (B, T, heads, D), cache.dtype)
-    if lse is not None:
-        _same(cache, "lse", lse, (B, T, heads), torch.float32)
-    elif with_lse:
+    if lse is None and with_lse:
         lse = torch.empty((B, T, heads), dtype=torch.float32, device=cache.device)
     if workspace is None:
         workspace = TreeWorkspace(B, T, heads, cache.kv_heads, D, device=cache.device)
-    elif workspace.buffer.device != cache.device:
+    elif workspace.buffer.get_device() != cache.index:
         raise ValueError("workspace must be on the cache's device")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with cache._current():
-        _check("dspark_tree_attention", _lib.load().dspark_tree_attention(
-            cache._ref, layer, _ptr(seq), length.data_ptr(), _ptr(token_count),
-            q.data_ptr(), _ptr(mask), stride, _ptr(position), window, scale, B, T, heads,
-            out.data_ptr(), _ptr(lse), workspace.buffer.data_ptr(), workspace.nbytes,
-            cache._stream(stream)))
+    i32, shape = torch.int32, (B,)
+    _call(cache, "dspark_tree_attention", stream, layer, _ptr_of(cache, "seq", seq, i32, shape),
+          _ptr_of(cache, "length", length, i32, shape),
+          _ptr_of(cache, "token_count", token_count, i32, shape), at,
+          _ptr_of(cache, "mask", mask, torch.int64, (B, T) if stride else (T,)), stride,
+          _ptr_of(cache, "position", position, i32, (B, T)), window, scale, B, T, heads,
+          _ptr_of(cache, "out", out, cache.dtype, full),
+          _ptr_of(cache, "lse", lse, torch.float32, (B, T, heads)),
+          workspace.buffer.data_ptr(), workspace.nbytes)
     return out, lse

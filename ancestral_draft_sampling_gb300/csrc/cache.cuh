@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dspark.h"
+#include "sm100_ptx.cuh"
 
 namespace dspark {
 
@@ -62,6 +63,13 @@ __host__ __device__ __forceinline__ size_t cache_row(const dspark_cache& c,
                                                      int head, int slot) {
   return ((((size_t)plane * c.num_pages + page) * c.kv_heads + head) *
               c.page_size + slot) * ((size_t)c.head_dim * dtype_bytes(c.dtype));
+}
+
+// Every kernel of the cache starts with this: the next one may be set up from
+// now on, and the ones before have finished and their writes are visible.
+__device__ __forceinline__ void follow() {
+  sm100::launch_dependents();
+  sm100::grid_dependency_wait();
 }
 
 // Exclusive sum over the block's threads (a multiple of 32, at most 1024);

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int spli
   const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int token = w / splits, split = w - token * splits;
   if (token >= a.B * a.T) return;
+  follow();
   const Token k = find_token(a, token, lane == 0 && split == 0);
   if (!k.there) return;
   const int sub = lane & (kLanes - 1);
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kThreads) append_row_kernel(AppendArgs a) {
   const long long w = (long long)blockIdx.x * (kThreads / 32) + warp;
   const int token = (int)(w / rows), h = (int)(w - (long long)token * rows);
   if (token >= a.B * a.T) return;
+  follow();
   const Token k = find_token(a, token, lane == 0 && h == 0);
   if (!k.there) return;
   const Row r = find_row(a, k, h);
@@ -313,15 +315,11 @@ cudaError_t launch_lanes(const AppendArgs& a, cudaStream_t stream) {
   const int splits = many ? (loads + 3) / 4 : loads;
   if (tokens * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = (unsigned)((tokens * splits + kThreads / 32 - 1) / (kThreads / 32));
-  if (many && a.interleaved)
-    append_kernel<T, kLanes, 4, true><<<blocks, kThreads, 0, stream>>>(a, splits);
-  else if (many)
-    append_kernel<T, kLanes, 4, false><<<blocks, kThreads, 0, stream>>>(a, splits);
-  else if (a.interleaved)
-    append_kernel<T, kLanes, 1, true><<<blocks, kThreads, 0, stream>>>(a, splits);
-  else
-    append_kernel<T, kLanes, 1, false><<<blocks, kThreads, 0, stream>>>(a, splits);
-  return cudaGetLastError();
+  const auto kernel = many ? (a.interleaved ? append_kernel<T, kLanes, 4, true>
+                                            : append_kernel<T, kLanes, 4, false>)
+                           : (a.interleaved ? append_kernel<T, kLanes, 1, true>
+                                            : append_kernel<T, kLanes, 1, false>);
+  return launch_behind(kernel, blocks, kThreads, 0, stream, a, splits);
 }
 
 template <typename T>
@@ -337,8 +335,7 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
   const long long blocks =
       ((long long)a.B * a.T * (a.heads + 2 * a.c.kv_heads) + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  append_row_kernel<T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_behind(append_row_kernel<T>, (unsigned)blocks, kThreads, 0, stream, a);
 }
 
 }  // namespace

@@ -11,7 +11,7 @@
 
 #include "cache.cuh"
 #include "dspark_common.cuh"
-#include "sm100_ptx.cuh"
+#include "host_util.cuh"
 
 namespace dspark {
 namespace {
@@ -133,6 +133,7 @@ __device__ __forceinline__ int free_pages(const dspark_cache& c) {
 }
 
 __global__ void init_kernel(dspark_cache c) {
+  follow();
   const size_t n = (size_t)gridDim.x * blockDim.x;
   const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
   for (size_t i = i0; i < (size_t)c.max_seqs * c.max_pages; i += n) c.block_table[i] = -1;
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(kBlock, 1)
                    int tokens, int B) {
   __shared__ int need[kMaxB], have[kMaxB], seqs[kMaxB], offset[kMaxB + 1], warps[33];
   const int b = threadIdx.x;
+  follow();
   if (b < B) {
     const int s = cache_seq(c, seq, b), len = length[b];
     int n = 0, h = 0;
@@ -186,6 +188,7 @@ __global__ void __launch_bounds__(kBlock, 1)
   __shared__ GiveList g;
   __shared__ int counts[kMaxB], warps[33];
   const int b = threadIdx.x;
+  follow();
   if (b < B) {
     const int s = cache_seq(c, seq, b);
     if (s < 0) cache_error(c, kCacheErrSeq);
@@ -209,6 +212,7 @@ __global__ void __launch_bounds__(kBlock, 1)
   __shared__ int par[kMaxB], full[kMaxB], need[kMaxB], warps[33];
   int* scratch = c.control + kCtlScratch;
   const int b = threadIdx.x;
+  follow();
   int len = 0, p = -1, s = -1;
   if (b < B) {
     p = cache_seq(c, parent, b);
@@ -294,7 +298,7 @@ constexpr int kCopyThreads = 256, kCopyBatch = 8;
 
 __global__ void __launch_bounds__(kCopyThreads)
     fork_copy_kernel(dspark_cache c, const int32_t* length) {
-  sm100::grid_dependency_wait();
+  follow();
   const int b = blockIdx.y;
   const int from = __ldcg(&c.control[kCtlScratch + 2 * b]);
   const int to = __ldcg(&c.control[kCtlScratch + 2 * b + 1]);
@@ -339,6 +343,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   __shared__ int first_move, last_block;
   int* scratch = c.control + kCtlScratch;
   const int b = blockIdx.y;
+  follow();
   const int s = cache_seq(c, seq, b), len = length[b], acc = accepted[b];
   const long long wanted = acc < 0 ? 0 : (long long)acc + extra;
   const int most = path ? path_width : tokens;
@@ -430,42 +435,28 @@ cudaError_t launch_cache_init(const dspark_cache& c, cudaStream_t stream) {
                           ? (size_t)c.max_seqs * c.max_pages
                           : (size_t)c.num_pages;
   const size_t blocks = (most + 255) / 256;
-  init_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, stream>>>(c);
-  return cudaGetLastError();
+  return launch_behind(init_kernel, (unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, stream, c);
 }
 
 cudaError_t launch_cache_reserve(const dspark_cache& c, const int32_t* seq,
                                  const int32_t* length, int tokens, int B,
                                  cudaStream_t stream) {
-  reserve_kernel<<<1, kBlock, 0, stream>>>(c, seq, length, tokens, B);
-  return cudaGetLastError();
+  return launch_behind(reserve_kernel, 1, kBlock, 0, stream, c, seq, length, tokens, B);
 }
 
 cudaError_t launch_cache_release(const dspark_cache& c, const int32_t* seq,
                                  int B, cudaStream_t stream) {
-  release_kernel<<<1, kBlock, 0, stream>>>(c, seq, B);
-  return cudaGetLastError();
+  return launch_behind(release_kernel, 1, kBlock, 0, stream, c, seq, B);
 }
 
 cudaError_t launch_cache_fork(const dspark_cache& c, const int32_t* parent,
                               const int32_t* child, const int32_t* length,
                               int B, cudaStream_t stream) {
-  fork_kernel<<<1, kBlock, 0, stream>>>(c, parent, child, length, B);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_behind(fork_kernel, 1, kBlock, 0, stream, c, parent, child, length, B);
   if (e != cudaSuccess) return e;
   const int items = 2 * c.layers * c.kv_heads;
   const int blocks = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, B);
-  cfg.blockDim = dim3(kCopyThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fork_copy_kernel, c, length);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_behind(fork_copy_kernel, dim3(blocks, B), kCopyThreads, 0, stream, c, length);
 }
 
 cudaError_t launch_cache_accept(const dspark_cache& c, const int32_t* seq,
@@ -480,9 +471,8 @@ cudaError_t launch_cache_accept(const dspark_cache& c, const int32_t* seq,
     const size_t blocks = (columns + kMoveThreads - 1) / kMoveThreads;
     x = (unsigned)(blocks < 1024 ? blocks : 1024);
   }
-  accept_kernel<<<dim3(x, B), kMoveThreads, 0, stream>>>(
-      c, seq, length, accepted, path, path_width, extra, tokens, B, new_length);
-  return cudaGetLastError();
+  return launch_behind(accept_kernel, dim3(x, B), kMoveThreads, 0, stream, c, seq, length,
+                       accepted, path, path_width, extra, tokens, B, new_length);
 }
 
 }  // namespace dspark

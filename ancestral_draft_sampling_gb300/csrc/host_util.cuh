@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdint>
 #include <mutex>
+#include <utility>
 
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -35,6 +36,26 @@ inline int sm_count() {
 
 inline dspark_status from_cuda(cudaError_t e) {
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+// Launches a kernel that waits for the kernels before it on the device
+// (griddepcontrol.wait before it touches global memory), so that its blocks
+// may be set up while the last of those still runs.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                 cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // The driver's tensor-map encoder, or null where the driver has none.

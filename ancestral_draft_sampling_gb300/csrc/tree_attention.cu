@@ -47,7 +47,7 @@ template <typename T, int ND>
 __global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
     tree_ffma_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ __align__(16) float smem[];
-  __shared__ long long sums[34];
+  __shared__ TreeShare share;
   const int D = a.c.head_dim, DP = D + 4;  // padded rows: lanes on different banks
   float* qs = smem;                        // [kRows][DP], scaled
   float* ks = qs + kRows * DP;             // [kTile][DP]
@@ -57,11 +57,11 @@ __global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
   const T* q = static_cast<const T*>(a.q);
   const T* pool = static_cast<const T*>(a.c.pool);
   float* pw = ps + warp * kTile * 4;
-  sm100::launch_dependents();
-  TreeWalk w = tree_start(a, sums);
+  follow();
+  TreeWalk w = tree_start(a, share);
   if (threadIdx.x == kThreads - 1) tree_describe(a, w);
   bool is_first = true;
-  while (w.next(a)) {
+  for (bool some = w.n > 0; some; some = w.next(a)) {
     const int t0 = w.rt * a.row_tokens;
     const int rows = (w.q.cnt - t0 < a.row_tokens ? w.q.cnt - t0 : a.row_tokens) * a.group;
     const int head0 = w.h * a.group;
@@ -230,7 +230,7 @@ constexpr int kMergeWarps = 4;
 template <typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  sm100::grid_dependency_wait();
+  follow();
   const TreeJoin j = a.join[blockIdx.x + 1];  // nothing cuts the line's start
   const int lane = threadIdx.x & 31, D = a.c.head_dim;
   const int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
@@ -299,8 +299,7 @@ cudaError_t launch_ffma(const TreeArgs& a, size_t smem, cudaStream_t stream) {
                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                          kMaxDynamic);
   });
-  tree_ffma_kernel<T, ND><<<a.blocks, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_behind(tree_ffma_kernel<T, ND>, a.blocks, kThreads, smem, stream, a);
 }
 
 }  // namespace
@@ -327,20 +326,10 @@ cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
 
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream) {
   if (a.blocks < 2) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.blocks - 1, (a.slot_rows + kMergeWarps - 1) / kMergeWarps);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      a.c.dtype == DSPARK_F32
-          ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<float>, a)
-          : cudaLaunchKernelEx(&cfg, tree_merge_kernel<__nv_bfloat16>, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const dim3 grid(a.blocks - 1, (a.slot_rows + kMergeWarps - 1) / kMergeWarps);
+  return launch_behind(a.c.dtype == DSPARK_F32 ? tree_merge_kernel<float>
+                                               : tree_merge_kernel<__nv_bfloat16>,
+                       grid, 32 * kMergeWarps, 0, stream, a);
 }
 
 }  // namespace dspark

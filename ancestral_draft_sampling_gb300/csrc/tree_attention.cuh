@@ -73,18 +73,32 @@ struct TreeSeq {
   int row_tiles;
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
-  TreeSeq r;
+// What is loaded for it, apart from what is made of that: a walk loads the
+// next sequence's numbers while it is still at work on this one.
+struct TreeRaw {
+  int s, len, cnt, held;
+};
+
+__device__ __forceinline__ TreeRaw tree_load(const TreeArgs& a, int b) {
+  TreeRaw r;
   r.s = cache_seq(a.c, a.seq, b);
   r.len = a.length[b];
   r.cnt = a.count ? a.count[b] : a.T;
-  r.cnt = r.cnt < 0 ? 0 : r.cnt > a.T ? a.T : r.cnt;
+  r.held = r.s < 0 ? 0 : a.c.page_count[r.s];
+  return r;
+}
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, const TreeRaw& w, bool report) {
+  TreeSeq r;
+  r.s = w.s;
+  r.len = w.len;
+  r.cnt = w.cnt < 0 ? 0 : w.cnt > a.T ? a.T : w.cnt;
   r.lo = 0;
   r.tiles = 0;
-  r.row_tiles = (r.cnt + a.row_tokens - 1) / a.row_tokens;
+  r.row_tiles = r.cnt <= a.row_tokens ? 1 : (r.cnt + a.row_tokens - 1) / a.row_tokens;
+  const int held = w.held < 0 ? 0 : w.held > a.c.max_pages ? a.c.max_pages : w.held;
   int err = r.s < 0 ? kCacheErrSeq : 0;
-  if (!err && (r.len < 0 || (long long)r.len + r.cnt >
-                                (long long)cache_held(a.c, r.s) * a.c.page_size))
+  if (!err && (r.len < 0 || (long long)r.len + r.cnt > (long long)held * a.c.page_size))
     err = kCacheErrPage;
   if (err) {
     if (report) cache_error(a.c, err);
@@ -92,19 +106,20 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
   }
   if (r.cnt == 0) return r;
   if (a.window > 0 && r.len >= a.window) r.lo = (r.len - a.window + 1) / a.tile;
-  r.tiles = (int)(((long long)r.len + r.cnt + a.tile - 1) / a.tile) - r.lo;
+  r.tiles = (r.len + r.cnt - 1) / a.tile + 1 - r.lo;  // lengths stay below 2^30
   return r;
 }
 
 __device__ __forceinline__ long long tree_work(const TreeArgs& a, const TreeSeq& r) {
-  return (long long)r.tiles * r.row_tiles * a.c.kv_heads;
+  return (long long)(r.row_tiles * a.c.kv_heads) * r.tiles;
 }
 
 // Blocks that have a share, and the share of block c.
 __device__ __forceinline__ long long tree_first(long long W, int G, int c) {
+  if (W < (1 << 23)) return (uint32_t)W * (uint32_t)c / (uint32_t)G;  // c <= 320
   return (W / G) * c + (W % G) * c / G;
 }
-// (W/G) c + floor((W % G) c / G) = floor(W c / G), without overflow.  The
+// The share starts at floor(W c / G) = (W/G) c + floor((W % G) c / G).  The
 // block of tile x: the largest c with floor(W c / G) <= x, found from the
 // quotient and corrected by at most a step or two.
 __device__ __forceinline__ int tree_block_of(long long W, int G, long long x) {
@@ -121,6 +136,7 @@ struct TreeWalk {
   long long base;      // first tile of sequence b
   int b;
   TreeSeq q;
+  TreeRaw ahead;       // of sequence b + 1
   // the current unit
   int h, rt;           // key head and row tile
   int first, n;        // its tiles here: first .. first + n - 1, counted from
@@ -134,13 +150,16 @@ struct TreeWalk {
     while (pos >= base + work) {
       base += work;
       if (++b >= a.B) return false;
-      q = tree_seq(a, b, false);
+      q = tree_seq(a, ahead, false);
+      if (b + 1 < a.B) ahead = tree_load(a, b + 1);
       work = tree_work(a, q);
     }
     const long long at = pos - base;
-    const int unit = (int)(at / q.tiles);
+    int unit;
+    if (at < 0x7fffffffLL) unit = (int)((uint32_t)at / (uint32_t)q.tiles);
+    else unit = (int)(at / q.tiles);
     first = (int)(at - (long long)unit * q.tiles);
-    h = unit / q.row_tiles;
+    h = q.row_tiles == 1 ? unit : unit / q.row_tiles;
     rt = unit - h * q.row_tiles;
     const long long left = end - pos;
     n = q.tiles - first;
@@ -151,49 +170,66 @@ struct TreeWalk {
   }
 };
 
-// Every thread of the block calls this (blockDim.x a multiple of 32, all of
-// `threads` of them): sums the work of the sequences and finds where this
-// block's share starts.  `sums` is shared memory of 34 long longs.
-__device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, long long* sums) {
+// What the threads of a block tell each other when they find its share.
+struct TreeShare {
+  long long sums[32];
+  TreeWalk walk;
+};
+
+// Every thread of the block calls this (blockDim.x a multiple of 32): sums the
+// work of the sequences and finds where this block's share starts.  The walk
+// comes back on its first unit (n = 0: there is none), which one thread finds
+// for all: the first run of any code costs its way from memory.  The block is
+// synchronised twice.
+__device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, TreeShare& sh) {
   const int n = blockDim.x, t = threadIdx.x;
-  const int per = (a.B + n - 1) / n;
+  const int per = (a.B + n - 1) / n;  // sequences of a thread; mostly one
   const int b0 = t * per, b1 = b0 + per < a.B ? b0 + per : a.B;
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tree_work(a, tree_seq(a, b, blockIdx.x == 0));
+  TreeSeq mine{};
+  long long work = 0;
+  for (int b = b0; b < b1; ++b) {
+    const TreeSeq q = tree_seq(a, tree_load(a, b), blockIdx.x == 0);
+    if (b == b0) mine = q;
+    work += tree_work(a, q);
+  }
   const int lane = t & 31, warp = t >> 5;
-  long long x = mine;
+  long long x = work;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long o = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += o;
   }
-  if (lane == 31) sums[warp] = x;
+  if (lane == 31) sh.sums[warp] = x;
   __syncthreads();
-  long long before = 0, W = 0;
+  long long before = x - work, W = 0;
   for (int i = 0; i < n / 32; ++i) {
-    if (i < warp) before += sums[i];
-    W += sums[i];
+    const long long v = sh.sums[i];
+    if (i < warp) before += v;
+    W += v;
   }
-  before += x - mine;
-  __syncthreads();
   const int G = W < a.blocks ? (int)W : a.blocks;
   TreeWalk w;
-  w.pos = w.end = 0;
-  w.base = 0;
-  w.b = 0;
-  w.h = w.rt = w.first = w.n = 0;
-  w.whole = false;
+  w.pos = w.end = w.base = 0;
   w.W = W;
-  if ((int)blockIdx.x < G) {
+  w.b = w.h = w.rt = w.first = w.n = 0;
+  w.whole = false;
+  w.q = TreeSeq{};
+  w.ahead = TreeRaw{};
+  const bool some = (int)blockIdx.x < G;
+  if (some) {
     w.pos = tree_first(W, G, blockIdx.x);
     w.end = tree_first(W, G, blockIdx.x + 1);
-    if (w.pos >= before && w.pos < before + mine) {
+    if (w.pos >= before && w.pos < before + work) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
-        const long long k = tree_work(a, tree_seq(a, b, false));
+        const TreeSeq q = b == b0 ? mine : tree_seq(a, tree_load(a, b), false);
+        const long long k = tree_work(a, q);
         if (w.pos < at + k) {
-          sums[32] = b;
-          sums[33] = at;
+          w.b = b;
+          w.base = at;
+          w.q = q;
+          w.next(a);
+          sh.walk = w;
           break;
         }
         at += k;
@@ -201,23 +237,22 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, long long* sum
     }
   }
   __syncthreads();
-  if ((int)blockIdx.x < G) {
-    w.b = (int)sums[32];
-    w.base = sums[33];
-    w.q = tree_seq(a, w.b, false);
+  if (some) {
+    w = sh.walk;
+    if (w.b + 1 < a.B) w.ahead = tree_load(a, w.b + 1);
   }
   return w;
 }
 
-// One thread of every block, with a walk of its own that has not begun: what
-// this block of the merge has to do.  The share's start cuts a unit when the
+// One thread of every block, with the walk on its first unit: what this block
+// of the merge has to do.  The share's start cuts a unit when the
 // first unit does not begin there; the unit is this block's to join when the
 // share before it holds the unit's beginning.
-__device__ __forceinline__ void tree_describe(const TreeArgs& a, TreeWalk w) {
+__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk& w) {
   TreeJoin j{};
   const int c = blockIdx.x;
-  const long long start = w.pos;
-  if (w.next(a) && w.first > 0) {
+  if (w.n > 0 && w.first > 0) {
+    const long long start = w.pos - w.n;
     const int G = w.W < a.blocks ? (int)w.W : a.blocks;
     const long long us = start - w.first, before = tree_first(w.W, G, c - 1);
     if (before <= us) {

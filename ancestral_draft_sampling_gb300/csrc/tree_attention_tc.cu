@@ -18,16 +18,16 @@
 //
 // Bound by HBM while rows * 4 flops for each key element stay below the
 // tensor cores' rate, that is up to about 285 rows a key head; the layout
-// follows from that: one block a multiprocessor, keys and values in a ring of
+// follows from that: one block a multiprocessor, keys and values in rings of
 // 32 KB (16 KB) tiles that TMA fills straight from the pages, up to 192 KB in
 // flight, which covers the latency of HBM several times over.
-//   warp 0       fills the ring: each lane copies one page's rows of one half
-//                of the head (64 values, 128-byte swizzle), and looks up its
-//                page of the next tile meanwhile.
-//   warp 1       one thread issues the products.
+//   warps 0, 3   fill the rings of keys and of values, a copy for each page's
+//                rows and each half of the head (64 values, 128-byte swizzle);
+//                the page numbers come 32 at a time, one load ahead.
+//   warp 1       issues the products.
 //   warp 2       loads a unit's queries (TMA, rows (token, head) of the key
-//                head), once the last unit's scores are done.
-//   warp 3       tells the merge what to do.
+//                head), once the last unit's scores are done, and tells the
+//                merge what to do.
 //   warps 4..7, 8..11  the streams' softmax: rows 32 (w % 4) .. + 31.
 // Tiles that some rows see and others do not (the drafted tokens, a window's
 // edge, the sequence's end) may hold NaN or infinities in places that weigh
@@ -59,20 +59,20 @@ template <int D>
 struct Shape {
   static constexpr int halves = D / 64;
   static constexpr int tile_bytes = halves * kHalfBytes;
-  static constexpr int tiles = D == 128 ? 7 : 13;  // queries (1 or 2) and ring
+  static constexpr int tiles = D == 128 ? 7 : 13;  // queries (1 or 2) and rings
   static constexpr uint32_t s_col(uint32_t i) { return 128 * i; }
   static constexpr uint32_t o_col(uint32_t i) { return 256 + D * i; }
 };
 
 struct Control {  // shared memory behind the tiles
-  uint64_t kv_full[12], kv_empty[12];
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t q_full, q_empty, drain, v_all, b_done;
   uint64_t s_full[2], p_ready[2], pv_done[2], v_sync[2];  // of each stream
   // sums have been read: by the first stream at the end of every unit (both
   // streams' where it joins them), by the second where it has rows of its own.
   // Nobody arrives without work in the unit, so no phase is run ahead of.
   uint64_t o_free[2];
-  long long sums[34];
+  TreeShare share;
   uint32_t bad[2][4];     // rows of a value tile that hold NaN or infinities
   uint32_t add_first[2];  // the unit's first product adds to O
   float2 b_stats[128];    // the second stream's maximum and sum of each row
@@ -155,6 +155,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       I8(8), I8(16), I8(24), "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::I8(0),
+      I8(8), "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t at) {
   uint32_t x;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(at) : "memory");
@@ -216,76 +223,186 @@ struct TcArgs {
   int fit;        // drafted tokens of a stream's 128 rows
   int q_tokens;   // drafted tokens of a query copy
   int q_tiles;    // query tiles of a unit: 2 where units have more than 128 rows
-  int slots;      // tiles of the ring
+  int k_slots, v_slots;  // tiles of the rings
+  int page_shift;        // log2 of the page size
+  int out32;             // out is aligned to 32 bytes
 };
 
-// Position in the ring of tile n's keys and values, of N tiles: keys run two
-// tiles ahead of values.
-__device__ __forceinline__ int k_at(int n) { return n == 0 ? 0 : 2 * n - 1; }
-__device__ __forceinline__ int v_at(int n, int N) { return (n + 2 < N ? n + 2 : N) + n; }
-
-// A role's view of the ring: the slot and the phase parity of an entry.
-struct Entry {
+// A role's place in a ring: the slot, and the parity of its phase.
+struct Place {
   int slot;
   uint32_t parity;
-};
-__device__ __forceinline__ Entry entry(int e, int slots) {
-  const int round = e / slots;
-  return {e - round * slots, (uint32_t)round & 1u};
-}
-
-// The largest (c >= 0) or smallest (c < 0) of n scores of the row that the
-// thread holds, from tensor memory; hidden ones (see) do not count.
-template <bool kMasked, bool kLeast>
-__device__ __forceinline__ float extreme(uint32_t at, const uint32_t (&see)[4]) {
-  float top[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top[i] = kLeast ? INFINITY : -INFINITY;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t x[64];
-    tmem_ld32(at + 64 * h, x);
-    tmem_ld32(at + 64 * h + 32, x + 32);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      float v = __uint_as_float(x[i]);
-      if (kMasked && !((see[2 * h + i / 32] >> (i % 32)) & 1)) v = kLeast ? INFINITY : -INFINITY;
-      top[i & 3] = kLeast ? fminf(top[i & 3], v) : fmaxf(top[i & 3], v);
+  __device__ __forceinline__ void step(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      parity ^= 1;
     }
   }
-  return kLeast ? fminf(fminf(top[0], top[1]), fminf(top[2], top[3]))
-                : fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 32 bytes in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// What hides keys from a row: see seen32.
+struct Sight {
+  int lo, len;
+  uint64_t bits;
+};
+
+// The largest (c >= 0) or smallest (c < 0) score of the row that the thread
+// holds, from tensor memory; hidden ones do not count.  A loop over quarters of
+// the row, the next one loaded meanwhile: unrolled code is slow the first
+// time, when it comes from memory (20 cycles an instruction), and a block runs
+// a few dozen tiles.
+template <bool kMasked>
+__device__ __forceinline__ float extreme(uint32_t at, bool least, int j, const Sight& see) {
+  float top[2] = {-INFINITY, -INFINITY};
+  uint32_t x[32], ahead[32];
+  tmem_ld32(at, x);
+  tmem_ld_wait();
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    tmem_ld32(at + 32 * ((h + 1) & 3), ahead);
+    uint32_t w = ~0u;
+    if (kMasked) w = seen32(j + 32 * h, see.lo, see.len, see.bits);
+    if (least) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] ^= 0x80000000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float v = __uint_as_float(x[i]);
+      if (kMasked && !((w >> i) & 1)) v = -INFINITY;
+      top[i & 1] = fmaxf(top[i & 1], v);
+    }
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = ahead[i];
+  }
+  const float best = fmaxf(top[0], top[1]);
+  return least ? -best : best;
 }
 
 // Weights 2^(c s - base) over the scores, in bfloat16; their float32 sum.
 template <bool kMasked>
-__device__ __forceinline__ float weigh(uint32_t at, float c, float base, const uint32_t (&see)[4]) {
+__device__ __forceinline__ float weigh(uint32_t at, float c, float base, int j, const Sight& see) {
   const uint64_t cc = pair(c, c), bb = pair(-base, -base);
   uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+  uint32_t x[32], ahead[32];
+  tmem_ld32(at, x);
+  tmem_ld_wait();
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    tmem_ld32(at + 32 * ((h + 1) & 3), ahead);
+    uint32_t w = ~0u;
+    if (kMasked) w = seen32(j + 32 * h, see.lo, see.len, see.bits);
+    uint32_t p[16];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t x[64];
-    tmem_ld32(at + 64 * h, x);
-    tmem_ld32(at + 64 * h + 32, x + 32);
-    tmem_ld_wait();
-    uint32_t p[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float2 y = unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, bb));
       float p0 = ex2(y.x), p1 = ex2(y.y);
       if (kMasked) {
-        const uint32_t w = see[2 * h + i / 16] >> (2 * i % 32);
-        p0 = w & 1 ? p0 : 0.0f;
-        p1 = w & 2 ? p1 : 0.0f;
+        p0 = (w >> (2 * i)) & 1 ? p0 : 0.0f;
+        p1 = (w >> (2 * i)) & 2 ? p1 : 0.0f;
       }
       sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
       p[i] = pack_bf16(p0, p1);
     }
-    tmem_st32(at + 32 * h, p);  // over scores that have been read
+    tmem_ld_wait();
+    tmem_st16(at + 16 * h, p);  // over scores that have been read
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = ahead[i];
   }
   const float2 t = unpair(add2(sum[0], sum[1]));
   return t.x + t.y;
+}
+
+// The tiles of a ring, from the walk to the copies: the page numbers of a
+// unit's tiles 32 at a time, the first of the next unit's loaded while this
+// one's are used.
+struct Pages {
+  const int32_t* row;  // of the block table
+  int h, n;            // key head and tiles
+  int key;             // first key
+  int last;            // last page that holds a key of the sequence
+  int ids, first;      // lane l: page first + l, or the place behind the pool
+
+  __device__ __forceinline__ int load(const TcArgs& P, int page) const {
+    if (page > last) return P.a.c.num_pages;
+    const int id = row[page];
+    if (id >= 0 && id < P.a.c.num_pages) return id;
+    cache_error(P.a.c, kCacheErrPage);
+    return P.a.c.num_pages;
+  }
+  __device__ __forceinline__ void set(const TcArgs& P, const TreeWalk& w, int lane) {
+    row = P.a.c.block_table + (size_t)w.q.s * P.a.c.max_pages;
+    h = w.h;
+    n = w.n;
+    key = (w.q.lo + w.first) * kTile;
+    last = (w.q.len + w.q.cnt - 1) >> P.page_shift;
+    first = key >> P.page_shift;
+    ids = load(P, first + lane);
+  }
+};
+
+template <int D>
+__device__ __forceinline__ bool fill_ring(const TcArgs& P, TreeWalk& w, const CUtensorMap* map,
+                                          uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                          int slots, int lane) {
+  using S = Shape<D>;
+  Place at{0, 1};  // the phase that frees a slot: the first round passes
+  int filled = 0;
+  bool ok = true;
+  // each lane copies one page's rows of one half of the head
+  const int half = lane / P.pages, part = lane - half * P.pages;
+  const bool mine = half < S::halves;
+  uint8_t* const to = ring + half * kHalfBytes + part * P.page_rows * 128;
+  Pages next{}, cur{};
+  bool some = w.n > 0;
+  if (some) next.set(P, w, lane);
+  while (some && ok) {
+    cur = next;
+    int ids2 = cur.load(P, cur.first + 32 + lane);
+    for (int i = 0; i < cur.n; ++i) {
+      const int j = cur.key + i * kTile, page = j >> P.page_shift;
+      if (page >= cur.first + 32) {
+        cur.first += 32;
+        cur.ids = ids2;
+        ids2 = cur.load(P, cur.first + 32 + lane);
+      }
+      ok = wait_warp(&empty[at.slot], at.parity);
+      if (!ok) break;
+      const int id = __shfl_sync(0xffffffffu, cur.ids, (page - cur.first + part) & 31);
+      if (lane == 0) mbar_arrive_expect_tx(&full[at.slot], S::tile_bytes);
+      __syncwarp();
+      if (mine)
+        tma_4d(to + at.slot * S::tile_bytes, map, &full[at.slot], half * 64,
+               j & ((1 << P.page_shift) - 1), cur.h, id);
+      at.step(slots);
+      ++filled;
+      if (i == 0) {  // the next unit, while this one's copies are under way
+        some = w.next(P.a);
+        if (some) next.set(P, w, lane);
+      }
+    }
+  }
+  if (!ok) {  // copies that nobody waited for land before the block ends
+    for (int e = filled > slots ? filled - slots : 0; e < filled; ++e)
+      mbar_wait(&full[e % slots], (e / slots) & 1, kSpin >> 4);
+  }
+  return ok;
 }
 
 template <int D>
@@ -296,16 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   extern __shared__ uint8_t raw[];
   uint8_t* q_tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint8_t* ring = q_tile + P.q_tiles * S::tile_bytes;
+  uint8_t* k_ring = q_tile + P.q_tiles * S::tile_bytes;
+  uint8_t* v_ring = k_ring + P.k_slots * S::tile_bytes;
   Control& sh = *reinterpret_cast<Control*>(q_tile + S::tiles * S::tile_bytes);
   const TreeArgs& a = P.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slots = P.slots;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < slots; ++i) {
-      mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 1);
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
@@ -324,174 +443,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 3) {
+  if (warp == 2) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
-  TreeWalk w = tree_start(a, sh.sums);  // synchronises the block
+  follow();
   tc_fence_before();
-  __syncthreads();
+  TreeWalk w = tree_start(a, sh.share);  // synchronises the block
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int N = (int)(w.end - w.pos);  // tiles of this block
   bool ok = true;
 
   if (warp == 0) {
-    // ------------------------------------------------- keys and values
-    const int half = lane / P.pages, part = lane - half * P.pages;
-    const bool mine = half < S::halves;
-    int at = 0, slot = 0;       // entries of the ring filled so far, the next one's slot
-    uint32_t parity = 1;        // of the phase that frees it: the first round passes
-    struct Where { int h, id, y; };
-    // the lane's page of the tile that starts with key j
-    auto look_up = [&](int j) {
-      j += part * P.page_rows;
-      Where t{w.h, a.c.num_pages, j % a.c.page_size};
-      if (mine && j < w.q.len + w.q.cnt) {
-        const int id = cache_page(a.c, w.q.s, j / a.c.page_size, a.c.max_pages);
-        if (id >= 0) t.id = id;
-        else cache_error(a.c, kCacheErrPage);
-      }
-      return t;  // no page: a place behind the pool, which reads as zeros
-    };
-    auto fill = [&](const CUtensorMap* map, const Where& t) {
-      ok = wait_warp(&sh.kv_empty[slot], parity);
-      if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], S::tile_bytes);
-      __syncwarp();
-      if (mine)
-        tma_4d(ring + slot * S::tile_bytes + half * kHalfBytes + part * P.page_rows * 128, map,
-               &sh.kv_full[slot], half * 64, t.y, t.h, t.id);
-      ++at;
-      if (++slot == slots) {
-        slot = 0;
-        parity ^= 1;
-      }
-    };
-    bool some = w.next(a);
-    int i = 0;
-    Where t0{0, 0, 0}, t1{0, 0, 0}, t2{0, 0, 0};  // tiles n, n - 1 and the next
-    if (some) t2 = look_up((w.q.lo + w.first) * kTile);
-    // keys 0, 1, then values n - 2 (n >= 2) before keys n: v_at and k_at
-    for (int n = 0; n < N && ok; ++n) {
-      const Where old = t1;
-      t1 = t0;
-      t0 = t2;
-      if (++i >= w.n) {  // the next tile's page, before this one's copies wait
-        i = 0;
-        some = w.next(a);
-      }
-      if (some) t2 = look_up((w.q.lo + w.first + i) * kTile);
-      if (n >= 2) fill(&map_v, old);
-      if (ok) fill(&map_k, t0);
-    }
-    if (N > 1 && ok) fill(&map_v, t1);
-    if (N > 0 && ok) fill(&map_v, t0);
-    if (!ok) {  // copies that nobody waited for land before the block ends
-      for (int e = at > slots ? at - slots : 0; e < at; ++e) {
-        const Entry f = entry(e, slots);
-        mbar_wait(&sh.kv_full[f.slot], f.parity, kSpin >> 4);
-      }
-    }
+    ok = fill_ring<D>(P, w, &map_k, k_ring, sh.k_full, sh.k_empty, P.k_slots, lane);
+  } else if (warp == 3) {
+    ok = fill_ring<D>(P, w, &map_v, v_ring, sh.v_full, sh.v_empty, P.v_slots, lane);
   } else if (warp == 1) {
     // -------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
-      const uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
-      const uint32_t q_base = smem_u32(q_tile), ring_base = smem_u32(ring);
-      int g = 0;                     // tiles of the units before
-      uint32_t halved = 0, freed = 0;  // units that gave each stream half the rows
-      uint32_t used[2] = {0, 0};     // tiles that a stream has weighed
-      Entry k{0, 0};
-      // scores of the keys in k for a stream, from its query tile
-      auto scores = [&](int st, int tile) {
-        const uint32_t k_base = ring_base + k.slot * S::tile_bytes;
-        const uint32_t q_at = q_base + tile * S::tile_bytes;
+    // The whole warp runs this, so that descriptors stay in uniform
+    // registers; one thread issues (issued from a single thread's code, each
+    // product took 100 cycles to set up and bounded wide trees).
+    const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+    const uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
+    // keys and queries: rows of 128 bytes, 8-row groups 1024 bytes apart;
+    // values: 64-wide halves kHalfBytes apart, 8-key groups 1024 bytes apart
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile), 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(k_ring), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(v_ring), kHalfBytes, 1024);
+    uint32_t halved = 0, freed = 0;  // units that gave each stream half the rows
+    uint32_t used[2] = {0, 0};       // tiles that a stream has weighed
+    Place k{0, 0}, v{0, 0};
+    // scores of the keys in k for a stream, from its query tile
+    auto scores = [&](int st, int tile, bool free_keys, bool free_queries) {
+      const uint64_t qd = q_desc + tile * (S::tile_bytes >> 4);
+      const uint64_t kd = k_desc + k.slot * (S::tile_bytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i >> 2) * kHalfBytes + (i & 3) * 32;
-          mma_bf16(tmem + S::s_col(st), smem_desc_sw128(q_at + off, 16, 1024),
-                   smem_desc_sw128(k_base + off, 16, 1024), idesc_s, i != 0);
+          const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
+          mma_bf16(tmem + S::s_col(st), qd + off, kd + off, idesc_s, i != 0);
         }
         mma_commit(&sh.s_full[st]);
-      };
-      auto keys = [&](int n) {
-        k = entry(k_at(n), slots);
-        ok = ok && wait(&sh.kv_full[k.slot], k.parity);
-        tc_fence_after();
-      };
-      auto sums = [&](int st, const Entry& v, bool first) {
-        ok = ok && wait(&sh.p_ready[st], used[st]++ & 1);
-        if (!ok) return;
-        tc_fence_after();
-        const bool add = !first || *(volatile uint32_t*)&sh.add_first[st];
-        const uint32_t v_base = ring_base + v.slot * S::tile_bytes;
+        if (free_keys) mma_commit(&sh.k_empty[k.slot]);
+        if (free_queries) mma_commit(&sh.q_empty);
+      }
+      if (free_keys) k.step(P.k_slots);
+    };
+    auto keys = [&]() {
+      ok = ok && wait_warp(&sh.k_full[k.slot], k.parity);
+      tc_fence_after();
+    };
+    auto sums = [&](int st, bool first, bool free_values) {
+      ok = ok && wait_warp(&sh.p_ready[st], used[st]++ & 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t add = !first || *(volatile uint32_t*)&sh.add_first[st];
+      const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
-          mma_bf16_ta(tmem + S::o_col(st), tmem + S::s_col(st) + 8 * i,
-                      smem_desc_sw128(v_base + i * 2048, kHalfBytes, 1024), idesc_o, add || i != 0);
+          mma_bf16_ta(tmem + S::o_col(st), tmem + S::s_col(st) + 8 * i, vd + i * (2048 >> 4),
+                      idesc_o, i != 0 ? 1u : add);
         mma_commit(&sh.pv_done[st]);
-      };
-      for (int unit = 0; ok && w.next(a); ++unit, g += w.n) {
-        ok = wait(&sh.q_full, unit & 1);
-        const bool both = w.q.cnt - w.rt * a.row_tokens > P.fit;
-        if (ok) keys(g);
+        if (free_values) mma_commit(&sh.v_empty[v.slot]);
+      }
+    };
+    bool some = w.n > 0;
+    for (int unit = 0; ok && some; ++unit, some = w.next(a)) {
+      ok = wait_warp(&sh.q_full, unit & 1);
+      const bool both = w.q.cnt - w.rt * a.row_tokens > P.fit;
+      if (ok) keys();
+      if (!ok) break;
+      scores(0, 0, !both, w.n == 1 && !both);
+      if (both) {
+        scores(1, 1, true, w.n == 1);
+      } else if (w.n > 1) {
+        keys();
         if (!ok) break;
-        scores(0, 0);
-        if (both) scores(1, 1);
-        mma_commit(&sh.kv_empty[k.slot]);
-        if (!both && w.n > 1) {
-          keys(g + 1);
-          if (!ok) break;
-          scores(1, 0);
-          mma_commit(&sh.kv_empty[k.slot]);
-        }
-        if (w.n <= (both ? 1 : 2)) mma_commit(&sh.q_empty);
-        if (unit > 0) ok = wait(&sh.o_free[0], (unit - 1) & 1);
-        if (freed < halved) ok = ok && wait(&sh.o_free[1], freed++ & 1);
-        halved += both;
-        for (int i = 0; i < w.n && ok; ++i) {
-          const Entry v = entry(v_at(g + i, N), slots);
-          ok = wait(&sh.kv_full[v.slot], v.parity);
-          if (both) {
-            const bool more = i + 1 < w.n;
-            sums(0, v, i == 0);
-            if (more && ok) {
-              keys(g + i + 1);
-              if (ok) scores(0, 0);
-            }
-            if (ok) sums(1, v, i == 0);
-            if (!ok) break;
-            mma_commit(&sh.kv_empty[v.slot]);
-            if (more) {
-              scores(1, 1);
-              mma_commit(&sh.kv_empty[k.slot]);
-              if (i + 2 == w.n) mma_commit(&sh.q_empty);
-            }
-          } else {
-            if (ok) sums(i & 1, v, i < 2);
-            if (!ok) break;
-            mma_commit(&sh.kv_empty[v.slot]);
-            if (i + 2 < w.n) {
-              keys(g + i + 2);
-              if (!ok) break;
-              scores(i & 1, 0);
-              mma_commit(&sh.kv_empty[k.slot]);
-              if (i + 3 == w.n) mma_commit(&sh.q_empty);
-            }
+        scores(1, 0, true, w.n == 2);
+      }
+      if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
+      if (freed < halved) ok = ok && wait_warp(&sh.o_free[1], freed++ & 1);
+      halved += both;
+      for (int i = 0; i < w.n && ok; ++i) {
+        ok = wait_warp(&sh.v_full[v.slot], v.parity);
+        if (both) {
+          const bool more = i + 1 < w.n;
+          if (ok) sums(0, i == 0, false);
+          if (more && ok) {
+            keys();
+            if (ok) scores(0, 0, false, false);
+          }
+          if (ok) sums(1, i == 0, true);
+          if (more && ok) scores(1, 1, true, i + 2 == w.n);
+        } else {
+          if (ok) sums(i & 1, i < 2, true);
+          if (ok && i + 2 < w.n) {
+            keys();
+            if (ok) scores(i & 1, 0, true, i + 3 == w.n);
           }
         }
+        v.step(P.v_slots);
       }
-      if (!ok) {
-        mma_commit(&sh.drain);
-        mbar_wait(&sh.drain, 0, kSpin >> 4);
-      }
+    }
+    if (!ok) {
+      if (elect_one()) mma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0, kSpin >> 4);
     }
   } else if (warp == 2) {
     // --------------------------------------------------------- queries
     if (lane == 0) {
       int unit = 0;
-      for (; ok && w.next(a); ++unit) {
+      for (bool some = w.n > 0; ok && some; ++unit, some = w.next(a)) {
         if (unit > 0) ok = wait(&sh.q_empty, (unit - 1) & 1);
         if (!ok) break;
         const int t0 = w.rt * a.row_tokens;
@@ -502,11 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_5d(q_tile + i * kHalfBytes, &map_q, &sh.q_full, half * 64, 0, w.h,
                  t0 + tile * P.fit, w.b);
         }
+        if (unit == 0) tree_describe(a, w);
       }
+      if (unit == 0) tree_describe(a, w);
       if (!ok && unit > 0) mbar_wait(&sh.q_full, (unit - 1) & 1, kSpin >> 4);
     }
-  } else if (warp == 3) {
-    if (lane == 0) tree_describe(a, w);
   } else {
     // --------------------------------------------------------- softmax
     const int st = warp >= 8, quarter = warp & 3, r = quarter * 32 + lane;
@@ -516,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;                       // tiles of the units before
     uint32_t used = 0, syncs = 0, alls = 0, joins = 0;  // phases of the barriers
     bool is_first = true;            // the block's first unit
-    for (; ok && w.next(a); g += w.n) {
+    bool some = w.n > 0;
+    for (; ok && some; g += w.n, some = w.next(a)) {
       const int t_unit = w.rt * a.row_tokens, left = w.q.cnt - t_unit;
       const bool both = left > P.fit;             // half the rows each
       const int t0 = t_unit + (both && st ? P.fit : 0);
@@ -526,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = r < rows, any = quarter * 32 < rows;
       const uint64_t bits = valid ? tree_mask(a, w.b, t, w.q.cnt) : 0;
       const int len = w.q.len;
-      const int lo = valid ? tree_window_lo(a, w.b, t, len) : 0;
+      const Sight sight{valid ? tree_window_lo(a, w.b, t, len) : 0, len, bits};
       int lo_most = 0;  // committed keys below this are hidden from some row
       if (a.window > 0) {
         for (int i = lane; i < left && i < a.row_tokens; i += 32) {
@@ -543,17 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_warp(&sh.s_full[st], used & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         if (any) {
-          float best;
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) see[i] = seen32(j0 + 32 * i, lo, len, bits);
-            best = c < 0.0f ? extreme<true, true>(s_at, see) : extreme<true, false>(s_at, see);
-          } else {
-            best = c < 0.0f ? extreme<false, true>(s_at, see) : extreme<false, false>(s_at, see);
-          }
-          best *= c;
+          const float best = c * (masked ? extreme<true>(s_at, c < 0.0f, j0, sight)
+                                         : extreme<false>(s_at, c < 0.0f, j0, sight));
           const bool raise = valid && best > m + kRaise;  // m = -inf: any maximum
           if (__any_sync(0xffffffffu, raise)) {
             const float now = raise ? best : m;
@@ -573,15 +629,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = now;
           }
           const float base = m == -INFINITY ? 0.0f : m;
-          l += masked ? weigh<true>(s_at, c, base, see) : weigh<false>(s_at, c, base, see);
+          l += masked ? weigh<true>(s_at, c, base, j0, sight) : weigh<false>(s_at, c, base, j0, sight);
           tmem_st_wait();
         }
         uint32_t found = 0;
         if (masked) {
           // the tile's values: this thread looks through key j0 + r's
-          const Entry e = entry(v_at(g + tile, N), slots);
-          uint8_t* v = ring + e.slot * S::tile_bytes;
-          ok = wait_warp(&sh.kv_full[e.slot], e.parity);
+          const int round = (g + tile) / P.v_slots, slot = g + tile - round * P.v_slots;
+          uint8_t* v = v_ring + slot * S::tile_bytes;
+          ok = wait_warp(&sh.v_full[slot], round & 1);
           if (!ok) break;
           uint32_t worst = 0;
 #pragma unroll
@@ -618,8 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t pp = tmem_ld1(s_at + (j >> 1));
                 tmem_ld_wait();
                 const float p = __uint_as_float(j & 1 ? pp & 0xffff0000u : pp << 16);
-                const uint32_t sw = j < 64 ? (j < 32 ? see[0] : see[1]) : (j < 96 ? see[2] : see[3]);
-                const bool sees = (sw >> (j & 31)) & 1;
+                const bool sees = seen32(j0 + j, sight.lo, sight.len, sight.bits) & 1;
                 for (int d = 0; d < D; ++d) {
                   const uint16_t u = *reinterpret_cast<const uint16_t*>(
                       v + (d >> 6) * kHalfBytes + j * 128 + ((((d & 63) >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
@@ -710,21 +765,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
             }
             if (valid && w.whole) {
-              uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * i);
+              char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * i);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t p[4];
+              for (int k = 0; k < 2; ++k) {
+                uint32_t p[8];
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                  p[d] = pack_bf16(__uint_as_float(o[8 * k + 2 * d]) * inv,
-                                   __uint_as_float(o[8 * k + 2 * d + 1]) * inv);
-                to[k] = make_uint4(p[0], p[1], p[2], p[3]);
+                for (int d = 0; d < 8; ++d)
+                  p[d] = pack_bf16(__uint_as_float(o[16 * k + 2 * d]) * inv,
+                                   __uint_as_float(o[16 * k + 2 * d + 1]) * inv);
+                if (P.out32) {
+                  store32(to + 32 * k, p);
+                } else {
+                  reinterpret_cast<uint4*>(to)[2 * k] = make_uint4(p[0], p[1], p[2], p[3]);
+                  reinterpret_cast<uint4*>(to)[2 * k + 1] = make_uint4(p[4], p[5], p[6], p[7]);
+                }
               }
             } else if (valid) {
-              uint4* to = reinterpret_cast<uint4*>(tree_part(a, slot) + (size_t)part_row * D + 32 * i);
+              float* to = tree_part(a, slot) + (size_t)part_row * D + 32 * i;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t p[8];
+#pragma unroll
+                for (int d = 0; d < 8; ++d) p[d] = o[8 * k + d];
+                store32(to + 8 * k, p);
+              }
             }
           }
           if (valid) {
@@ -746,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok) sh.failed = 1;
   tc_fence_before();
   __syncthreads();
-  if (warp == 3) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -775,7 +839,11 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   P.fit = kTreeRows / a.group;
   P.q_tokens = a.T < P.fit ? a.T : P.fit;
   P.q_tiles = a.T > P.fit ? 2 : 1;
-  P.slots = Shape<D>::tiles - P.q_tiles;
+  const int slots = Shape<D>::tiles - P.q_tiles;
+  P.v_slots = slots / 2;
+  P.k_slots = slots - P.v_slots;
+  while ((1 << P.page_shift) < a.c.page_size) ++P.page_shift;
+  P.out32 = aligned_to(a.out, 32);
   CUtensorMap mq, mk, mv;
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   {
@@ -801,8 +869,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  tree_tc_kernel<D><<<a.blocks, kThreads, smem_bytes<D>(), stream>>>(P, mq, mk, mv);
-  return cudaGetLastError();
+  return launch_behind(tree_tc_kernel<D>, a.blocks, kThreads, smem_bytes<D>(), stream, P, mq, mk, mv);
 }
 
 }  // namespace
