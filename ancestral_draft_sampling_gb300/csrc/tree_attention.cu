@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
 // Joins the partial results of the units that several blocks worked on: a
 // warp for each row, o = sum_c e^(m_c - M) o_c / sum_c e^(m_c - M) l_c over
 // the unit's blocks c in order, M the largest m_c.
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 4, kMergeBatch = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -253,20 +253,30 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       if (M == -INFINITY) wt = 0.0f;
       lw = wt * st[1];
     }
-    for (int i = 0; i < n; ++i) {
-      const int c = cb + i;
-      const float wi = __shfl_sync(0xffffffffu, wt, i);
-      L += __shfl_sync(0xffffffffu, lw, i);
-      const float* part = tree_part(a, c == c0 ? slot0 : 2 * c) + (size_t)r * D;
+    for (int i0 = 0; i0 < n; i0 += kMergeBatch) {  // loads of a batch in flight
+      float4 x[kMergeBatch][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int d = k * 128 + lane * 4;
-        if (d < D) {
-          const float4 x = load4(part + d);
-          o[k].x = fmaf(wi, x.x, o[k].x);
-          o[k].y = fmaf(wi, x.y, o[k].y);
-          o[k].z = fmaf(wi, x.z, o[k].z);
-          o[k].w = fmaf(wi, x.w, o[k].w);
+      for (int i = 0; i < kMergeBatch; ++i) {
+        const int c = cb + i0 + i;
+        const float* part = tree_part(a, c == c0 ? slot0 : 2 * c) + (size_t)r * D;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int d = k * 128 + lane * 4;
+          x[i][k] = make_float4(0, 0, 0, 0);
+          if (i0 + i < n && d < D) x[i][k] = load4(part + d);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kMergeBatch; ++i) {
+        if (i0 + i >= n) break;
+        const float wi = __shfl_sync(0xffffffffu, wt, i0 + i);
+        L += __shfl_sync(0xffffffffu, lw, i0 + i);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          o[k].x = fmaf(wi, x[i][k].x, o[k].x);
+          o[k].y = fmaf(wi, x[i][k].y, o[k].y);
+          o[k].z = fmaf(wi, x[i][k].z, o[k].z);
+          o[k].w = fmaf(wi, x[i][k].w, o[k].w);
         }
       }
     }

@@ -38,6 +38,8 @@
 // Every wait is bounded; where one runs out the kernel sets the error word,
 // waits (bounded) for its copies and products, frees its tensor memory and
 // returns.
+#include <cstddef>
+
 #include "dspark_common.cuh"
 #include "host_util.cuh"
 #include "sm100_ptx.cuh"
@@ -62,12 +64,20 @@ struct Shape {
   static constexpr int tiles = D == 128 ? 7 : 13;  // queries (1 or 2) and rings
   static constexpr uint32_t s_col(uint32_t i) { return 128 * i; }
   static constexpr uint32_t o_col(uint32_t i) { return 256 + D * i; }
+  // Weights lie over the scores they come from, or, where tensor memory has
+  // the room, apart: the next scores then need not wait for their product.
+  static constexpr bool apart = D == 64;
+  static constexpr uint32_t p_col(uint32_t i) { return apart ? 384 + 64 * i : s_col(i); }
 };
 
 struct Control {  // shared memory behind the tiles
+  // barriers: one arrival completes a phase of the first 31, four (a stream's
+  // warps) one of those behind but v_all, which takes eight
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t q_full, q_empty, drain, v_all, b_done;
-  uint64_t s_full[2], p_ready[2], pv_done[2], v_sync[2];  // of each stream
+  uint64_t q_full, q_empty, drain;
+  uint64_t s_full[2], pv_done[2];  // of each stream
+  uint64_t v_all, b_done;
+  uint64_t p_ready[2], v_sync[2];  // of each stream
   // sums have been read: by the first stream at the end of every unit (both
   // streams' where it joins them), by the second where it has rows of its own.
   // Nobody arrives without work in the unit, so no phase is run ahead of.
@@ -147,20 +157,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
       : "r"(at)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::I8(0),
-      I8(8), I8(16), I8(24), "r"(at)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::I8(0),
       I8(8), "r"(at)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : R8(0)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::I8(0),
+               "r"(at)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t at) {
   uint32_t x;
@@ -262,21 +276,17 @@ struct Sight {
 };
 
 // The largest (c >= 0) or smallest (c < 0) score of the row that the thread
-// holds, from tensor memory; hidden ones do not count.  A loop over quarters of
-// the row, the next one loaded meanwhile: unrolled code is slow the first
-// time, when it comes from memory (20 cycles an instruction), and a block runs
-// a few dozen tiles.
-template <bool kMasked>
-__device__ __forceinline__ float extreme(uint32_t at, bool least, int j, const Sight& see) {
+// holds, from tensor memory; hidden ones do not count.  Loops over parts of the
+// row: code is slow the first time, when it comes from memory (20 cycles an
+// instruction measured), and a block runs a few dozen tiles.
+__device__ __forceinline__ float extreme_seen(uint32_t at, bool least, int j, const Sight& see) {
   float top[2] = {-INFINITY, -INFINITY};
-  uint32_t x[32], ahead[32];
-  tmem_ld32(at, x);
-  tmem_ld_wait();
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
-    tmem_ld32(at + 32 * ((h + 1) & 3), ahead);
-    uint32_t w = ~0u;
-    if (kMasked) w = seen32(j + 32 * h, see.lo, see.len, see.bits);
+    uint32_t x[32];
+    tmem_ld32(at + 32 * h, x);
+    const uint32_t w = seen32(j + 32 * h, see.lo, see.len, see.bits);
+    tmem_ld_wait();
     if (least) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] ^= 0x80000000u;
@@ -284,46 +294,82 @@ __device__ __forceinline__ float extreme(uint32_t at, bool least, int j, const S
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float v = __uint_as_float(x[i]);
-      if (kMasked && !((w >> i) & 1)) v = -INFINITY;
+      if (!((w >> i) & 1)) v = -INFINITY;
       top[i & 1] = fmaxf(top[i & 1], v);
     }
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = ahead[i];
   }
   const float best = fmaxf(top[0], top[1]);
   return least ? -best : best;
 }
 
-// Weights 2^(c s - base) over the scores, in bfloat16; their float32 sum.
+// Weights 2^(c s - base) of 32 scores, in bfloat16 to tensor memory; adds them
+// to the sums in float32.  Hidden ones (0 in see) weigh nothing.
 template <bool kMasked>
-__device__ __forceinline__ float weigh(uint32_t at, float c, float base, int j, const Sight& see) {
+__device__ __forceinline__ void weigh32(uint32_t to, const uint32_t* x, uint32_t see, uint64_t cc,
+                                        uint64_t bb, uint64_t (&sum)[2]) {
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 y = unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, bb));
+    float p0 = ex2(y.x), p1 = ex2(y.y);
+    if (kMasked) {
+      p0 = (see >> (2 * i)) & 1 ? p0 : 0.0f;
+      p1 = (see >> (2 * i)) & 2 ? p1 : 0.0f;
+    }
+    sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+    p[i] = pack_bf16(p0, p1);
+  }
+  tmem_st16(to, p);  // at most over scores that have been read
+}
+
+// The same over a whole row with hidden keys; returns the sum.
+__device__ __forceinline__ float weigh_seen(uint32_t at, uint32_t to, float c, float base, int j,
+                                            const Sight& see) {
   const uint64_t cc = pair(c, c), bb = pair(-base, -base);
   uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-  uint32_t x[32], ahead[32];
-  tmem_ld32(at, x);
-  tmem_ld_wait();
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
-    tmem_ld32(at + 32 * ((h + 1) & 3), ahead);
-    uint32_t w = ~0u;
-    if (kMasked) w = seen32(j + 32 * h, see.lo, see.len, see.bits);
-    uint32_t p[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 y = unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, bb));
-      float p0 = ex2(y.x), p1 = ex2(y.y);
-      if (kMasked) {
-        p0 = (w >> (2 * i)) & 1 ? p0 : 0.0f;
-        p1 = (w >> (2 * i)) & 2 ? p1 : 0.0f;
-      }
-      sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
-      p[i] = pack_bf16(p0, p1);
-    }
+    uint32_t x[32];
+    tmem_ld32(at + 32 * h, x);
+    const uint32_t w = seen32(j + 32 * h, see.lo, see.len, see.bits);
     tmem_ld_wait();
-    tmem_st16(at + 16 * h, p);  // over scores that have been read
+    weigh32<true>(to + 16 * h, x, w, cc, bb, sum);
+  }
+  const float2 t = unpair(add2(sum[0], sum[1]));
+  return t.x + t.y;
+}
+
+// Rows that see the whole tile: the same two steps, 64 scores at a time.
+__device__ __forceinline__ float extreme_all(uint32_t at, bool least) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[64];
+    tmem_ld32(at + 64 * h, x);
+    tmem_ld32(at + 64 * h + 32, x + 32);
+    tmem_ld_wait();
+    if (least) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = ahead[i];
+      for (int i = 0; i < 64; ++i) x[i] ^= 0x80000000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(x[i]));
+  }
+  const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  return least ? -best : best;
+}
+
+__device__ __forceinline__ float weigh_all(uint32_t at, uint32_t to, float c, float base) {
+  const uint64_t cc = pair(c, c), bb = pair(-base, -base);
+  uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[64];
+    tmem_ld32(at + 64 * h, x);
+    tmem_ld32(at + 64 * h + 32, x + 32);
+    tmem_ld_wait();
+    weigh32<false>(to + 32 * h, x, 0, cc, bb, sum);
+    weigh32<false>(to + 32 * h + 16, x + 32, 0, cc, bb, sum);
   }
   const float2 t = unpair(add2(sum[0], sum[1]));
   return t.x + t.y;
@@ -419,27 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const TreeArgs& a = P.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
-    }
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
-    mbar_init(&sh.drain, 1);
-    mbar_init(&sh.v_all, 8);
-    mbar_init(&sh.b_done, 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 4);
-      mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.v_sync[i], 4);
-      mbar_init(&sh.o_free[i], 4);
-      sh.add_first[i] = 0;
-    }
-    sh.failed = 0;
+  static_assert(offsetof(Control, v_all) == 31 * 8 && offsetof(Control, o_free) == 37 * 8, "barriers");
+  if (warp == 0) {
+    uint64_t* bar = sh.k_full;
+    mbar_init(bar + lane, lane < 31 ? 1 : 8);
+    if (lane < 7) mbar_init(bar + 32 + lane, 4);
+    if (lane < 2) sh.add_first[lane] = 0;
+    if (lane == 0) sh.failed = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -493,16 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && wait_warp(&sh.k_full[k.slot], k.parity);
       tc_fence_after();
     };
-    auto sums = [&](int st, bool first, bool free_values) {
+    auto weighed = [&](int st) {
       ok = ok && wait_warp(&sh.p_ready[st], used[st]++ & 1);
-      if (!ok) return;
       tc_fence_after();
+    };
+    auto sums = [&](int st, bool first, bool free_values) {
       const uint32_t add = !first || *(volatile uint32_t*)&sh.add_first[st];
       const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
-          mma_bf16_ta(tmem + S::o_col(st), tmem + S::s_col(st) + 8 * i, vd + i * (2048 >> 4),
+          mma_bf16_ta(tmem + S::o_col(st), tmem + S::p_col(st) + 8 * i, vd + i * (2048 >> 4),
                       idesc_o, i != 0 ? 1u : add);
         mma_commit(&sh.pv_done[st]);
         if (free_values) mma_commit(&sh.v_empty[v.slot]);
@@ -526,22 +559,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (freed < halved) ok = ok && wait_warp(&sh.o_free[1], freed++ & 1);
       halved += both;
       for (int i = 0; i < w.n && ok; ++i) {
-        ok = wait_warp(&sh.v_full[v.slot], v.parity);
-        if (both) {
-          const bool more = i + 1 < w.n;
-          if (ok) sums(0, i == 0, false);
-          if (more && ok) {
-            keys();
-            if (ok) scores(0, 0, false, false);
-          }
-          if (ok) sums(1, i == 0, true);
-          if (more && ok) scores(1, 1, true, i + 2 == w.n);
-        } else {
-          if (ok) sums(i & 1, i < 2, true);
-          if (ok && i + 2 < w.n) {
-            keys();
-            if (ok) scores(i & 1, 0, true, i + 3 == w.n);
-          }
+        // a stream's next scores go before its sums where the weights lie
+        // apart, else behind them
+        const bool more = i + (both ? 1 : 2) < w.n, last = i + (both ? 2 : 3) == w.n;
+        for (int h = 0; h < (both ? 2 : 1) && ok; ++h) {
+          const int st = both ? h : i & 1;
+          auto next_scores = [&]() {
+            if (h == 0) keys();  // both streams use the same ones
+            if (ok) scores(st, both ? h : 0, !both || h == 1, last && (!both || h == 1));
+          };
+          weighed(st);
+          if (S::apart && more && ok) next_scores();
+          if (h == 0) ok = ok && wait_warp(&sh.v_full[v.slot], v.parity);
+          if (!ok) break;
+          sums(st, i < (both ? 1 : 2), !both || h == 1);
+          if (!S::apart && more) next_scores();
         }
         v.step(P.v_slots);
       }
@@ -574,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------- softmax
     const int st = warp >= 8, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_at = lanes + S::s_col(st), o_at = lanes + S::o_col(st);
+    const uint32_t o_at = lanes + S::o_col(st), p_real = lanes + S::p_col(st);
     const float c = a.scale * kLog2e;
     int g = 0;                       // tiles of the units before
     uint32_t used = 0, syncs = 0, alls = 0, joins = 0;  // phases of the barriers
@@ -601,36 +633,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.0f;
       const int first = both ? 0 : st, step = both ? 1 : 2;
-      for (int tile = first; tile < w.n && ok; tile += step, ++used) {
+      // The block's first tile is rehearsed while its data are on their way:
+      // the same code over whatever O holds, so that it is there when they
+      // come.  O is this stream's own until its first weights are ready.
+      bool real = is_first ? first >= w.n : true;
+      for (int tile = first; tile < w.n && ok;) {
         const int j0 = (w.q.lo + w.first + tile) * kTile;
         const bool masked = j0 + kTile > len || j0 < lo_most;
-        ok = wait_warp(&sh.s_full[st], used & 1);
-        if (!ok) break;
+        const uint32_t s_at = lanes + (real ? S::s_col(st) : S::o_col(st));
+        const uint32_t p_at = lanes + (real ? S::p_col(st) : S::o_col(st));
+        if (real) {
+          ok = wait_warp(&sh.s_full[st], used & 1);
+          if (!ok) break;
+        }
         tc_fence_after();
         if (any) {
-          const float best = c * (masked ? extreme<true>(s_at, c < 0.0f, j0, sight)
-                                         : extreme<false>(s_at, c < 0.0f, j0, sight));
+          float best = masked ? extreme_seen(s_at, c < 0.0f, j0, sight)
+                              : extreme_all(s_at, c < 0.0f);
+          best *= c;
+          if (S::apart && used > 0 && real) {  // the last product has read its weights
+            ok = wait_warp(&sh.pv_done[st], (used - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
           const bool raise = valid && best > m + kRaise;  // m = -inf: any maximum
           if (__any_sync(0xffffffffu, raise)) {
             const float now = raise ? best : m;
             const float f = raise ? ex2(m - now) : 1.0f;
-            if (tile > first) {  // the last product into O ended before these scores did
+            if (tile > first) {  // the last product into O has ended
 #pragma unroll 1
-              for (int i = 0; i < D / 32; ++i) {
-                uint32_t o[32];
-                tmem_ld32(o_at + 32 * i, o);
+              for (int i = 0; i < D / 8; ++i) {
+                uint32_t o[8];
+                tmem_ld8(o_at + 8 * i, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st32(o_at + 32 * i, o);
+                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st8(o_at + 8 * i, o);
               }
             }
             l *= f;
             m = now;
           }
           const float base = m == -INFINITY ? 0.0f : m;
-          l += masked ? weigh<true>(s_at, c, base, j0, sight) : weigh<false>(s_at, c, base, j0, sight);
+          l += masked ? weigh_seen(s_at, p_at, c, base, j0, sight) : weigh_all(s_at, p_at, c, base);
           tmem_st_wait();
+        }
+        if (!real) {
+          real = true;
+          m = -INFINITY;
+          l = 0.0f;
+          continue;
         }
         uint32_t found = 0;
         if (masked) {
@@ -671,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t word = j < 64 ? (j < 32 ? rows_bad[0] : rows_bad[1])
                                              : (j < 96 ? rows_bad[2] : rows_bad[3]);
                 if (!((word >> (j & 31)) & 1)) continue;
-                const uint32_t pp = tmem_ld1(s_at + (j >> 1));
+                const uint32_t pp = tmem_ld1(p_real + (j >> 1));
                 tmem_ld_wait();
                 const float p = __uint_as_float(j & 1 ? pp & 0xffff0000u : pp << 16);
                 const bool sees = seen32(j0 + j, sight.lo, sight.len, sight.bits) & 1;
@@ -714,6 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_ready[st]);
+        tile += step;
+        ++used;
       }
       if (!ok) break;
       const bool worked = first < w.n;  // the stream had a tile of this unit
