@@ -56,6 +56,25 @@ __device__ __forceinline__ int cache_page(const dspark_cache& c, int s, int i,
   return p >= 0 && p < c.num_pages ? p : -1;
 }
 
+// The page of token x of a sequence, and its place there.  Page sizes are
+// mostly powers of two, and a division is 25 instructions: in kernels this
+// short they come from memory, one cache line after another.
+__device__ __forceinline__ uint32_t page_of(const dspark_cache& c, uint32_t x, int& slot) {
+  const uint32_t n = (uint32_t)c.page_size;
+  if ((n & (n - 1)) == 0) {
+    slot = (int)(x & (n - 1));
+    return x >> (31 - __clz(n));
+  }
+  const uint32_t p = x / n;
+  slot = (int)(x - p * n);
+  return p;
+}
+// Pages that hold x tokens.
+__device__ __forceinline__ uint32_t pages_for(const dspark_cache& c, uint32_t x) {
+  int slot;
+  return x == 0 ? 0u : page_of(c, x - 1, slot) + 1;
+}
+
 // Bytes from the start of the pool to a token of one head: plane 2 layer
 // (keys) or 2 layer + 1 (values).
 __host__ __device__ __forceinline__ size_t cache_row(const dspark_cache& c,

@@ -11,8 +11,7 @@
 // so a warp's load is 512 contiguous bytes; the mean is a butterfly over the
 // group, and the other half of a pair sits in the lane rot_dim / 2 values
 // away (or in the same lane, for neighbouring pairs).  A warp stays on one
-// token and loads kPer times before it stores, so the rotation's cosines are
-// loaded once for all its heads.  Rows that do not split that way (other head
+// token, so the rotation's cosines are loaded once for all its heads.  Rows that do not split that way (other head
 // dims than 8, 16 or 32 lanes hold, rotations that end inside a lane's words,
 // unaligned tables) take the row kernel: a warp for each row, through shared
 // memory.
@@ -84,10 +83,11 @@ __device__ __forceinline__ Token find_token(const AppendArgs& a, int i, bool rep
   k.there = s >= 0 && (a.count == nullptr || k.t < a.count[k.b]);
   if (s < 0 && report) cache_error(a.c, kCacheErrSeq);
   if (!k.there) return k;
-  const long long at = (long long)a.length[k.b] + k.t;
-  if (at >= k.t && at < (long long)cache_held(a.c, s) * a.c.page_size) {
-    k.page = cache_page(a.c, s, (int)(at / a.c.page_size), a.c.max_pages);
-    k.slot = (int)(at % a.c.page_size);
+  const int len = a.length[k.b];
+  // held pages hold at most 2^30 tokens, and t < 2^24
+  if (len >= 0 && len < (1 << 30)) {
+    const uint32_t i = page_of(a.c, (uint32_t)(len + k.t), k.slot);
+    if (i < (uint32_t)cache_held(a.c, s)) k.page = cache_page(a.c, s, (int)i, a.c.max_pages);
   }
   if (k.page < 0 && report) cache_error(a.c, kCacheErrPage);
   if (k.position < 0 || k.position >= a.max_position) {
@@ -148,35 +148,41 @@ __device__ __forceinline__ void load_floats(const float* p, float* x) {
   }
 }
 
-// kLanes lanes hold a row, kPer loads a warp.  The table and the weights are
-// read 16 bytes at a time (one value at a time the loads of angles and
-// weights, not HBM, bound the pass: 119 us for two prompts of 13k tokens).
+// kLanes lanes hold a row; a warp takes `batches` times kPer loads of a token,
+// the next batch on its way while one is worked on.  The table and the weights
+// are read 16 bytes at a time (one value at a time the loads of angles and
+// weights, not HBM, bound the pass: 119 us for two prompts of 13k tokens), and
+// the first batch is under way before the token's place is looked up (97 us
+// when each warp took one batch and looked its token up first).
 template <typename T, int kLanes, int kPer, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int splits, int batches) {
   constexpr int N = Word<T>::n, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31;
   const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int token = w / splits, split = w - token * splits;
   if (token >= a.B * a.T) return;
   follow();
-  const Token k = find_token(a, token, lane == 0 && split == 0);
-  if (!k.there) return;
   const int sub = lane & (kLanes - 1);
   const int d0 = sub * N, half = a.rot >> 1;
-  const int h0 = split * kPer * kRows + lane / kLanes;
   const int Hq = a.heads, Hk = a.c.kv_heads;
   constexpr int elt = sizeof(T), row = kLanes * 16;
   const char* q = a.q + (size_t)token * a.q_stride * elt + 16 * sub;
-  const char* kk = a.k + (size_t)token * a.k_stride * elt + 16 * sub;
-  const char* v = a.v + (size_t)token * a.v_stride * elt + 16 * sub;
+  const char* kk = a.k + (size_t)token * a.k_stride * elt + 16 * sub - Hq * row;
+  const char* v = a.v + (size_t)token * a.v_stride * elt + 16 * sub - (Hq + Hk) * row;
+  int h0 = split * batches * kPer * kRows + lane / kLanes;
   uint4 word[kPer];
+  auto load = [&](int from, uint4 (&to)[kPer]) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int h = h0 + i * kRows;
-    const char* src = h < Hq ? q + h * row : h < Hq + Hk ? kk + (h - Hq) * row : v + (h - Hq - Hk) * row;
-    word[i] = make_uint4(0, 0, 0, 0);
-    if (h < Hq + 2 * Hk) word[i] = *reinterpret_cast<const uint4*>(src);
-  }
+    for (int i = 0; i < kPer; ++i) {
+      const int h = from + i * kRows;
+      const char* src = h < Hq ? q : h < Hq + Hk ? kk : v;
+      to[i] = make_uint4(0, 0, 0, 0);
+      if (h < Hq + 2 * Hk) to[i] = __ldcs(reinterpret_cast<const uint4*>(src + h * row));
+    }
+  };
+  load(h0, word);
+  const Token k = find_token(a, token, lane == 0 && split == 0);
+  if (!k.there) return;
   // the angle of each of the lane's values; the sine carries the sign
   float cs[N], sn[N];
   int partner = lane;
@@ -216,42 +222,51 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int spli
   char* k_out = static_cast<char*>(a.c.pool) +
                 cache_row(a.c, 2 * a.layer, k.page < 0 ? 0 : k.page, 0, k.slot) + 16 * sub;
   char* v_out = k_out + cache_row(a.c, 1, 0, 0, 0);
+  for (int batch = 0; batch < batches; ++batch) {
+    uint4 ahead[kPer];
+    if (kPer > 1 && batch + 1 < batches) load(h0 + kPer * kRows, ahead);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int h = h0 + i * kRows;
-    const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hk;
-    float x[N], y[N];
-    Word<T>::load(word[i], x);
-    if (norm) {  // the butterfly is the whole warp's
-      float sum = 0.0f;
+    for (int i = 0; i < kPer; ++i) {
+      const int h = h0 + i * kRows;
+      const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hk;
+      float x[N], y[N];
+      Word<T>::load(word[i], x);
+      if (norm) {  // the butterfly is the whole warp's
+        float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum = fmaf(x[e], x[e], sum);
+        for (int e = 0; e < N; ++e) sum = fmaf(x[e], x[e], sum);
 #pragma unroll
-      for (int m = kLanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      const float r = rsqrtf(sum * (1.0f / (kLanes * N)) + a.eps);
-      if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+        for (int m = kLanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const float r = rsqrtf(sum * (1.0f / (kLanes * N)) + a.eps);
+        if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
+          for (int e = 0; e < N; ++e) x[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
+        }
+      }
+      if (kInterleaved) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] = x[e ^ 1];
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
+      }
+      // a value that is not turned keeps its bits (0 * infinity is no 0)
+      if (turn) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
+      }
+      if (is_q) {
+        *reinterpret_cast<uint4*>(q_out + h * row) = Word<T>::store(x);
+      } else if (k.page >= 0) {
+        if (is_k) *reinterpret_cast<uint4*>(k_out + (h - Hq) * step) = Word<T>::store(x);
+        else if (h < Hq + 2 * Hk) *reinterpret_cast<uint4*>(v_out + (h - Hq - Hk) * step) = word[i];
       }
     }
-    if (kInterleaved) {
+    if (kPer > 1) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = x[e ^ 1];
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
+      for (int i = 0; i < kPer; ++i) word[i] = ahead[i];
     }
-    // a value that is not turned keeps its bits (0 * infinity is no 0)
-    if (turn) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
-    }
-    if (is_q) {
-      *reinterpret_cast<uint4*>(q_out + h * row) = Word<T>::store(x);
-    } else if (k.page >= 0) {
-      if (is_k) *reinterpret_cast<uint4*>(k_out + (h - Hq) * step) = Word<T>::store(x);
-      else if (h < Hq + 2 * Hk) *reinterpret_cast<uint4*>(v_out + (h - Hq - Hk) * step) = word[i];
-    }
+    h0 += kPer * kRows;
   }
 }
 
@@ -309,17 +324,21 @@ cudaError_t launch_lanes(const AppendArgs& a, cudaStream_t stream) {
   const long long tokens = (long long)a.B * a.T;
   // rows of a warp's load, and loads of a token
   const int per_warp = 32 / kLanes, loads = (rows + per_warp - 1) / per_warp;
-  // four loads a warp where that still leaves every multiprocessor 16 warps,
-  // else one: fewer tokens than that are bound by latency
-  const bool many = tokens * loads / 4 >= 16LL * sm_count();
-  const int splits = many ? (loads + 3) / 4 : loads;
+  // Four loads a batch, and a whole token a warp, as far as that leaves every
+  // multiprocessor 16 warps; fewer tokens than that are bound by latency.
+  const long long enough = 16LL * sm_count();
+  const bool many = tokens * ((loads + 3) / 4) >= enough;
+  const int all = many ? (loads + 3) / 4 : loads;  // batches of a token
+  int splits = all;
+  while (many && splits > 1 && tokens * (splits / 2) >= enough) splits = (splits + 1) / 2;
+  const int batches = (all + splits - 1) / splits;
   if (tokens * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = (unsigned)((tokens * splits + kThreads / 32 - 1) / (kThreads / 32));
   const auto kernel = many ? (a.interleaved ? append_kernel<T, kLanes, 4, true>
                                             : append_kernel<T, kLanes, 4, false>)
                            : (a.interleaved ? append_kernel<T, kLanes, 1, true>
                                             : append_kernel<T, kLanes, 1, false>);
-  return launch_behind(kernel, blocks, kThreads, 0, stream, a, splits);
+  return launch_behind(kernel, blocks, kThreads, 0, stream, a, splits, batches);
 }
 
 template <typename T>

@@ -160,9 +160,9 @@ __global__ void __launch_bounds__(kBlock, 1)
       cache_error(c, kCacheErrPage);
     } else {
       h = cache_held(c, s);
-      const long long want = ((long long)len + tokens + c.page_size - 1) / c.page_size;
-      if (want > c.max_pages) cache_error(c, kCacheErrFull);
-      else if (want > h) n = (int)want - h;
+      const uint32_t want = pages_for(c, (uint32_t)len + (uint32_t)tokens);
+      if (want > (uint32_t)c.max_pages) cache_error(c, kCacheErrFull);
+      else if ((int)want > h) n = (int)want - h;
     }
     need[b] = n;
     have[b] = h;
@@ -245,12 +245,12 @@ __global__ void __launch_bounds__(kBlock, 1)
   if (b < B) {
     int f = 0, n = 0;
     if (s >= 0) {
-      const long long have = (long long)cache_held(c, p) * c.page_size;
-      if (len < 0 || len > have) {
+      if (len < 0 || len > cache_held(c, p) * c.page_size) {  // at most 2^30
         cache_error(c, kCacheErrPage);
       } else {
-        f = len / c.page_size;
-        n = len % c.page_size > 0 ? 1 : 0;
+        int rest;
+        f = (int)page_of(c, (uint32_t)len, rest);
+        n = rest > 0 ? 1 : 0;
       }
     }
     full[b] = f;
@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kCopyThreads)
   const int from = __ldcg(&c.control[kCtlScratch + 2 * b]);
   const int to = __ldcg(&c.control[kCtlScratch + 2 * b + 1]);
   if (to < 0) return;
-  const int words = length[b] % c.page_size * (c.head_dim * dtype_bytes(c.dtype) / 16);
+  int rows;
+  page_of(c, (uint32_t)length[b], rows);
+  const int words = rows * (c.head_dim * dtype_bytes(c.dtype) / 16);
   const int lane = threadIdx.x & 31, items = 2 * c.layers * c.kv_heads;
   char* pool = static_cast<char*>(c.pool);
   for (int item = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); item < items;
@@ -345,12 +347,13 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int b = blockIdx.y;
   follow();
   const int s = cache_seq(c, seq, b), len = length[b], acc = accepted[b];
-  const long long wanted = acc < 0 ? 0 : (long long)acc + extra;
+  const uint32_t wanted = acc < 0 ? 0u : (uint32_t)acc + (uint32_t)extra;
   const int most = path ? path_width : tokens;
   const int held = s < 0 ? 0 : cache_held(c, s);
   int err = s < 0 ? kCacheErrSeq : 0;
-  if (!err && (wanted > most || wanted > tokens)) err = kCacheErrPath;
-  if (!err && (len < 0 || len + wanted > (long long)held * c.page_size)) err = kCacheErrPage;
+  if (!err && (wanted > (uint32_t)most || wanted > (uint32_t)tokens)) err = kCacheErrPath;
+  if (!err && (len < 0 || (uint32_t)len + wanted > (uint32_t)(held * c.page_size)))
+    err = kCacheErrPage;  // both below 2^31; held pages hold at most 2^30
   int n = err ? 0 : (int)wanted;
   if (threadIdx.x == 0) first_move = DSPARK_TREE_MAX_TOKENS;
   __syncthreads();
@@ -363,14 +366,16 @@ __global__ void __launch_bounds__(kMoveThreads)
         bad = true;
         continue;
       }
-      const int from = cache_page(c, s, (int)(((long long)len + at) / c.page_size), held);
-      const int to = cache_page(c, s, (len + i) / c.page_size, held);
+      int from_slot, to_slot;
+      const uint32_t fi = page_of(c, (uint32_t)len + (uint32_t)at, from_slot);
+      const int from = fi < (uint32_t)held ? cache_page(c, s, (int)fi, held) : -1;
+      const int to = cache_page(c, s, (int)page_of(c, (uint32_t)(len + i), to_slot), held);
       if (from < 0 || to < 0) {
         unheld = true;
         continue;
       }
-      src[i] = cache_row(c, 0, from, 0, (int)(((long long)len + at) % c.page_size));
-      dst[i] = cache_row(c, 0, to, 0, (len + i) % c.page_size);
+      src[i] = cache_row(c, 0, from, 0, from_slot);
+      dst[i] = cache_row(c, 0, to, 0, to_slot);
       if (at != i) atomicMin(&first_move, i);
     }
     if (__syncthreads_or(bad)) err = kCacheErrPath;
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     int from = 0, count = 0;
     if (si >= 0 && now >= 0) {
       const int h = cache_held(c, si);
-      from = (int)(((long long)now + c.page_size - 1) / c.page_size);
+      from = (int)pages_for(c, (uint32_t)now);
       count = h > from ? h - from : 0;
     }
     g.seq[i] = si;
@@ -441,7 +446,9 @@ cudaError_t launch_cache_init(const dspark_cache& c, cudaStream_t stream) {
 cudaError_t launch_cache_reserve(const dspark_cache& c, const int32_t* seq,
                                  const int32_t* length, int tokens, int B,
                                  cudaStream_t stream) {
-  return launch_behind(reserve_kernel, 1, kBlock, 0, stream, c, seq, length, tokens, B);
+  // a thread for each sequence: fewer warps to sum over where there are few
+  const int threads = B <= 128 ? 128 : kBlock;
+  return launch_behind(reserve_kernel, 1, threads, 0, stream, c, seq, length, tokens, B);
 }
 
 cudaError_t launch_cache_release(const dspark_cache& c, const int32_t* seq,
