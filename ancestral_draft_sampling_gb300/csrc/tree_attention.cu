@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
   const T* pool = static_cast<const T*>(a.c.pool);
   float* pw = ps + warp * kTile * 4;
   follow();
-  TreeWalk w = tree_start(a, share);
+  tree_start(a, share);
+  TreeWalk w = share.walk;
   if (threadIdx.x == kThreads - 1) tree_describe(a, w);
   bool is_first = true;
   for (bool some = w.n > 0; some; some = w.next(a)) {
@@ -316,7 +317,8 @@ cudaError_t launch_ffma(const TreeArgs& a, size_t smem, cudaStream_t stream) {
 
 cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
   const int D = a.c.head_dim;
-  a.tile = kTile;
+  a.tile_shift = 6;
+  static_assert(kTile == 1 << 6, "tile");
   a.row_tokens = kRows / a.group;
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
   a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;

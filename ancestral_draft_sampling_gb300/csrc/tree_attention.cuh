@@ -43,7 +43,7 @@ struct TreeArgs {
   float* lse;
   // schedule
   int blocks;      // G
-  int tile;        // keys of a tile
+  int tile_shift;  // log2 of the keys of a tile
   int row_tokens;  // drafted tokens of a row tile
   int row_tiles;   // of T tokens
   int slot_rows;   // rows of a partial result
@@ -95,18 +95,20 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, const TreeRaw& w,
   r.cnt = w.cnt < 0 ? 0 : w.cnt > a.T ? a.T : w.cnt;
   r.lo = 0;
   r.tiles = 0;
-  r.row_tiles = r.cnt <= a.row_tokens ? 1 : (r.cnt + a.row_tokens - 1) / a.row_tokens;
+  r.row_tiles = 1;
+  if (r.cnt > a.row_tokens) r.row_tiles = (uint32_t)(r.cnt + a.row_tokens - 1) / (uint32_t)a.row_tokens;
   const int held = w.held < 0 ? 0 : w.held > a.c.max_pages ? a.c.max_pages : w.held;
   int err = r.s < 0 ? kCacheErrSeq : 0;
-  if (!err && (r.len < 0 || (long long)r.len + r.cnt > (long long)held * a.c.page_size))
+  // a table row holds at most 2^30 tokens
+  if (!err && (r.len < 0 || r.len > (1 << 30) || r.len + r.cnt > held * a.c.page_size))
     err = kCacheErrPage;
   if (err) {
     if (report) cache_error(a.c, err);
     return r;
   }
   if (r.cnt == 0) return r;
-  if (a.window > 0 && r.len >= a.window) r.lo = (r.len - a.window + 1) / a.tile;
-  r.tiles = (r.len + r.cnt - 1) / a.tile + 1 - r.lo;  // lengths stay below 2^30
+  if (a.window > 0 && r.len >= a.window) r.lo = (r.len - a.window + 1) >> a.tile_shift;
+  r.tiles = ((r.len + r.cnt - 1) >> a.tile_shift) + 1 - r.lo;
   return r;
 }
 
@@ -114,26 +116,21 @@ __device__ __forceinline__ long long tree_work(const TreeArgs& a, const TreeSeq&
   return (long long)(r.row_tiles * a.c.kv_heads) * r.tiles;
 }
 
-// Blocks that have a share, and the share of block c.
-__device__ __forceinline__ long long tree_first(long long W, int G, int c) {
-  if (W < (1 << 23)) return (uint32_t)W * (uint32_t)c / (uint32_t)G;  // c <= 320
-  return (W / G) * c + (W % G) * c / G;
-}
-// The share starts at floor(W c / G) = (W/G) c + floor((W % G) c / G).  The
-// block of tile x: the largest c with floor(W c / G) <= x, found from the
-// quotient and corrected by at most a step or two.
-__device__ __forceinline__ int tree_block_of(long long W, int G, long long x) {
-  int c = (int)((double)x * G / (double)W);
-  if (c >= G) c = G - 1;
-  while (c > 0 && tree_first(W, G, c) > x) --c;
-  while (c + 1 < G && tree_first(W, G, c + 1) <= x) ++c;
-  return c;
+// The line's tiles are counted in 32 bits (more than 2^31 of them, some ten
+// seconds of work, are refused): code comes from memory while a block waits
+// for it, and a 64-bit division is a hundred instructions.
+
+// Where share c of W tiles over G blocks starts: floor(W c / G); c <= G <= 320.
+__device__ __forceinline__ int tree_first(int W, int G, int c) {
+  const uint32_t q = (uint32_t)W / (uint32_t)G, r = (uint32_t)W - q * G;
+  return (int)(q * c + r * c / (uint32_t)G);
 }
 
 // A block's walk over its share, one unit at a time.
 struct TreeWalk {
-  long long pos, end;  // tiles of the line
-  long long base;      // first tile of sequence b
+  int pos, end;        // tiles of the line
+  int base;            // first tile of sequence b
+  int W;               // tiles of the line
   int b;
   TreeSeq q;
   TreeRaw ahead;       // of sequence b + 1
@@ -142,28 +139,29 @@ struct TreeWalk {
   int first, n;        // its tiles here: first .. first + n - 1, counted from
                        // the unit's own first tile
   bool whole;          // all of the unit's tiles are here
-  long long W;         // tiles of the line
 
   __device__ __forceinline__ bool next(const TreeArgs& a) {
     if (pos >= end) return false;
-    long long work = tree_work(a, q);
+    int work = q.row_tiles * a.c.kv_heads * q.tiles;
     while (pos >= base + work) {
       base += work;
       if (++b >= a.B) return false;
       q = tree_seq(a, ahead, false);
       if (b + 1 < a.B) ahead = tree_load(a, b + 1);
-      work = tree_work(a, q);
+      work = q.row_tiles * a.c.kv_heads * q.tiles;
     }
-    const long long at = pos - base;
-    int unit;
-    if (at < 0x7fffffffLL) unit = (int)((uint32_t)at / (uint32_t)q.tiles);
-    else unit = (int)(at / q.tiles);
-    first = (int)(at - (long long)unit * q.tiles);
-    h = q.row_tiles == 1 ? unit : unit / q.row_tiles;
-    rt = unit - h * q.row_tiles;
-    const long long left = end - pos;
+    const uint32_t at = (uint32_t)(pos - base);
+    const int unit = (int)(at / (uint32_t)q.tiles);
+    first = (int)at - unit * q.tiles;
+    h = unit;
+    rt = 0;
+    if (q.row_tiles > 1) {
+      h = (int)((uint32_t)unit / (uint32_t)q.row_tiles);
+      rt = unit - h * q.row_tiles;
+    }
+    const int left = end - pos;
     n = q.tiles - first;
-    if (n > left) n = (int)left;
+    if (n > left) n = left;
     whole = n == q.tiles;
     pos += n;
     return true;
@@ -177,21 +175,17 @@ struct TreeShare {
 };
 
 // Every thread of the block calls this (blockDim.x a multiple of 32): sums the
-// work of the sequences and finds where this block's share starts.  The walk
-// comes back on its first unit (n = 0: there is none), which one thread finds
-// for all: the first run of any code costs its way from memory.  The block is
-// synchronised twice.
-__device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, TreeShare& sh) {
+// work of the sequences and finds where this block's share starts.  Leaves the
+// walk in sh, on its first unit (n = 0: there is none), which one thread finds
+// for all.  The block is synchronised twice.
+__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare& sh) {
   const int n = blockDim.x, t = threadIdx.x;
-  const int per = (a.B + n - 1) / n;  // sequences of a thread; mostly one
+  const int per = a.B <= n ? 1 : (int)((uint32_t)(a.B + n - 1) / (uint32_t)n);
   const int b0 = t * per, b1 = b0 + per < a.B ? b0 + per : a.B;
-  TreeSeq mine{};
   long long work = 0;
-  for (int b = b0; b < b1; ++b) {
-    const TreeSeq q = tree_seq(a, tree_load(a, b), blockIdx.x == 0);
-    if (b == b0) mine = q;
-    work += tree_work(a, q);
-  }
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b)
+    work += tree_work(a, tree_seq(a, tree_load(a, b), blockIdx.x == 0));
   const int lane = t & 31, warp = t >> 5;
   long long x = work;
 #pragma unroll
@@ -201,60 +195,48 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, TreeShare& sh)
   }
   if (lane == 31) sh.sums[warp] = x;
   __syncthreads();
-  long long before = x - work, W = 0;
+  long long before = x - work, all = 0;
+#pragma unroll 1
   for (int i = 0; i < n / 32; ++i) {
     const long long v = sh.sums[i];
     if (i < warp) before += v;
-    W += v;
+    all += v;
   }
-  const int G = W < a.blocks ? (int)W : a.blocks;
-  TreeWalk w;
-  w.pos = w.end = w.base = 0;
-  w.W = W;
-  w.b = w.h = w.rt = w.first = w.n = 0;
-  w.whole = false;
-  w.q = TreeSeq{};
-  w.ahead = TreeRaw{};
+  TreeWalk w{};
+  if (all > 0x7fffffffLL) {
+    if (blockIdx.x == 0 && t == 0) cache_error(a.c, kCacheErrPage);
+    all = 0;
+  }
+  w.W = (int)all;
+  const int G = w.W < a.blocks ? w.W : a.blocks;
   const bool some = (int)blockIdx.x < G;
   if (some) {
-    w.pos = tree_first(W, G, blockIdx.x);
-    w.end = tree_first(W, G, blockIdx.x + 1);
-    if (w.pos >= before && w.pos < before + work) {
-      long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        const TreeSeq q = b == b0 ? mine : tree_seq(a, tree_load(a, b), false);
-        const long long k = tree_work(a, q);
-        if (w.pos < at + k) {
-          w.b = b;
-          w.base = at;
-          w.q = q;
-          w.next(a);
-          sh.walk = w;
-          break;
-        }
-        at += k;
-      }
+    w.pos = tree_first(w.W, G, blockIdx.x);
+    w.end = tree_first(w.W, G, blockIdx.x + 1);
+    if (w.pos >= before && w.pos < before + work) {  // one thread
+      w.base = (int)before;
+      w.b = b0;
+      w.q = tree_seq(a, tree_load(a, b0), false);
+      if (b0 + 1 < a.B) w.ahead = tree_load(a, b0 + 1);
+      w.next(a);
+      sh.walk = w;
     }
+  } else if (t == 0) {
+    sh.walk = w;
   }
   __syncthreads();
-  if (some) {
-    w = sh.walk;
-    if (w.b + 1 < a.B) w.ahead = tree_load(a, w.b + 1);
-  }
-  return w;
 }
 
 // One thread of every block, with the walk on its first unit: what this block
-// of the merge has to do.  The share's start cuts a unit when the
-// first unit does not begin there; the unit is this block's to join when the
-// share before it holds the unit's beginning.
+// of the merge has to do.  The share's start cuts a unit when the first unit
+// does not begin there; the unit is this block's to join when the share before
+// it holds the unit's beginning.
 __device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk& w) {
   TreeJoin j{};
   const int c = blockIdx.x;
   if (w.n > 0 && w.first > 0) {
-    const long long start = w.pos - w.n;
-    const int G = w.W < a.blocks ? (int)w.W : a.blocks;
-    const long long us = start - w.first, before = tree_first(w.W, G, c - 1);
+    const int G = w.W < a.blocks ? w.W : a.blocks;
+    const int us = w.pos - w.n - w.first, before = tree_first(w.W, G, c - 1);
     if (before <= us) {
       j.b = w.b;
       j.h = w.h;
@@ -263,7 +245,9 @@ __device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk&
       j.rows = tokens * a.group;
       j.first = c - 1;
       j.slot = 2 * (c - 1) + (before == us ? 0 : 1);
-      j.last = tree_block_of(w.W, G, us + w.q.tiles - 1);
+      j.last = c;
+#pragma unroll 1
+      while (j.last + 1 < G && tree_first(w.W, G, j.last + 1) < us + w.q.tiles) ++j.last;
     }
   }
   a.join[c] = j;

@@ -23,11 +23,15 @@
 // flight, which covers the latency of HBM several times over.
 //   warps 0, 3   fill the rings of keys and of values, a copy for each page's
 //                rows and each half of the head (64 values, 128-byte swizzle);
-//                the page numbers come 32 at a time, one load ahead.
+//                the page numbers come 32 at a time, one load ahead.  Warp 3
+//                also loads a unit's queries (rows (token, head) of the key
+//                head), once the last unit's scores are done.
 //   warp 1       issues the products.
-//   warp 2       loads a unit's queries (TMA, rows (token, head) of the key
-//                head), once the last unit's scores are done, and tells the
-//                merge what to do.
+//   warp 2       walks the block's units and describes them to the others, up
+//                to four ahead (walks of their own made each role's code 8 KB
+//                longer, and code comes from memory: 160 KB in all, of which a
+//                unit of a few tiles waited for 9 us); tells the merge what to
+//                do.
 //   warps 4..7, 8..11  the streams' softmax: rows 32 (w % 4) .. + 31.
 // Tiles that some rows see and others do not (the drafted tokens, a window's
 // edge, the sequence's end) may hold NaN or infinities in places that weigh
@@ -70,6 +74,17 @@ struct Shape {
   static constexpr uint32_t p_col(uint32_t i) { return apart ? 384 + 64 * i : s_col(i); }
 };
 
+// A unit as warp 2 describes it.
+struct Unit {
+  int n;            // its tiles here; 0: no more units
+  int key;          // first key
+  int s, len, cnt;  // sequence: its table row, committed and drafted tokens
+  int b, h, t0;     // batch row, key head, first drafted token
+  int both;         // more than 128 rows: half of them for each stream
+  int whole;        // all of its tiles are here
+};
+constexpr int kUnits = 4, kUnitReaders = 11;  // warps 0, 1, 3 and the softmax
+
 struct Control {  // shared memory behind the tiles
   // barriers: one arrival completes a phase of the first 31, four (a stream's
   // warps) one of those behind but v_all, which takes eight
@@ -82,6 +97,8 @@ struct Control {  // shared memory behind the tiles
   // streams' where it joins them), by the second where it has rows of its own.
   // Nobody arrives without work in the unit, so no phase is run ahead of.
   uint64_t o_free[2];
+  uint64_t u_full[kUnits], u_empty[kUnits];
+  Unit units[kUnits];
   TreeShare share;
   uint32_t bad[2][4];     // rows of a value tile that hold NaN or infinities
   uint32_t add_first[2];  // the unit's first product adds to O
@@ -96,8 +113,12 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a block");
 
+// The polls of a wait that is not over at once: out of line, there are many.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
+  return mbar_wait(bar, parity, kSpin);
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, kSpin);
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity);
 }
 
 // The same for a whole warp: either all its lanes go on or none does.
@@ -262,6 +283,20 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// A warp's view of the units.
+struct UnitReader {
+  Place at{0, 0};
+  __device__ __forceinline__ bool next(Control& sh, Unit& u, bool& ok, int lane) {
+    ok = wait_warp(&sh.u_full[at.slot], at.parity);
+    if (!ok) return false;
+    u = sh.units[at.slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.u_empty[at.slot]);
+    at.step(kUnits);
+    return u.n > 0;
+  }
+};
+
 // 32 bytes in one store.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
@@ -375,15 +410,12 @@ __device__ __forceinline__ float weigh_all(uint32_t at, uint32_t to, float c, fl
   return t.x + t.y;
 }
 
-// The tiles of a ring, from the walk to the copies: the page numbers of a
-// unit's tiles 32 at a time, the first of the next unit's loaded while this
-// one's are used.
+// The page numbers of a unit's tiles, 32 at a time: lane l has page first + l,
+// or the place behind the pool, which reads as zeros.
 struct Pages {
   const int32_t* row;  // of the block table
-  int h, n;            // key head and tiles
-  int key;             // first key
   int last;            // last page that holds a key of the sequence
-  int ids, first;      // lane l: page first + l, or the place behind the pool
+  int first, ids;
 
   __device__ __forceinline__ int load(const TcArgs& P, int page) const {
     if (page > last) return P.a.c.num_pages;
@@ -392,45 +424,72 @@ struct Pages {
     cache_error(P.a.c, kCacheErrPage);
     return P.a.c.num_pages;
   }
-  __device__ __forceinline__ void set(const TcArgs& P, const TreeWalk& w, int lane) {
-    row = P.a.c.block_table + (size_t)w.q.s * P.a.c.max_pages;
-    h = w.h;
-    n = w.n;
-    key = (w.q.lo + w.first) * kTile;
-    last = (w.q.len + w.q.cnt - 1) >> P.page_shift;
-    first = key >> P.page_shift;
+  __device__ __forceinline__ void set(const TcArgs& P, const Unit& u, int lane) {
+    row = P.a.c.block_table + (size_t)u.s * P.a.c.max_pages;
+    last = (u.len + u.cnt - 1) >> P.page_shift;
+    first = u.key >> P.page_shift;
     ids = load(P, first + lane);
   }
 };
 
+// The queries of a unit: one copy for each 128 rows and half of the head.
 template <int D>
-__device__ __forceinline__ bool fill_ring(const TcArgs& P, TreeWalk& w, const CUtensorMap* map,
-                                          uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                          int slots, int lane) {
+__device__ __forceinline__ void load_queries(const TcArgs& P, const Unit& u, const CUtensorMap* map,
+                                             uint8_t* q_tile, uint64_t* full) {
+  const int copies = (1 + u.both) * Shape<D>::halves;
+  mbar_arrive_expect_tx(full, copies * P.q_tokens * P.a.group * 128);
+#pragma unroll 1
+  for (int i = 0; i < copies; ++i) {
+    const int tile = i / Shape<D>::halves, half = i - tile * Shape<D>::halves;
+    tma_5d(q_tile + i * kHalfBytes, map, full, half * 64, 0, u.h, u.t0 + tile * P.fit, u.b);
+  }
+}
+
+// Fills the ring of keys, or that of values and the queries before a unit's
+// first values.
+template <int D>
+__device__ __noinline__ bool fill_ring(const TcArgs& P, Control& sh, bool values,
+                                       const CUtensorMap* map, const CUtensorMap* map_q,
+                                       uint8_t* q_tile, uint8_t* ring, int lane) {
   using S = Shape<D>;
+  uint64_t* full = values ? sh.v_full : sh.k_full;
+  uint64_t* empty = values ? sh.v_empty : sh.k_empty;
+  const int slots = values ? P.v_slots : P.k_slots;
   Place at{0, 1};  // the phase that frees a slot: the first round passes
-  int filled = 0;
+  int filled = 0, unit = 0;
   bool ok = true;
   // each lane copies one page's rows of one half of the head
   const int half = lane / P.pages, part = lane - half * P.pages;
   const bool mine = half < S::halves;
   uint8_t* const to = ring + half * kHalfBytes + part * P.page_rows * 128;
-  Pages next{}, cur{};
-  bool some = w.n > 0;
-  if (some) next.set(P, w, lane);
+  UnitReader units;
+  Unit next{}, cur{};
+  Pages next_pages{}, pages{};
+  bool some = units.next(sh, next, ok, lane);
+  if (some) next_pages.set(P, next, lane);
+#pragma unroll 1
   while (some && ok) {
     cur = next;
-    int ids2 = cur.load(P, cur.first + 32 + lane);
+    pages = next_pages;
+    if (values) {
+      if (unit > 0) ok = wait_warp(&sh.q_empty, (unit - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) load_queries<D>(P, cur, map_q, q_tile, &sh.q_full);
+      __syncwarp();
+      ++unit;
+    }
+    int ids2 = pages.load(P, pages.first + 32 + lane);
+#pragma unroll 1
     for (int i = 0; i < cur.n; ++i) {
       const int j = cur.key + i * kTile, page = j >> P.page_shift;
-      if (page >= cur.first + 32) {
-        cur.first += 32;
-        cur.ids = ids2;
-        ids2 = cur.load(P, cur.first + 32 + lane);
+      if (page >= pages.first + 32) {
+        pages.first += 32;
+        pages.ids = ids2;
+        ids2 = pages.load(P, pages.first + 32 + lane);
       }
       ok = wait_warp(&empty[at.slot], at.parity);
       if (!ok) break;
-      const int id = __shfl_sync(0xffffffffu, cur.ids, (page - cur.first + part) & 31);
+      const int id = __shfl_sync(0xffffffffu, pages.ids, (page - pages.first + part) & 31);
       if (lane == 0) mbar_arrive_expect_tx(&full[at.slot], S::tile_bytes);
       __syncwarp();
       if (mine)
@@ -439,14 +498,16 @@ __device__ __forceinline__ bool fill_ring(const TcArgs& P, TreeWalk& w, const CU
       at.step(slots);
       ++filled;
       if (i == 0) {  // the next unit, while this one's copies are under way
-        some = w.next(P.a);
-        if (some) next.set(P, w, lane);
+        some = units.next(sh, next, ok, lane);
+        if (some) next_pages.set(P, next, lane);
+        if (!ok) break;
       }
     }
   }
   if (!ok) {  // copies that nobody waited for land before the block ends
     for (int e = filled > slots ? filled - slots : 0; e < filled; ++e)
-      mbar_wait(&full[e % slots], (e / slots) & 1, kSpin >> 4);
+      wait_on(&full[e % slots], (e / slots) & 1);
+    if (unit > 0) wait_on(&sh.q_full, (unit - 1) & 1);
   }
   return ok;
 }
@@ -470,6 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bar = sh.k_full;
     mbar_init(bar + lane, lane < 31 ? 1 : 8);
     if (lane < 7) mbar_init(bar + 32 + lane, 4);
+    if (lane < kUnits) {
+      mbar_init(&sh.u_full[lane], 1);
+      mbar_init(&sh.u_empty[lane], kUnitReaders);
+    }
     if (lane < 2) sh.add_first[lane] = 0;
     if (lane == 0) sh.failed = 0;
     fence_mbar_init();
@@ -481,15 +546,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   follow();
   tc_fence_before();
-  TreeWalk w = tree_start(a, sh.share);  // synchronises the block
+  tree_start(a, sh.share);  // synchronises the block
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   bool ok = true;
 
   if (warp == 0) {
-    ok = fill_ring<D>(P, w, &map_k, k_ring, sh.k_full, sh.k_empty, P.k_slots, lane);
+    ok = fill_ring<D>(P, sh, false, &map_k, &map_q, q_tile, k_ring, lane);
   } else if (warp == 3) {
-    ok = fill_ring<D>(P, w, &map_v, v_ring, sh.v_full, sh.v_empty, P.v_slots, lane);
+    ok = fill_ring<D>(P, sh, true, &map_v, &map_q, q_tile, v_ring, lane);
   } else if (warp == 1) {
     // -------------------------------------------------------- products
     // The whole warp runs this, so that descriptors stay in uniform
@@ -541,10 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (free_values) mma_commit(&sh.v_empty[v.slot]);
       }
     };
-    bool some = w.n > 0;
-    for (int unit = 0; ok && some; ++unit, some = w.next(a)) {
+    UnitReader units;
+    Unit w;
+#pragma unroll 1
+    for (int unit = 0; ok && units.next(sh, w, ok, lane); ++unit) {
       ok = wait_warp(&sh.q_full, unit & 1);
-      const bool both = w.q.cnt - w.rt * a.row_tokens > P.fit;
+      const bool both = w.both;
       if (ok) keys();
       if (!ok) break;
       scores(0, 0, !both, w.n == 1 && !both);
@@ -583,24 +650,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sh.drain, 0, kSpin >> 4);
     }
   } else if (warp == 2) {
-    // --------------------------------------------------------- queries
+    // ----------------------------------------------------------- units
     if (lane == 0) {
-      int unit = 0;
-      for (bool some = w.n > 0; ok && some; ++unit, some = w.next(a)) {
-        if (unit > 0) ok = wait(&sh.q_empty, (unit - 1) & 1);
+      TreeWalk w = sh.share.walk;
+      Place at{0, 1};
+      bool some = w.n > 0, first = true;
+#pragma unroll 1
+      while (true) {
+        ok = wait(&sh.u_empty[at.slot], at.parity);
         if (!ok) break;
-        const int t0 = w.rt * a.row_tokens;
-        const int tiles = w.q.cnt - t0 > P.fit ? 2 : 1;
-        mbar_arrive_expect_tx(&sh.q_full, tiles * S::halves * P.q_tokens * a.group * 128);
-        for (int i = 0; i < tiles * S::halves; ++i) {
-          const int tile = i / S::halves, half = i - tile * S::halves;
-          tma_5d(q_tile + i * kHalfBytes, &map_q, &sh.q_full, half * 64, 0, w.h,
-                 t0 + tile * P.fit, w.b);
+        Unit u{};
+        if (some) {
+          u.n = w.n;
+          u.key = (w.q.lo + w.first) * kTile;
+          u.s = w.q.s;
+          u.len = w.q.len;
+          u.cnt = w.q.cnt;
+          u.b = w.b;
+          u.h = w.h;
+          u.t0 = w.rt * a.row_tokens;
+          u.both = w.q.cnt - u.t0 > P.fit;
+          u.whole = w.whole;
         }
-        if (unit == 0) tree_describe(a, w);
+        sh.units[at.slot] = u;
+        mbar_arrive(&sh.u_full[at.slot]);
+        at.step(kUnits);
+        if (first) tree_describe(a, w);
+        first = false;
+        if (!some) break;
+        some = w.next(a);
       }
-      if (unit == 0) tree_describe(a, w);
-      if (!ok && unit > 0) mbar_wait(&sh.q_full, (unit - 1) & 1, kSpin >> 4);
     }
   } else {
     // --------------------------------------------------------- softmax
@@ -611,22 +690,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;                       // tiles of the units before
     uint32_t used = 0, syncs = 0, alls = 0, joins = 0;  // phases of the barriers
     bool is_first = true;            // the block's first unit
-    bool some = w.n > 0;
-    for (; ok && some; g += w.n, some = w.next(a)) {
-      const int t_unit = w.rt * a.row_tokens, left = w.q.cnt - t_unit;
-      const bool both = left > P.fit;             // half the rows each
-      const int t0 = t_unit + (both && st ? P.fit : 0);
-      const int more = w.q.cnt - t0, tokens = more < P.fit ? more : P.fit;
+    // the row's token and head within a query tile
+    const int r_token = (int)((uint32_t)r / (uint32_t)a.group), r_head = r - r_token * a.group;
+    UnitReader units;
+    Unit w;
+#pragma unroll 1
+    for (; ok && units.next(sh, w, ok, lane); g += w.n) {
+      const int left = w.cnt - w.t0;
+      const bool both = w.both;                   // half the rows each
+      const int t0 = w.t0 + (both && st ? P.fit : 0);
+      const int more = w.cnt - t0, tokens = more < P.fit ? more : P.fit;
       const int rows = tokens * a.group;
-      const int t = t0 + r / a.group;
+      const int t = t0 + r_token;
       const bool valid = r < rows, any = quarter * 32 < rows;
-      const uint64_t bits = valid ? tree_mask(a, w.b, t, w.q.cnt) : 0;
-      const int len = w.q.len;
+      const uint64_t bits = valid ? tree_mask(a, w.b, t, w.cnt) : 0;
+      const int len = w.len;
       const Sight sight{valid ? tree_window_lo(a, w.b, t, len) : 0, len, bits};
       int lo_most = 0;  // committed keys below this are hidden from some row
       if (a.window > 0) {
         for (int i = lane; i < left && i < a.row_tokens; i += 32) {
-          const int x = tree_window_lo(a, w.b, t_unit + i, len);
+          const int x = tree_window_lo(a, w.b, w.t0 + i, len);
           lo_most = x > lo_most ? x : lo_most;
         }
         lo_most = __reduce_max_sync(0xffffffffu, lo_most);
@@ -637,8 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the same code over whatever O holds, so that it is there when they
       // come.  O is this stream's own until its first weights are ready.
       bool real = is_first ? first >= w.n : true;
+#pragma unroll 1
       for (int tile = first; tile < w.n && ok;) {
-        const int j0 = (w.q.lo + w.first + tile) * kTile;
+        const int j0 = w.key + tile * kTile;
         const bool masked = j0 + kTile > len || j0 < lo_most;
         const uint32_t s_at = lanes + (real ? S::s_col(st) : S::o_col(st));
         const uint32_t p_at = lanes + (real ? S::p_col(st) : S::o_col(st));
@@ -716,9 +800,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (found) {
             if (any) {
               if (tile == first) {  // O starts from what is added here
+#pragma unroll 1
                 for (int d = 0; d < D; ++d) tmem_st1(o_at + d, 0);
                 tmem_st_wait();
               }
+#pragma unroll 1
               for (int j = 0; j < kTile; ++j) {
                 const uint32_t word = j < 64 ? (j < 32 ? rows_bad[0] : rows_bad[1])
                                              : (j < 96 ? rows_bad[2] : rows_bad[3]);
@@ -727,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 const float p = __uint_as_float(j & 1 ? pp & 0xffff0000u : pp << 16);
                 const bool sees = seen32(j0 + j, sight.lo, sight.len, sight.bits) & 1;
+#pragma unroll 1
                 for (int d = 0; d < D; ++d) {
                   const uint16_t u = *reinterpret_cast<const uint16_t*>(
                       v + (d >> 6) * kHalfBytes + j * 128 + ((((d & 63) >> 3) ^ (j & 7)) << 4) + (d & 7) * 2);
@@ -747,6 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_warp(bar, phase++ & 1);
             if (!ok) break;
             if ((!both || st == 0) && ((rows_bad[quarter] >> lane) & 1)) {
+#pragma unroll 1
               for (int d = 0; d < D; ++d) {
                 uint16_t* u = reinterpret_cast<uint16_t*>(
                     v + (d >> 6) * kHalfBytes + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2);
@@ -800,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = now;
         }
         if (any) {
-          const size_t row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r % a.group;
-          const int part_row = (t0 - t_unit) * a.group + r;
+          const size_t row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
+          const int part_row = (t0 - w.t0) * a.group + r;
           const float inv = w.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
@@ -934,7 +1022,8 @@ bool tree_tc_supported(const TreeArgs& a) {
 }
 
 cudaError_t launch_tree_tc(TreeArgs& a, int sms, cudaStream_t stream) {
-  a.tile = kTile;
+  a.tile_shift = 7;
+  static_assert(kTile == 1 << 7, "tile");
   const int fit = kTreeRows / a.group;  // tokens of a stream's rows
   a.row_tokens = a.T <= fit ? fit : 2 * fit;
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
