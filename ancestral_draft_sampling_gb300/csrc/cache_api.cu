@@ -44,8 +44,7 @@ dspark_status check_heads(int heads, int kv_heads) {
 }
 
 // The workspace of the attention: what the merge has to do, then the partial
-// results.  The FFMA kernel runs two blocks of 32 rows a
-// multiprocessor.
+// results, two a block; no kernel has larger units than the tensor-core one.
 struct TreeLayout {
   size_t part, total;
 };
@@ -55,9 +54,6 @@ TreeLayout tree_layout(int T, int group, int D) {
   L.part = align_up((size_t)2 * kTreeMaxBlocks * sizeof(TreeJoin), 256);
   const int fit = 2 * (kTreeRows / group);  // drafted tokens of a tensor-core unit
   size_t rows = (size_t)(T < fit ? T : fit) * group * 2 * kTreeMaxBlocks;
-  const int fit32 = 32 / group;
-  const size_t rows32 = (size_t)(T < fit32 ? T : fit32) * group * 4 * kTreeMaxBlocks;
-  if (rows32 > rows) rows = rows32;
   L.total = align_up(L.part + rows * (D + 2) * sizeof(float), 256);
   return L;
 }

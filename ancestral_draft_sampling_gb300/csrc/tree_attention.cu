@@ -5,11 +5,18 @@
 // One pass over a unit's keys with the running maximum m and sum l of each
 // row: for a tile, s = scale q.k, m' = max(m, max s), p = exp(s - m'),
 // l' = l e^(m - m') + sum p, o' = o e^(m - m') + p v.  All of it is float32.
-// Eight warps hold four rows each, so a row's statistics stay in one warp and
-// its weights p never leave it but for a small buffer of its own; keys and
-// values of a tile are shared.  A tile is 64 keys by 32 rows.  Bound by the
-// FFMA rate and by shared memory (6 loads of 16 bytes for 32 multiply-adds of
-// the scores, 2 for 16 of the sums).
+//
+// Scores are in units of log2, so that a weight is one ex2.
+//
+// Sixteen warps share a tile of 64 keys (32 where head_dim is above 128) in
+// shared memory.  A warp holds four or eight rows, and two to sixteen groups
+// of warps take the same rows and part of the keys each, with statistics of
+// their own (a row's maximum is the warp's; its sum stays spread over the
+// lanes); the groups are joined at the unit's end.  The next tile, of whatever
+// unit, is copied (cp.async) while one is worked on, and the pages of the one
+// behind it are looked up.  Products are packed, two a lane.  Eight warps of
+// two keys a lane waited for shared memory and shuffles half of the time
+// (119 us for 8 x 8 tokens, 4 x 8 heads, 2000 keys of 128).
 #include "dspark_common.cuh"
 #include "host_util.cuh"
 #include "sm100_ptx.cuh"
@@ -18,8 +25,7 @@
 namespace dspark {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRows = 32, kTile = 64;
+constexpr int kWarps = 16, kThreads = 32 * kWarps, kRowGroups = 8;
 
 __device__ __forceinline__ float4 load4(const float* p) {
   return *reinterpret_cast<const float4*>(p);
@@ -38,177 +44,339 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
                                             *reinterpret_cast<const uint32_t*>(&b));
 }
 
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+// Two partial sums of a dot product.
+__device__ __forceinline__ uint64_t dot4(float4 a, float4 b, uint64_t c) {
+  return fma2(pair(a.z, a.w), pair(b.z, b.w), fma2(pair(a.x, a.y), pair(b.x, b.y), c));
 }
 
-// ND: chunks of 128 dims that a lane's four cover (1: D <= 128, 2: D <= 256).
-template <typename T, int ND>
-__global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
-    tree_ffma_kernel(const __grid_constant__ TreeArgs a) {
-  extern __shared__ __align__(16) float smem[];
+// 16 bytes to shared memory, or zeros where `there` is false.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool there) {
+  const int n = there ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(to)), "l"(from),
+               "r"(n)
+               : "memory");
+}
+
+// Shared memory of a block, in bytes.
+template <typename T, int ND, int RW>
+struct Tiles {
+  static constexpr int kTile = ND == 1 ? 64 : 32;  // keys
+  static constexpr int kRows = kRowGroups * RW;    // rows of a unit
+  int D;
+  __host__ __device__ int pad() const { return D + 16 / (int)sizeof(T); }  // rows on different banks
+  __host__ __device__ int key_bytes() const { return kTile * pad() * (int)sizeof(T); }
+  __host__ __device__ int value_bytes() const { return kTile * D * (int)sizeof(T); }
+  __host__ __device__ int stage() const { return key_bytes() + value_bytes(); }
+  // the queries, and at a unit's end the parts that groups leave each other
+  __host__ __device__ int q_at() const { return 2 * stage(); }
+  __host__ __device__ int p_at() const { return q_at() + kRows * (D + 4) * 4; }
+  __host__ __device__ int where_at() const { return p_at() + kWarps * (kTile / 2) * RW * 8; }
+  __host__ __device__ int total() const { return where_at() + 2 * kTile * 8; }
+};
+
+// A tile of the block's line, one ahead of the work.
+struct NextTile {
+  TreeWalk w;
+  int i;      // within the unit
+  bool some;
+  __device__ __forceinline__ void step(const TreeArgs& a) {
+    if (++i < w.n) return;
+    i = 0;
+    some = w.next(a);
+  }
+};
+
+// ND: chunks of 128 dims that a lane's four cover (1: D <= 128, 2: D <= 256);
+// RW: rows of a warp.
+template <typename T, int ND, int RW>
+__global__ void __launch_bounds__(kThreads)
+    tree_ffma_kernel(const __grid_constant__ TreeArgs a, int row_groups) {
+  using L = Tiles<T, ND, RW>;
+  constexpr int kTile = L::kTile;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ TreeShare share;
-  const int D = a.c.head_dim, DP = D + 4;  // padded rows: lanes on different banks
-  float* qs = smem;                        // [kRows][DP], scaled
-  float* ks = qs + kRows * DP;             // [kTile][DP]
-  float* vs = ks + kTile * DP;             // [kTile][D]
-  float* ps = vs + kTile * D;              // [kWarps][kTile][4]
+  __shared__ uchar2 row_of[L::kRows];  // a row's token and head
+  const int D = a.c.head_dim, DP = D + 4;
+  const L layout{D};
+  const int pad = layout.pad(), words = D * (int)sizeof(T) / 16;
+  float* qs = reinterpret_cast<float*>(smem + layout.q_at());  // [kRows][DP], scaled
+  long long* where = reinterpret_cast<long long*>(smem + layout.where_at());  // [2][kTile]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // weights, each twice: the pair that a packed product takes
+  uint64_t* pw = reinterpret_cast<uint64_t*>(smem + layout.p_at()) + warp * (kTile / 2) * RW;
+  // the warp's rows and keys
+  const int key_groups = kWarps / row_groups, rg = warp & (row_groups - 1), kg = warp / row_groups;
+  const int keys = kTile / key_groups, key0 = kg * keys;
   const T* q = static_cast<const T*>(a.q);
-  const T* pool = static_cast<const T*>(a.c.pool);
-  float* pw = ps + warp * kTile * 4;
+  const char* pool = static_cast<const char*>(a.c.pool);
+  if (threadIdx.x < L::kRows) {
+    const uint32_t t = threadIdx.x / (uint32_t)a.group;
+    row_of[threadIdx.x] = make_uchar2(t, threadIdx.x - t * a.group);
+  }
+  const float c = a.scale * 1.4426950408889634f;
   follow();
   tree_start(a, share);
+  NextTile ahead{share.walk, 0, share.walk.n > 0};
   TreeWalk w = share.walk;
-  if (threadIdx.x == kThreads - 1) tree_describe(a, w);
+
+  // Where a tile's keys lie (bytes from the start of the pool, -1: zeros), a
+  // key a thread: the page is loaded first and used when the tile before is
+  // done.
+  int look_page = -1, look_slot = 0, look_head = 0;
+  bool look_there = false;
+  auto look = [&]() {
+    look_there = false;
+    if (threadIdx.x < kTile && ahead.some) {
+      const int j = ((ahead.w.q.lo + ahead.w.first + ahead.i) * kTile) + threadIdx.x;
+      look_head = ahead.w.h;
+      look_there = j < ahead.w.q.len + ahead.w.q.cnt;
+      if (look_there)
+        look_page = a.c.block_table[(size_t)ahead.w.q.s * a.c.max_pages +
+                                    page_of(a.c, (uint32_t)j, look_slot)];
+    }
+  };
+  auto found = [&](int buffer) {
+    if (threadIdx.x < kTile) {
+      long long at = -1;
+      if (look_there) {
+        if (look_page >= 0 && look_page < a.c.num_pages)
+          at = (long long)cache_row(a.c, 2 * a.layer, look_page, look_head, look_slot);
+        else
+          cache_error(a.c, kCacheErrPage);
+      }
+      where[buffer * kTile + threadIdx.x] = at;
+    }
+  };
+  const size_t to_values = cache_row(a.c, 1, 0, 0, 0);
+  const int row_step = kThreads / words, word_step = kThreads - row_step * words;
+  const int copy_row = (int)threadIdx.x / words, copy_word = (int)threadIdx.x - copy_row * words;
+  auto copy = [&](int buffer) {
+    uint8_t* stage = smem + buffer * layout.stage();
+    int r = copy_row, d = copy_word;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < 2 * kTile * words; i += kThreads) {
+      const bool value = r >= kTile;
+      const int key = value ? r - kTile : r;
+      const long long at = where[buffer * kTile + key];
+      uint8_t* to = value ? stage + layout.key_bytes() + key * D * (int)sizeof(T)
+                          : stage + key * pad * (int)sizeof(T);
+      copy16(to + 16 * d, pool + (at < 0 ? 0 : at + (value ? to_values : 0)) + 16 * d, at >= 0);
+      r += row_step;
+      d += word_step;
+      if (d >= words) {
+        d -= words;
+        ++r;
+      }
+    }
+  };
+  // the first tile, and where the second lies
+  look();
+  found(0);
+  __syncthreads();
+  if (ahead.some) {
+    copy(0);
+    ahead.step(a);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  look();
+  found(1);
+  int n = 0;  // tiles worked on
   bool is_first = true;
   for (bool some = w.n > 0; some; some = w.next(a)) {
     const int t0 = w.rt * a.row_tokens;
     const int rows = (w.q.cnt - t0 < a.row_tokens ? w.q.cnt - t0 : a.row_tokens) * a.group;
     const int head0 = w.h * a.group;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-      float4 x = make_float4(0, 0, 0, 0);
-      if (r < rows) {
-        const int t = t0 + r / a.group, g = r % a.group;
-        x = load4(q + (((size_t)w.b * a.T + t) * a.heads + head0 + g) * D + d);
-        x = make_float4(x.x * a.scale, x.y * a.scale, x.z * a.scale, x.w * a.scale);
-      }
-      *reinterpret_cast<float4*>(qs + r * DP + d) = x;
+    __syncthreads();  // the last unit's queries are used up
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int r = (int)((uint32_t)i / (uint32_t)(D / 4)), d = (i - r * (D / 4)) * 4;
+      const int t = t0 + row_of[r].x, g = row_of[r].y;
+      const float4 x = load4(q + (((size_t)w.b * a.T + t) * a.heads + head0 + g) * D + d);
+      *reinterpret_cast<float4*>(qs + r * DP + d) =
+          make_float4(x.x * c, x.y * c, x.z * c, x.w * c);
     }
-    // the warp's four rows
-    float m[4], l[4];
-    float4 o[4][ND];
-    uint64_t bits[4];
-    int lo[4];
+    float m[RW], l[RW];
+    uint64_t o[RW][ND][2];
+    uint64_t bits[RW];
+    int lo[RW];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = warp * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+      const int r = rg * RW + i;
       m[i] = -INFINITY;
       l[i] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < ND; ++n) o[i][n] = make_float4(0, 0, 0, 0);
+      for (int x = 0; x < ND; ++x) o[i][x][0] = o[i][x][1] = 0;
       bits[i] = 0;
       lo[i] = w.q.len;
       if (r < rows) {
-        const int t = t0 + r / a.group;
+        const int t = t0 + row_of[r].x;
         bits[i] = tree_mask(a, w.b, t, w.q.cnt);
         lo[i] = tree_window_lo(a, w.b, t, w.q.len);
       }
     }
     const int total = w.q.len + w.q.cnt;
-    for (int tile = 0; tile < w.n; ++tile) {
+    const bool busy = rg * RW < rows;
+#pragma unroll 1
+    for (int tile = 0; tile < w.n; ++tile, ++n) {
       const int j0 = (w.q.lo + w.first + tile) * kTile;
-      __syncthreads();  // the last tile's keys and values are used up
-      for (int i = threadIdx.x; i < 2 * kTile * (D / 4); i += kThreads) {
-        const bool val = i >= kTile * (D / 4);
-        const int e = val ? i - kTile * (D / 4) : i;
-        const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-        float4 x = make_float4(0, 0, 0, 0);
-        if (j0 + r < total) {
-          const int page = cache_page(a.c, w.q.s, (j0 + r) / a.c.page_size, a.c.max_pages);
-          if (page >= 0)
-            x = load4(pool + cache_row(a.c, 2 * a.layer + (val ? 1 : 0), page, w.h,
-                                       (j0 + r) % a.c.page_size) / sizeof(T) + d);
-          else
-            cache_error(a.c, kCacheErrPage);
-        }
-        if (val) *reinterpret_cast<float4*>(vs + r * D + d) = x;
-        else *reinterpret_cast<float4*>(ks + r * DP + d) = x;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();  // the tile is there, and the one before it is used up
+      if (ahead.some) {
+        copy((n + 1) & 1);
+        ahead.step(a);
       }
-      __syncthreads();
-      if (warp * 4 >= rows) continue;
-      float s[4][2];
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      look();
+      if (!busy) {
+        found(n & 1);
+        continue;
+      }
+      const T* ks = reinterpret_cast<const T*>(smem + (n & 1) * layout.stage());
+      const T* vs = reinterpret_cast<const T*>(smem + (n & 1) * layout.stage() + layout.key_bytes());
+      // the score of a key a lane
+      const int k0 = key0 + (lane < keys ? lane : 0);
+      uint64_t s2[RW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.0f;
+      for (int i = 0; i < RW; ++i) s2[i] = 0;
+      const float* qr = qs + rg * RW * DP;
+#pragma unroll 2
       for (int d = 0; d < D; d += 4) {
-        const float4 k0 = load4(ks + lane * DP + d), k1 = load4(ks + (lane + 32) * DP + d);
+        const float4 x0 = load4(ks + k0 * pad + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x = load4(qs + (warp * 4 + i) * DP + d);
-          s[i][0] = dot4(x, k0, s[i][0]);
-          s[i][1] = dot4(x, k1, s[i][1]);
-        }
+        for (int i = 0; i < RW; ++i) s2[i] = dot4(load4(qr + i * DP + d), x0, s2[i]);
       }
-      uint64_t seen[4];  // the tile's keys that the row sees
-      uint64_t all = ~0ull;
+      const int j = j0 + key0 + lane;
+      const uint32_t full = keys >= 32 ? ~0u : (1u << keys) - 1;
+      uint32_t seen[RW];  // the warp's keys that the row sees
+      bool all = true;
+      float s[RW], now[RW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bool see[2];
+      for (int i = 0; i < RW; ++i) {
+        const float2 x = unpair(s2[i]);
+        s[i] = x.x + x.y;
+        const bool see = lane < keys && (j < w.q.len ? j >= lo[i]
+                                                     : j < total && ((bits[i] >> (j - w.q.len)) & 1));
+        seen[i] = __ballot_sync(0xffffffffu, see);
+        all &= seen[i] == full;
+        if (!see) s[i] = -INFINITY;
+      }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int j = j0 + lane + 32 * n;
-          see[n] = j < w.q.len ? j >= lo[i]
-                               : j < total && ((bits[i] >> (j - w.q.len)) & 1);
-          if (!see[n]) s[i][n] = -INFINITY;
+      for (int i = 0; i < RW; ++i)  // a NaN is no maximum
+        now[i] = fmaxf(m[i], from_ordered_bits(__reduce_max_sync(
+                                 0xffffffffu, ordered_bits(s[i] == s[i] ? s[i] : -INFINITY))));
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const float keep = m[i] == now[i] ? 1.0f : ex2(m[i] - now[i]);
+        const float p = ((seen[i] >> lane) & 1) && s[i] != -INFINITY ? ex2(s[i] - now[i]) : 0.0f;
+        l[i] = l[i] * keep + p;  // the lane's keys
+        m[i] = now[i];
+#pragma unroll
+        for (int x = 0; x < ND; ++x) {
+          o[i][x][0] = mul2(o[i][x][0], pair(keep, keep));
+          o[i][x][1] = mul2(o[i][x][1], pair(keep, keep));
         }
-        seen[i] = __ballot_sync(0xffffffffu, see[0]) |
-                  (uint64_t)__ballot_sync(0xffffffffu, see[1]) << 32;
-        all &= seen[i];
-        float top = fmaxf(s[i][0], s[i][1]);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float now = fmaxf(m[i], top);
-        const float keep = m[i] == now ? 1.0f : expf(m[i] - now);
-        const float p0 = see[0] && s[i][0] != -INFINITY ? expf(s[i][0] - now) : 0.0f;
-        const float p1 = see[1] && s[i][1] != -INFINITY ? expf(s[i][1] - now) : 0.0f;
-        float sum = p0 + p1;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l[i] = l[i] * keep + sum;
-        m[i] = now;
-#pragma unroll
-        for (int n = 0; n < ND; ++n) {
-          o[i][n].x *= keep;
-          o[i][n].y *= keep;
-          o[i][n].z *= keep;
-          o[i][n].w *= keep;
-        }
-        pw[lane * 4 + i] = p0;
-        pw[(lane + 32) * 4 + i] = p1;
+        if (lane < keys) pw[lane * RW + i] = pair(p, p);
       }
       __syncwarp();
-      // a key that a row does not see is left out, whatever its values hold
-#pragma unroll 4
-      for (int j = 0; j < kTile; ++j) {
-        const float4 p = load4(pw + j * 4);
-        const float pr[4] = {p.x, p.y, p.z, p.w};
+      auto add = [&](int j, bool every) {
+        ulonglong2 p[RW / 2];
 #pragma unroll
-        for (int n = 0; n < ND; ++n) {
-          const int d = n * 128 + lane * 4;
+        for (int i = 0; i < RW / 2; ++i)
+          p[i] = *reinterpret_cast<const ulonglong2*>(pw + j * RW + 2 * i);
+#pragma unroll
+        for (int x = 0; x < ND; ++x) {
+          const int d = x * 128 + lane * 4;
           if (d < D) {
-            const float4 v = load4(vs + j * D + d);
+            const float4 v = load4(vs + (key0 + j) * D + d);
+            const uint64_t v0 = pair(v.x, v.y), v1 = pair(v.z, v.w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (all != ~0ull && !((seen[i] >> j) & 1)) continue;
-              o[i][n].x = fmaf(pr[i], v.x, o[i][n].x);
-              o[i][n].y = fmaf(pr[i], v.y, o[i][n].y);
-              o[i][n].z = fmaf(pr[i], v.z, o[i][n].z);
-              o[i][n].w = fmaf(pr[i], v.w, o[i][n].w);
+            for (int i = 0; i < RW; ++i) {
+              if (!every && !((seen[i] >> j) & 1)) continue;
+              const uint64_t pi = i & 1 ? p[i / 2].y : p[i / 2].x;
+              o[i][x][0] = fma2(pi, v0, o[i][x][0]);
+              o[i][x][1] = fma2(pi, v1, o[i][x][1]);
+            }
+          }
+        }
+      };
+      if (all) {
+#pragma unroll 4
+        for (int j = 0; j < keys; ++j) add(j, true);
+      } else {  // a key that a row does not see is left out, whatever its values hold
+#pragma unroll 1
+        for (int j = 0; j < keys; ++j) add(j, false);
+      }
+      __syncwarp();
+      found(n & 1);
+    }
+    // the lanes' sums
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+    const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
+    is_first = false;
+    {  // the groups' parts, one after the other into the first group's
+#pragma unroll 1
+      for (int g = 1; g < key_groups; ++g) {
+        __syncthreads();
+        if (kg == g && busy) {
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            float* at = qs + (rg * RW + i) * DP;
+#pragma unroll
+            for (int x = 0; x < ND; ++x) {
+              const int d = x * 128 + lane * 4;
+              if (d < D) {
+                *reinterpret_cast<uint64_t*>(at + d) = o[i][x][0];
+                *reinterpret_cast<uint64_t*>(at + d + 2) = o[i][x][1];
+              }
+            }
+            if (lane == 0) {
+              at[D] = m[i];
+              at[D + 1] = l[i];
+            }
+          }
+        }
+        __syncthreads();
+        if (kg == 0 && busy) {
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            const float* at = qs + (rg * RW + i) * DP;
+            const float om = at[D], now = fmaxf(m[i], om);
+            const float f = m[i] == now ? 1.0f : ex2(m[i] - now);
+            const float g2 = om == now ? 1.0f : ex2(om - now);
+            l[i] = l[i] * f + at[D + 1] * g2;
+            m[i] = now;
+#pragma unroll
+            for (int x = 0; x < ND; ++x) {
+              const int d = x * 128 + lane * 4;
+              if (d < D) {
+                const uint64_t gg = pair(g2, g2), ff = pair(f, f);
+                o[i][x][0] = fma2(*reinterpret_cast<const uint64_t*>(at + d), gg, mul2(o[i][x][0], ff));
+                o[i][x][1] = fma2(*reinterpret_cast<const uint64_t*>(at + d + 2), gg, mul2(o[i][x][1], ff));
+              }
             }
           }
         }
       }
-      __syncwarp();
     }
-    const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
-    is_first = false;
+    if (kg > 0) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = warp * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+      const int r = rg * RW + i;
       if (r >= rows) break;
-      const int t = t0 + r / a.group, g = r % a.group;
+      const int t = t0 + row_of[r].x, g = row_of[r].y;
       const size_t row = ((size_t)w.b * a.T + t) * a.heads + head0 + g;
       const float inv = w.whole ? (l[i] == 0.0f ? 0.0f : 1.0f / l[i]) : 1.0f;
 #pragma unroll
-      for (int n = 0; n < ND; ++n) {
-        const int d = n * 128 + lane * 4;
+      for (int x = 0; x < ND; ++x) {
+        const int d = x * 128 + lane * 4;
         if (d >= D) continue;
-        const float4 x = make_float4(o[i][n].x * inv, o[i][n].y * inv, o[i][n].z * inv,
-                                     o[i][n].w * inv);
-        if (w.whole) put4(static_cast<T*>(a.out) + row * D + d, x);
-        else put4(tree_part(a, slot) + (size_t)r * D + d, x);
+        const float2 x0 = unpair(o[i][x][0]), x1 = unpair(o[i][x][1]);
+        const float4 y = make_float4(x0.x * inv, x0.y * inv, x1.x * inv, x1.y * inv);
+        if (w.whole) put4(static_cast<T*>(a.out) + row * D + d, y);
+        else put4(tree_part(a, slot) + (size_t)r * D + d, y);
       }
       if (lane == 0) {
         if (!w.whole) {
@@ -216,132 +384,177 @@ __global__ void __launch_bounds__(kThreads, ND == 1 ? 2 : 1)
           st[0] = m[i];
           st[1] = l[i];
         } else if (a.lse) {
-          a.lse[row] = l[i] == 0.0f ? -INFINITY : m[i] + logf(l[i]);
+          a.lse[row] = l[i] == 0.0f ? -INFINITY : m[i] * a.stat_ln + logf(l[i]);
         }
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // behind the work, so that the first tile does not wait for it
+  if (threadIdx.x == 0) tree_describe(a, share.walk);
 }
 
 // Joins the partial results of the units that several blocks worked on: a
-// warp for each row, o = sum_c e^(m_c - M) o_c / sum_c e^(m_c - M) l_c over
-// the unit's blocks c in order, M the largest m_c.
-constexpr int kMergeWarps = 4, kMergeBatch = 4;
+// warp for kRows rows, o = sum_c e^(m_c - M) o_c / sum_c e^(m_c - M) l_c over
+// the unit's blocks c in order, M the largest m_c.  Bound by latency, so the
+// loads of eight parts are in flight together: one row's of eight blocks, or,
+// where units have many rows, four rows' of two (a warp a row takes 18 us for
+// 150 units of 256 rows, against 11; four rows a warp take 5 us more than one
+// for units of 32 rows over eight blocks).
+constexpr int kMergeWarps = 4;
 
-template <typename T>
+template <typename T, int ND, int kRows>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   follow();
   const TreeJoin j = a.join[blockIdx.x + 1];  // nothing cuts the line's start
   const int lane = threadIdx.x & 31, D = a.c.head_dim;
-  const int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  if (r >= j.rows) return;
-  const int c0 = j.first, c1 = j.last, slot0 = j.slot;
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32)
-    M = fmaxf(M, tree_part_stats(a, c == c0 ? slot0 : 2 * c)[2 * r]);
+  const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kRows;
+  if (r0 >= j.rows) return;
+  const int parts = j.last - j.first + 1;
+  auto slot_of = [&](int i) { return i == 0 ? j.slot : 2 * (j.first + i); };
+  float M[kRows], L[kRows];
+  float4 o[kRows][ND];
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float L = 0.0f;
-  float4 o[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-  for (int cb = c0; cb <= c1; cb += 32) {
-    const int n = c1 - cb + 1 < 32 ? c1 - cb + 1 : 32;
-    float wt = 0.0f, lw = 0.0f;
-    if (lane < n) {
-      const int c = cb + lane;
-      const float* st = tree_part_stats(a, c == c0 ? slot0 : 2 * c) + 2 * r;
-      wt = st[0] == M ? 1.0f : exp2f((st[0] - M) * a.stat_log2);  // saw nothing: 0
-      if (M == -INFINITY) wt = 0.0f;
-      lw = wt * st[1];
+  for (int i = 0; i < kRows; ++i) {
+    M[i] = -INFINITY;
+    L[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < ND; ++k) o[i][k] = make_float4(0, 0, 0, 0);
+  }
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (p0 + lane < parts && r0 + i < j.rows)
+        M[i] = fmaxf(M[i], tree_part_stats(a, slot_of(p0 + lane))[2 * (r0 + i)]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], x));
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    const int n = parts - p0 < 32 ? parts - p0 : 32;
+    float w[kRows], lw[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      w[i] = lw[i] = 0.0f;
+      if (lane < n && r0 + i < j.rows) {
+        const float2 st =
+            *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p0 + lane)) + 2 * (r0 + i));
+        // a part that saw nothing weighs nothing
+        if (M[i] != -INFINITY) w[i] = st.x == M[i] ? 1.0f : exp2f((st.x - M[i]) * a.stat_log2);
+        lw[i] = w[i] * st.y;
+      }
     }
-    for (int i0 = 0; i0 < n; i0 += kMergeBatch) {  // loads of a batch in flight
-      float4 x[kMergeBatch][2];
+    constexpr int kBatch = 8 / kRows;
+#pragma unroll 1
+    for (int p = 0; p < n; p += kBatch) {
+      float4 x[kBatch][kRows][ND];
 #pragma unroll
-      for (int i = 0; i < kMergeBatch; ++i) {
-        const int c = cb + i0 + i;
-        const float* part = tree_part(a, c == c0 ? slot0 : 2 * c) + (size_t)r * D;
+      for (int q = 0; q < kBatch; ++q) {
+        const float* part = tree_part(a, slot_of(p0 + p + q)) + (size_t)r0 * D;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int d = k * 128 + lane * 4;
-          x[i][k] = make_float4(0, 0, 0, 0);
-          if (i0 + i < n && d < D) x[i][k] = load4(part + d);
-        }
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int k = 0; k < ND; ++k) {
+            const int d = k * 128 + lane * 4;
+            x[q][i][k] = make_float4(0, 0, 0, 0);
+            if (p + q < n && d < D && r0 + i < j.rows) x[q][i][k] = load4(part + i * D + d);
+          }
       }
 #pragma unroll
-      for (int i = 0; i < kMergeBatch; ++i) {
-        if (i0 + i >= n) break;
-        const float wi = __shfl_sync(0xffffffffu, wt, i0 + i);
-        L += __shfl_sync(0xffffffffu, lw, i0 + i);
+      for (int q = 0; q < kBatch; ++q) {
+        if (p + q >= n) break;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          o[k].x = fmaf(wi, x[i][k].x, o[k].x);
-          o[k].y = fmaf(wi, x[i][k].y, o[k].y);
-          o[k].z = fmaf(wi, x[i][k].z, o[k].z);
-          o[k].w = fmaf(wi, x[i][k].w, o[k].w);
+        for (int i = 0; i < kRows; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w[i], p + q);
+          L[i] += __shfl_sync(0xffffffffu, lw[i], p + q);
+#pragma unroll
+          for (int k = 0; k < ND; ++k) {
+            o[i][k].x = fmaf(wi, x[q][i][k].x, o[i][k].x);
+            o[i][k].y = fmaf(wi, x[q][i][k].y, o[i][k].y);
+            o[i][k].z = fmaf(wi, x[q][i][k].z, o[i][k].z);
+            o[i][k].w = fmaf(wi, x[q][i][k].w, o[i][k].w);
+          }
         }
       }
     }
   }
-  const size_t row =
-      ((size_t)j.b * a.T + j.t0 + r / a.group) * a.heads + j.h * a.group + r % a.group;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = k * 128 + lane * 4;
-    if (d < D)
-      put4(static_cast<T*>(a.out) + row * D + d,
-           make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+  for (int i = 0; i < kRows; ++i) {
+    const uint32_t r = r0 + i;
+    if ((int)r >= j.rows) break;
+    const uint32_t t = r / (uint32_t)a.group;
+    const size_t row = ((size_t)j.b * a.T + j.t0 + t) * a.heads + j.h * a.group + (r - t * a.group);
+    const float inv = L[i] == 0.0f ? 0.0f : 1.0f / L[i];
+#pragma unroll
+    for (int k = 0; k < ND; ++k) {
+      const int d = k * 128 + lane * 4;
+      if (d < D)
+        put4(static_cast<T*>(a.out) + row * D + d,
+             make_float4(o[i][k].x * inv, o[i][k].y * inv, o[i][k].z * inv, o[i][k].w * inv));
+    }
+    if (lane == 0 && a.lse)
+      a.lse[row] = L[i] == 0.0f ? -INFINITY : M[i] * a.stat_ln + logf(L[i]);
   }
-  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * a.stat_ln + logf(L);
 }
 
-// Dynamic shared memory a block may have beside its few static words.
-constexpr int kMaxDynamic = 232448 - 1024;
-
-template <typename T, int ND>
-cudaError_t launch_ffma(const TreeArgs& a, size_t smem, cudaStream_t stream) {
+template <typename T, int ND, int RW>
+cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
+  using L = Tiles<T, ND, RW>;
   static std::once_flag once[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::call_once(once[dev], [] {
-    cudaFuncSetAttribute(tree_ffma_kernel<T, ND>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         kMaxDynamic);
+    cudaFuncSetAttribute(tree_ffma_kernel<T, ND, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         L{ND * 128}.total());
   });
-  return launch_behind(tree_ffma_kernel<T, ND>, a.blocks, kThreads, smem, stream, a);
+  a.tile_shift = L::kTile == 64 ? 6 : 5;
+  a.row_tokens = L::kRows / a.group;
+  a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
+  a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
+  a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
+  a.stat_log2 = 1.0f;
+  a.stat_ln = 0.6931471805599453f;
+  // warps side by side over the rows that a unit has; the rest share the keys
+  int groups = 1;
+  while (groups < kRowGroups && groups * RW < a.slot_rows) groups *= 2;
+  return launch_behind(tree_ffma_kernel<T, ND, RW>, a.blocks, kThreads, L{a.c.head_dim}.total(),
+                       stream, a, groups);
+}
+
+template <typename T>
+cudaError_t launch_ffma_rows(TreeArgs& a, int sms, cudaStream_t stream) {
+  if (a.c.head_dim > 128) return launch_ffma<T, 2, 4>(a, sms, stream);
+  // eight rows a warp halve the shared memory reads of a product, where there
+  // are the rows
+  return a.T * a.group > 32 ? launch_ffma<T, 1, 8>(a, sms, stream)
+                            : launch_ffma<T, 1, 4>(a, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
-  const int D = a.c.head_dim;
-  a.tile_shift = 6;
-  static_assert(kTile == 1 << 6, "tile");
-  a.row_tokens = kRows / a.group;
-  a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
-  a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
-  a.stat_log2 = 1.4426950408889634f;
-  a.stat_ln = 1.0f;
-  const size_t smem = sizeof(float) * ((size_t)(kRows + kTile) * (D + 4) +
-                                       (size_t)kTile * D + kWarps * kTile * 4);
-  // two blocks a multiprocessor where shared memory allows it (D <= 128)
-  a.blocks = (smem * 2 + 4096 <= (size_t)kMaxDynamic ? 2 : 1) *
-             (sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks);
-  if (a.c.dtype == DSPARK_F32)
-    return D <= 128 ? launch_ffma<float, 1>(a, smem, stream)
-                    : launch_ffma<float, 2>(a, smem, stream);
-  return D <= 128 ? launch_ffma<__nv_bfloat16, 1>(a, smem, stream)
-                  : launch_ffma<__nv_bfloat16, 2>(a, smem, stream);
+  return a.c.dtype == DSPARK_F32 ? launch_ffma_rows<float>(a, sms, stream)
+                                 : launch_ffma_rows<__nv_bfloat16>(a, sms, stream);
 }
 
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream) {
   if (a.blocks < 2) return cudaSuccess;
-  const dim3 grid(a.blocks - 1, (a.slot_rows + kMergeWarps - 1) / kMergeWarps);
-  return launch_behind(a.c.dtype == DSPARK_F32 ? tree_merge_kernel<float>
-                                               : tree_merge_kernel<__nv_bfloat16>,
-                       grid, 32 * kMergeWarps, 0, stream, a);
+  const bool wide = a.c.head_dim > 128, many = a.slot_rows > 64;
+  const int rows = kMergeWarps * (many ? 4 : 1);
+  const dim3 grid(a.blocks - 1, (a.slot_rows + rows - 1) / rows);
+  const auto pick = [&](auto zero) {
+    using T = decltype(zero);
+    return many ? (wide ? tree_merge_kernel<T, 2, 4> : tree_merge_kernel<T, 1, 4>)
+                : (wide ? tree_merge_kernel<T, 2, 1> : tree_merge_kernel<T, 1, 1>);
+  };
+  return launch_behind(a.c.dtype == DSPARK_F32 ? pick(0.0f) : pick(__nv_bfloat16()), grid,
+                       32 * kMergeWarps, 0, stream, a);
 }
 
 }  // namespace dspark
