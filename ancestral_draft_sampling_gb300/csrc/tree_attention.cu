@@ -9,7 +9,7 @@
 // Scores are in units of log2, so that a weight is one ex2.
 //
 // Sixteen warps share a tile of 64 keys (32 where head_dim is above 128) in
-// shared memory.  A warp holds four or eight rows, and two to sixteen groups
+// shared memory.  A warp holds four rows, and two to sixteen groups
 // of warps take the same rows and part of the keys each, with statistics of
 // their own (a row's maximum is the warp's; its sum stays spread over the
 // lanes); the groups are joined at the unit's end.  The next tile, of whatever
@@ -26,6 +26,7 @@ namespace dspark {
 namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kRowGroups = 8;
+constexpr int RW = 4;  // rows of a warp
 
 __device__ __forceinline__ float4 load4(const float* p) {
   return *reinterpret_cast<const float4*>(p);
@@ -58,7 +59,7 @@ __device__ __forceinline__ void copy16(void* to, const void* from, bool there) {
 }
 
 // Shared memory of a block, in bytes.
-template <typename T, int ND, int RW>
+template <typename T, int ND>
 struct Tiles {
   static constexpr int kTile = ND == 1 ? 64 : 32;  // keys
   static constexpr int kRows = kRowGroups * RW;    // rows of a unit
@@ -86,12 +87,11 @@ struct NextTile {
   }
 };
 
-// ND: chunks of 128 dims that a lane's four cover (1: D <= 128, 2: D <= 256);
-// RW: rows of a warp.
-template <typename T, int ND, int RW>
+// ND: chunks of 128 dims that a lane's four cover (1: D <= 128, 2: D <= 256).
+template <typename T, int ND>
 __global__ void __launch_bounds__(kThreads)
     tree_ffma_kernel(const __grid_constant__ TreeArgs a, int row_groups) {
-  using L = Tiles<T, ND, RW>;
+  using L = Tiles<T, ND>;
   constexpr int kTile = L::kTile;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ TreeShare share;
@@ -107,6 +107,16 @@ __global__ void __launch_bounds__(kThreads)
   // the warp's rows and keys
   const int key_groups = kWarps / row_groups, rg = warp & (row_groups - 1), kg = warp / row_groups;
   const int keys = kTile / key_groups, key0 = kg * keys;
+  // of a warp's keys, four to a lane while scores are made, one after that
+  const int key_lanes = keys / 4, key_lane = lane & (key_lanes - 1);
+  const int key_shift = 31 - __clz(key_lanes), segment = lane >> key_shift;
+  const int share_of = 4 * ((D / 4 * key_lanes + 31) / 32);
+  const int dim0 = segment * share_of, dim1 = dim0 + share_of < D ? dim0 + share_of : D;
+  const int lane_key = key_lane + key_lanes * (2 * (segment & 1) + ((segment >> 1) & 1));
+  auto holder = [&](int j) {  // the lane of key j
+    const int x = j >> key_shift;
+    return ((x >> 1) + 2 * (x & 1)) * key_lanes + (j & (key_lanes - 1));
+  };
   const T* q = static_cast<const T*>(a.q);
   const char* pool = static_cast<const char*>(a.c.pool);
   if (threadIdx.x < L::kRows) {
@@ -233,27 +243,59 @@ __global__ void __launch_bounds__(kThreads)
       }
       const T* ks = reinterpret_cast<const T*>(smem + (n & 1) * layout.stage());
       const T* vs = reinterpret_cast<const T*>(smem + (n & 1) * layout.stage() + layout.key_bytes());
-      // the score of a key a lane
-      const int k0 = key0 + (lane < keys ? lane : 0);
-      uint64_t s2[RW];
+      // Scores: a lane has four keys and a stretch of the dims, 8 loads from
+      // shared memory for 16 products of four (a key a lane over all dims takes
+      // 5 for 4, and single tokens over 4000 keys take 119 us instead of 80).
+      // The lanes of the same keys then add up and keep a key each.
+      uint64_t s2[RW][4];
 #pragma unroll
-      for (int i = 0; i < RW; ++i) s2[i] = 0;
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s2[i][x] = 0;
       const float* qr = qs + rg * RW * DP;
-#pragma unroll 2
-      for (int d = 0; d < D; d += 4) {
-        const float4 x0 = load4(ks + k0 * pad + d);
+      const T* kr = ks + (key0 + key_lane) * pad;
+#pragma unroll 1
+      for (int d = dim0; d < dim1; d += 4) {
+        float4 x[4];
 #pragma unroll
-        for (int i = 0; i < RW; ++i) s2[i] = dot4(load4(qr + i * DP + d), x0, s2[i]);
+        for (int y = 0; y < 4; ++y) x[y] = load4(kr + y * key_lanes * pad + d);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const float4 y = load4(qr + i * DP + d);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) s2[i][z] = dot4(y, x[z], s2[i][z]);
+        }
       }
-      const int j = j0 + key0 + lane;
+      __syncwarp();
+      float s[RW];
+      {
+        const bool odd = segment & 1, odd2 = segment & 2;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          float v[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 y = unpair(s2[i][x]);
+            v[x] = y.x + y.y;
+          }
+          const float a0 = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[2], key_lanes);
+          const float a1 = __shfl_xor_sync(0xffffffffu, odd ? v[1] : v[3], key_lanes);
+          const float b0 = (odd ? v[2] : v[0]) + a0, b1 = (odd ? v[3] : v[1]) + a1;
+          const float c0 = __shfl_xor_sync(0xffffffffu, odd2 ? b0 : b1, 2 * key_lanes);
+          s[i] = (odd2 ? b1 : b0) + c0;
+        }
+#pragma unroll 1
+        for (int x = 4 * key_lanes; x < 32; x *= 2)
+#pragma unroll
+          for (int i = 0; i < RW; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
+      }
+      const int j = j0 + key0 + lane_key;
       const uint32_t full = keys >= 32 ? ~0u : (1u << keys) - 1;
-      uint32_t seen[RW];  // the warp's keys that the row sees
+      uint32_t seen[RW];  // the warp's keys that the row sees (bit l: lane l's)
       bool all = true;
-      float s[RW], now[RW];
+      float now[RW];
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
-        const float2 x = unpair(s2[i]);
-        s[i] = x.x + x.y;
         const bool see = lane < keys && (j < w.q.len ? j >= lo[i]
                                                      : j < total && ((bits[i] >> (j - w.q.len)) & 1));
         seen[i] = __ballot_sync(0xffffffffu, see);
@@ -275,7 +317,7 @@ __global__ void __launch_bounds__(kThreads)
           o[i][x][0] = mul2(o[i][x][0], pair(keep, keep));
           o[i][x][1] = mul2(o[i][x][1], pair(keep, keep));
         }
-        if (lane < keys) pw[lane * RW + i] = pair(p, p);
+        if (lane < keys) pw[lane_key * RW + i] = pair(p, p);
       }
       __syncwarp();
       auto add = [&](int j, bool every) {
@@ -291,7 +333,7 @@ __global__ void __launch_bounds__(kThreads)
             const uint64_t v0 = pair(v.x, v.y), v1 = pair(v.z, v.w);
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
-              if (!every && !((seen[i] >> j) & 1)) continue;
+              if (!every && !((seen[i] >> holder(j)) & 1)) continue;
               const uint64_t pi = i & 1 ? p[i / 2].y : p[i / 2].x;
               o[i][x][0] = fma2(pi, v0, o[i][x][0]);
               o[i][x][1] = fma2(pi, v1, o[i][x][1]);
@@ -501,16 +543,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
-template <typename T, int ND, int RW>
+template <typename T, int ND>
 cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
-  using L = Tiles<T, ND, RW>;
+  using L = Tiles<T, ND>;
   static std::once_flag once[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::call_once(once[dev], [] {
-    cudaFuncSetAttribute(tree_ffma_kernel<T, ND, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(tree_ffma_kernel<T, ND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          L{ND * 128}.total());
   });
   a.tile_shift = L::kTile == 64 ? 6 : 5;
@@ -521,26 +563,20 @@ cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
   a.stat_log2 = 1.0f;
   a.stat_ln = 0.6931471805599453f;
   // warps side by side over the rows that a unit has; the rest share the keys
-  int groups = 1;
+  int groups = ND;  // at least four keys a warp
   while (groups < kRowGroups && groups * RW < a.slot_rows) groups *= 2;
-  return launch_behind(tree_ffma_kernel<T, ND, RW>, a.blocks, kThreads, L{a.c.head_dim}.total(),
+  return launch_behind(tree_ffma_kernel<T, ND>, a.blocks, kThreads, L{a.c.head_dim}.total(),
                        stream, a, groups);
-}
-
-template <typename T>
-cudaError_t launch_ffma_rows(TreeArgs& a, int sms, cudaStream_t stream) {
-  if (a.c.head_dim > 128) return launch_ffma<T, 2, 4>(a, sms, stream);
-  // eight rows a warp halve the shared memory reads of a product, where there
-  // are the rows
-  return a.T * a.group > 32 ? launch_ffma<T, 1, 8>(a, sms, stream)
-                            : launch_ffma<T, 1, 4>(a, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
-  return a.c.dtype == DSPARK_F32 ? launch_ffma_rows<float>(a, sms, stream)
-                                 : launch_ffma_rows<__nv_bfloat16>(a, sms, stream);
+  const bool wide = a.c.head_dim > 128;
+  if (a.c.dtype == DSPARK_F32)
+    return wide ? launch_ffma<float, 2>(a, sms, stream) : launch_ffma<float, 1>(a, sms, stream);
+  return wide ? launch_ffma<__nv_bfloat16, 2>(a, sms, stream)
+              : launch_ffma<__nv_bfloat16, 1>(a, sms, stream);
 }
 
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream) {
