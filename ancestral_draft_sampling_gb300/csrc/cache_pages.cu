@@ -55,14 +55,9 @@ __device__ __forceinline__ void row_offsets(int* offset, const int* counts,
   __syncthreads();
 }
 
-// Takes one hold off each listed page; the pages that nobody holds any more
-// go on the free stack, the last listed first.  A page that is listed several
-// times goes there once, for its first entry: after the holds are taken off,
-// the entries of a page without holds compete with an atomic minimum over
-// their numbers, in the page's own count (the order does not matter to a
-// minimum, so the stack is the same on every run).
-__device__ void give_pages(const dspark_cache& c, const GiveList& g, int B,
-                           int* warps) {
+// The same for a list of any length: the entries are walked anew in each step.
+__device__ __noinline__ int give_many(const dspark_cache& c, const GiveList& g, int B, int top,
+                                      int* warps) {
   const int n = g.offset[B];
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
     const int b = row_of(g.offset, B, e);
@@ -79,15 +74,12 @@ __device__ void give_pages(const dspark_cache& c, const GiveList& g, int B,
       atomicMin(&c.ref_count[p], INT_MIN + e);
   }
   __syncthreads();
-  int top = c.control[kCtlFree];
   for (int e0 = 0; e0 < n; e0 += blockDim.x) {
     const int e = n - 1 - e0 - (int)threadIdx.x;  // from the last entry on
     int p = -1;
     if (e >= 0) {
       const int b = row_of(g.offset, B, e);
-      const size_t at = (size_t)g.seq[b] * c.max_pages + g.from[b] + e - g.offset[b];
-      p = c.block_table[at];
-      c.block_table[at] = -1;
+      p = c.block_table[(size_t)g.seq[b] * c.max_pages + g.from[b] + e - g.offset[b]];
       if (p < 0 || p >= c.num_pages || __ldcg(&c.ref_count[p]) != INT_MIN + e) p = -1;
     }
     int total;
@@ -97,6 +89,99 @@ __device__ void give_pages(const dspark_cache& c, const GiveList& g, int B,
       if (top + x >= 0 && top + x < c.num_pages) c.free_list[top + x] = p;
     }
     top += total;
+  }
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {  // a row may be listed twice
+    const int b = row_of(g.offset, B, e);
+    c.block_table[(size_t)g.seq[b] * c.max_pages + g.from[b] + e - g.offset[b]] = -1;
+  }
+  return top;
+}
+
+// Takes one hold off each listed page; the pages that nobody holds any more
+// go on the free stack, the last listed first.  A page that is listed several
+// times goes there once, for its first entry: after the holds are taken off,
+// the entries of a page without holds compete with an atomic minimum over
+// their numbers, in the page's own count (the order does not matter to a
+// minimum, so the stack is the same on every run).  There is nothing to
+// compete for where each page either had one hold or still has some, and no
+// places to count where all go on the stack.
+constexpr int kPer = 4;  // entries of a thread, their loads in flight together
+
+__device__ void give_pages(const dspark_cache& c, const GiveList& g, int B,
+                           int* warps) {
+  const int n = g.offset[B], before = c.control[kCtlFree];
+  int top = before;
+  if (n > kPer * (int)blockDim.x) {
+    top = give_many(c, g, B, before, warps);
+  } else {
+    int page[kPer], held[kPer];
+    size_t at[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int e = threadIdx.x + k * blockDim.x;
+      page[k] = -1;
+      held[k] = 1;
+      if (e >= n) continue;
+      const int b = row_of(g.offset, B, e);
+      at[k] = (size_t)g.seq[b] * c.max_pages + g.from[b] + e - g.offset[b];
+      page[k] = c.block_table[at[k]];
+    }
+    __syncthreads();  // a row may be listed twice
+    bool plain = true;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (threadIdx.x + k * blockDim.x >= n) continue;
+      if (page[k] >= 0 && page[k] < c.num_pages) {
+        held[k] = atomicSub(&c.ref_count[page[k]], 1);
+      } else {
+        page[k] = -1;
+        cache_error(c, kCacheErrPage);
+      }
+      c.block_table[at[k]] = -1;
+      plain &= page[k] >= 0 && held[k] == 1;
+    }
+    if (__syncthreads_and(plain)) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int to = top + n - 1 - (int)(threadIdx.x + k * blockDim.x);
+        if (page[k] >= 0 && to >= 0 && to < c.num_pages) c.free_list[to] = page[k];
+      }
+      top += n;
+    } else {
+      bool compete = false;
+      int left[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        left[k] = page[k] >= 0 ? __ldcg(&c.ref_count[page[k]]) : 1;
+        compete |= page[k] >= 0 && held[k] != 1 && left[k] <= 0;
+      }
+      compete = __syncthreads_or(compete);
+      if (compete) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (left[k] <= 0)
+            atomicMin(&c.ref_count[page[k]], INT_MIN + (int)(threadIdx.x + k * blockDim.x));
+        __syncthreads();
+      }
+      int place[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int e = threadIdx.x + k * blockDim.x;
+        const bool goes = left[k] <= 0 &&
+                          (!compete || __ldcg(&c.ref_count[page[k]]) == INT_MIN + e);
+        int total;
+        place[k] = top + block_exclusive(goes, warps, total);
+        if (!goes) page[k] = -1;
+        top += total;
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int to = before + top - 1 - place[k];
+        if (page[k] < 0) continue;
+        __stcg(&c.ref_count[page[k]], 0);
+        if (to >= 0 && to < c.num_pages) c.free_list[to] = page[k];
+      }
+    }
   }
   __syncthreads();
   if (threadIdx.x == 0) c.control[kCtlFree] = top < c.num_pages ? top : c.num_pages;
@@ -184,7 +269,7 @@ __global__ void __launch_bounds__(kBlock, 1)
 }
 
 __global__ void __launch_bounds__(kBlock, 1)
-    release_kernel(dspark_cache c, const int32_t* seq, int B) {
+    release_kernel(const __grid_constant__ dspark_cache c, const int32_t* seq, int B) {
   __shared__ GiveList g;
   __shared__ int counts[kMaxB], warps[33];
   const int b = threadIdx.x;
@@ -206,7 +291,7 @@ __global__ void __launch_bounds__(kBlock, 1)
 // and 2 b + 1 tell the copy what to do: the page to copy from and the page to
 // copy to, or -1.
 __global__ void __launch_bounds__(kBlock, 1)
-    fork_kernel(dspark_cache c, const int32_t* parent, const int32_t* child,
+    fork_kernel(const __grid_constant__ dspark_cache c, const int32_t* parent, const int32_t* child,
                 const int32_t* length, int B) {
   __shared__ GiveList g;
   __shared__ int par[kMaxB], full[kMaxB], need[kMaxB], warps[33];
@@ -280,13 +365,25 @@ __global__ void __launch_bounds__(kBlock, 1)
   __syncthreads();
   if (threadIdx.x == 0 && taken > 0) c.control[kCtlFree] = free - taken;
   row_offsets(offset, full, B, warps);
-  for (int e = threadIdx.x; e < offset[B]; e += blockDim.x) {
-    const int r = row_of(offset, B, e);
-    const int i = e - offset[r];
-    const int id = cache_page(c, par[r], i, c.max_pages);
-    c.block_table[(size_t)g.seq[r] * c.max_pages + i] = id;
-    if (id >= 0) atomicAdd(&c.ref_count[id], 1);
-    else cache_error(c, kCacheErrPage);
+  for (int e0 = threadIdx.x; e0 < offset[B]; e0 += kPer * blockDim.x) {
+    int id[kPer];
+    size_t to[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int e = e0 + k * blockDim.x;
+      if (e >= offset[B]) continue;
+      const int r = row_of(offset, B, e);
+      const int i = e - offset[r];
+      id[k] = cache_page(c, par[r], i, c.max_pages);
+      to[k] = (size_t)g.seq[r] * c.max_pages + i;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (e0 + k * blockDim.x >= offset[B]) continue;
+      c.block_table[to[k]] = id[k];
+      if (id[k] >= 0) atomicAdd(&c.ref_count[id[k]], 1);
+      else cache_error(c, kCacheErrPage);
+    }
   }
 }
 
@@ -336,7 +433,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 constexpr int kMoveThreads = 256, kMoveBatch = 8;
 
 __global__ void __launch_bounds__(kMoveThreads)
-    accept_kernel(dspark_cache c, const int32_t* seq, const int32_t* length,
+    accept_kernel(const __grid_constant__ dspark_cache c, const int32_t* seq, const int32_t* length,
                   const int32_t* accepted, const int32_t* path, int path_width,
                   int extra, int tokens, int B, int32_t* new_length) {
   __shared__ GiveList g;
@@ -435,6 +532,13 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 }  // namespace
 
+// Threads for B sequences and the pages that they may hold: a block-wide step
+// of few warps is shorter.
+static int list_threads(const dspark_cache& c, int B) {
+  const long long most = (long long)B * c.max_pages;
+  return B <= 128 && most <= 128 * kPer ? 128 : kBlock;
+}
+
 cudaError_t launch_cache_init(const dspark_cache& c, cudaStream_t stream) {
   const size_t most = (size_t)c.max_seqs * c.max_pages > (size_t)c.num_pages
                           ? (size_t)c.max_seqs * c.max_pages
@@ -453,13 +557,14 @@ cudaError_t launch_cache_reserve(const dspark_cache& c, const int32_t* seq,
 
 cudaError_t launch_cache_release(const dspark_cache& c, const int32_t* seq,
                                  int B, cudaStream_t stream) {
-  return launch_behind(release_kernel, 1, kBlock, 0, stream, c, seq, B);
+  return launch_behind(release_kernel, 1, list_threads(c, B), 0, stream, c, seq, B);
 }
 
 cudaError_t launch_cache_fork(const dspark_cache& c, const int32_t* parent,
                               const int32_t* child, const int32_t* length,
                               int B, cudaStream_t stream) {
-  cudaError_t e = launch_behind(fork_kernel, 1, kBlock, 0, stream, c, parent, child, length, B);
+  cudaError_t e = launch_behind(fork_kernel, 1, list_threads(c, B), 0, stream, c, parent, child,
+                                length, B);
   if (e != cudaSuccess) return e;
   const int items = 2 * c.layers * c.kv_heads;
   const int blocks = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
