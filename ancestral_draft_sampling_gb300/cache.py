@@ -4,6 +4,7 @@ library.  The layouts, limits and device errors are described in
 include/dspark.h."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional
@@ -14,6 +15,15 @@ from . import _lib
 from ._lib import BF16, F32, DsparkError
 
 CONTROL_WORDS = 64 + 2 * 1024  # DSPARK_CACHE_CONTROL_WORDS
+
+
+_here = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Memory that a call makes belongs to the stream that the call runs on:
+    the allocator hands it out again only behind the call's kernels."""
+    return _here if stream is None else torch.cuda.stream(stream)
 
 
 class PagedCache:
@@ -27,11 +37,12 @@ class PagedCache:
                  device=None, stream=None):
         device = device or "cuda"
         i32 = dict(dtype=torch.int32, device=device)
-        self._set(torch.empty(layers, 2, num_pages, kv_heads, page_size, head_dim,
-                              dtype=dtype or torch.bfloat16, device=device),
-                  torch.empty(max_seqs, max_pages, **i32), torch.empty(max_seqs, **i32),
-                  torch.empty(num_pages, **i32), torch.empty(num_pages, **i32),
-                  torch.empty(CONTROL_WORDS, **i32))
+        with _on(stream):
+            self._set(torch.empty(layers, 2, num_pages, kv_heads, page_size, head_dim,
+                                  dtype=dtype or torch.bfloat16, device=device),
+                      torch.empty(max_seqs, max_pages, **i32), torch.empty(max_seqs, **i32),
+                      torch.empty(num_pages, **i32), torch.empty(num_pages, **i32),
+                      torch.empty(CONTROL_WORDS, **i32))
         _call(self, "dspark_cache_init", stream)
 
     @classmethod
@@ -166,7 +177,8 @@ def cache_accept(cache: PagedCache, length, accepted_len, tokens: int, *, path=N
         width = path.shape[1]
     at = _ptr_of(cache, "length", length, i32, shape)
     if new_length is None:
-        new_length = length.new_empty(shape)
+        with _on(stream):
+            new_length = torch.empty(shape, dtype=i32, device=cache.device)
     _call(cache, "dspark_cache_accept", stream, _ptr_of(cache, "seq", seq, i32, shape), at,
           _ptr_of(cache, "accepted_len", accepted_len, i32, shape),
           _ptr_of(cache, "path", path, i32, (shape[0], width)), width, extra, tokens, shape[0],
@@ -209,7 +221,8 @@ def cache_append(cache: PagedCache, layer: int, q, k, v, length, *, position, co
     if cos_sin.dim() != 2:
         raise TypeError("cos_sin must be float32 [max_position, rot_dim]")
     if q_out is None:
-        q_out = torch.empty((B, T, heads, D), dtype=dtype, device=cache.device)
+        with _on(stream):
+            q_out = torch.empty((B, T, heads, D), dtype=dtype, device=cache.device)
     i32, f32, shape = torch.int32, torch.float32, (B,)
     _call(cache, "dspark_cache_append", stream, layer, _ptr_of(cache, "seq", seq, i32, shape),
           _ptr_of(cache, "length", length, i32, shape),
@@ -257,11 +270,14 @@ def tree_attention(cache: PagedCache, layer: int, q, length, *, mask=None, token
     if mask is not None and mask.dim() == 2:
         stride = T
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     if lse is None and with_lse:
-        lse = torch.empty((B, T, heads), dtype=torch.float32, device=cache.device)
+        with _on(stream):
+            lse = torch.empty((B, T, heads), dtype=torch.float32, device=cache.device)
     if workspace is None:
-        workspace = TreeWorkspace(B, T, heads, cache.kv_heads, D, device=cache.device)
+        with _on(stream):
+            workspace = TreeWorkspace(B, T, heads, cache.kv_heads, D, device=cache.device)
     elif workspace.buffer.get_device() != cache.index:
         raise ValueError("workspace must be on the cache's device")
     if scale is None:

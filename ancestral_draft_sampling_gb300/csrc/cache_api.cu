@@ -203,6 +203,10 @@ dspark_status dspark_tree_attention(
   const TreeLayout L = tree_layout(T, group, cache->head_dim);
   if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
     return DSPARK_ERR_WORKSPACE;
+  // blocks read queries while others write results
+  const uintptr_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(out);
+  const size_t bytes = (size_t)B * T * heads * cache->head_dim * dtype_bytes(cache->dtype);
+  if (from < to + bytes && to < from + bytes) return DSPARK_ERR_INVALID_ARG;
   TreeArgs a{};
   a.c = *cache;
   a.layer = layer;

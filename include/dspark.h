@@ -428,7 +428,8 @@ DSPARK_API dspark_status dspark_sample_temperature(
  *
  * Sequences, pages, positions and paths that are out of range are seen on
  * the device: the entry is skipped as its call says and the error word is
- * set (6: a seq outside [0, max_seqs); 7: a length or page outside what the
+ * set (2: a bounded wait inside the attention ran out, its result is not to
+ * be used; 6: a seq outside [0, max_seqs); 7: a length or page outside what the
  * sequence holds; 8: no free page left, or more pages than a table row has;
  * 9: an accepted path or length that is not one; 10: a position outside the
  * rotation table; 11: a fork whose child is a parent, or twice a child).
@@ -491,7 +492,10 @@ DSPARK_API dspark_status dspark_cache_release(const dspark_cache* cache,
  * Several children may have the same parent; a child that is also a parent
  * of the call, or is named twice, makes the whole call do nothing (error 11).
  * A child whose parent holds fewer than length[b] tokens (error 7), or for
- * which no page is free (error 8), ends up empty.  Two launches.
+ * which no page is free (error 8), ends up empty.  Shared pages are full, so
+ * nothing writes to them as long as a sequence's length does not shrink; one
+ * that is to be cut back is forked at the shorter length instead.  Two
+ * launches.
  */
 DSPARK_API dspark_status dspark_cache_fork(const dspark_cache* cache,
                                            const int32_t* parent,
@@ -583,17 +587,20 @@ DSPARK_API size_t dspark_tree_workspace_bytes(int B, int T, int heads,
  *   scale        of the scores q.k, finite.
  *   out          [B,T,heads,D] dense: sum_j p_j v_j, p = softmax(scale q.k)
  *                over the visible tokens; zeros for a token that sees none.
+ *                Must not overlap q.
  *   lse          [B,T,heads] float32 or NULL: log(sum_j exp(scale q.k_j)),
  *                -inf for a token that sees none.
  *   workspace    dspark_tree_workspace_bytes(...) bytes, 256-byte aligned; its
  *                contents need not be initialised.  Two calls in flight at
  *                the same time must not share it.
  * Scores, softmax statistics and sums are float32; bfloat16 inputs multiply
- * weights rounded to bfloat16 (relative error 2^-9 each).  Keys and values of
+ * weights rounded to bfloat16 (relative error 2^-8 each).  Keys and values of
  * places that a token does not see never reach its result, whatever they
  * hold.  A sequence whose length or pages are out of range is not computed
  * (error 6 or 7; its rows are left as they are); a table entry that names no
- * page reads as zeros (error 7).
+ * page reads as zeros (error 7).  A call with 2^31 tiles of keys or more (128
+ * keys a tile on the tensor cores, 64 or 32 on the FFMA kernel), over all
+ * sequences, key heads and groups of query rows, is not computed (error 7).
  * 1 <= T <= 64, group <= 32.  bfloat16 with head_dim 64 or 128 and a page size
  * that is a power of two from 8 on runs on the tensor cores, everything else
  * on the FFMA kernel.  Two launches, graph capturable, no synchronisation.
@@ -637,7 +644,9 @@ DSPARK_API dspark_status dspark_noise_words_folded(uint64_t seed, uint64_t offse
  * no kernel of the last call on this workspace recorded an error,
  * DSPARK_ERR_DEVICE (and *code != 0) if one did.  Every draft-block and
  * sampler call clears the word when it starts, so the code describes the
- * last call only.  Codes: 1 a d0 outside [0, V) (token 0 used), 2 a bounded
+ * last call only; the calls on a cache never clear its word (control), which
+ * this call reads likewise: their codes 2 and 6 to 11 are described there.
+ * Codes: 1 a d0 outside [0, V) (token 0 used), 2 a bounded
  * wait inside a kernel ran out, 3 a per-request temperature that is not
  * finite and positive (1 used), 4 a proposal slot outside [0, num_slots),
  * 5 a sampler position outside [0, 65535] (0 used).  Synchronises
