@@ -126,6 +126,19 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
+// Whether it is over, for a whole warp alike.
+__device__ __forceinline__ bool over_warp(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0);
+}
+
 __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                        int x, int y, int z, int w) {
   asm volatile(
@@ -601,15 +614,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a stream's next scores go before its sums where the weights lie
         // apart, else behind them
         const bool more = i + (both ? 1 : 2) < w.n, last = i + (both ? 2 : 3) == w.n;
+        bool there = false;  // the next keys
         for (int h = 0; h < (both ? 2 : 1) && ok; ++h) {
           const int st = both ? h : i & 1;
           auto next_scores = [&]() {
-            if (h == 0) keys();  // both streams use the same ones
+            if (h == 0 && !there) keys();  // both streams use the same ones
             if (ok) scores(st, both ? h : 0, !both || h == 1, last && (!both || h == 1));
           };
+          if (h == 0) {  // behind the weights nothing should be waited for
+            ok = wait_warp(&sh.v_full[v.slot], v.parity);
+            there = more && over_warp(&sh.k_full[k.slot], k.parity);
+          }
           weighed(st);
           if (S::apart && more && ok) next_scores();
-          if (h == 0) ok = ok && wait_warp(&sh.v_full[v.slot], v.parity);
           if (!ok) break;
           sums(st, i < (both ? 1 : 2), !both || h == 1);
           if (!S::apart && more) next_scores();
