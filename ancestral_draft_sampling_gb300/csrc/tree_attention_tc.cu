@@ -610,6 +610,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
       if (freed < halved) ok = ok && wait_warp(&sh.o_free[1], freed++ & 1);
       halved += both;
+      if (both && !S::apart) {  // bound by the products: as little as can be between them
+#pragma unroll 1
+        for (int i = 0; i < w.n && ok; ++i) {
+          const bool more = i + 1 < w.n, last = i + 2 == w.n;
+          ok = wait_warp(&sh.v_full[v.slot], v.parity);
+          if (more) ok = ok && wait_warp(&sh.k_full[k.slot], k.parity);
+          const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
+          const uint64_t kd = k_desc + k.slot * (S::tile_bytes >> 4);
+          uint64_t* const v_empty = &sh.v_empty[v.slot];
+          uint64_t* const k_empty = &sh.k_empty[k.slot];
+          v.step(P.v_slots);
+          if (more) k.step(P.k_slots);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait_warp(&sh.p_ready[h], used[h]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t add = i > 0 || *(volatile uint32_t*)&sh.add_first[h];
+            if (elect_one()) {
+#pragma unroll
+              for (int x = 0; x < kTile / 16; ++x)
+                mma_bf16_ta(tmem + S::o_col(h), tmem + S::p_col(h) + 8 * x, vd + x * (2048 >> 4),
+                            idesc_o, x != 0 ? 1u : add);
+              mma_commit(&sh.pv_done[h]);
+              if (more) {
+                const uint64_t qd = q_desc + h * (S::tile_bytes >> 4);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                  const uint32_t off = ((x >> 2) * kHalfBytes + (x & 3) * 32) >> 4;
+                  mma_bf16(tmem + S::s_col(h), qd + off, kd + off, idesc_s, x != 0);
+                }
+                mma_commit(&sh.s_full[h]);
+                if (h == 1) mma_commit(k_empty);
+                if (h == 1 && last) mma_commit(&sh.q_empty);
+              }
+              if (h == 1) mma_commit(v_empty);
+            }
+          }
+        }
+        continue;
+      }
       for (int i = 0; i < w.n && ok; ++i) {
         // a stream's next scores go before its sums where the weights lie
         // apart, else behind them
