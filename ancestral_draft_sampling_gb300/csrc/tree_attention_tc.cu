@@ -57,6 +57,7 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kTile = 128;             // keys of a tile
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 bfloat16
+constexpr int kNarrowRows = 32;        // rows that each warp of a stream has
 constexpr uint32_t kSpin = 1u << 22;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;         // log2 units that a weight may exceed 1
@@ -112,6 +113,18 @@ constexpr size_t smem_bytes() {
   return 1024 + (size_t)Shape<D>::tiles * Shape<D>::tile_bytes + sizeof(Control);
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a block");
+
+// Narrow units: the weights of both streams, and what a stream's warps tell
+// each other about each row.  Behind them there is always more shared memory
+// that a product may read: it takes 128 rows of weights, of which 32 count.
+struct Narrow {
+  uint8_t weights[2][2][kNarrowRows * 128];  // [stream][64 keys]
+  float top[2][4][kNarrowRows];              // of each warp: a maximum that raises m,
+  float sum[2][4][kNarrowRows];              // and at the end its part of l
+  uint32_t raise[2][4];                      // the warp has such maxima
+  uint8_t rest[32768 - 16384 - 2048 - 32];
+};
+static_assert(sizeof(Narrow) == 32768, "a multiple of every tile");
 
 // The polls of a wait that is not over at once: out of line, there are many.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
@@ -246,6 +259,7 @@ struct TcArgs {
   int k_slots, v_slots;  // tiles of the rings
   int page_shift;        // log2 of the page size
   int out32;             // out is aligned to 32 bytes
+  int narrow;            // at most 32 rows a unit: the kernel's other form
 };
 
 // A role's place in a ring: the slot, and the parity of its phase.
@@ -359,6 +373,45 @@ __device__ __forceinline__ float weigh_seen(uint32_t at, uint32_t to, float c, f
   return t.x + t.y;
 }
 
+// Narrow units: the two steps over the 32 scores that a warp has of its rows;
+// the weights go to shared memory, half a row (64 keys) of 128 bytes whose
+// 16-byte words are swizzled by the row.
+__device__ __forceinline__ float extreme32(uint32_t (&x)[32], bool least, uint32_t see) {
+  float top[2] = {-INFINITY, -INFINITY};
+  const uint32_t flip = least ? 0x80000000u : 0u;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float v = __uint_as_float(x[i] ^ flip);
+    top[i & 1] = fmaxf(top[i & 1], (see >> i) & 1 ? v : -INFINITY);
+  }
+  const float best = fmaxf(top[0], top[1]);
+  return least ? -best : best;
+}
+__device__ __forceinline__ float weigh_narrow(uint8_t* to, int words, int swizzle,
+                                              const uint32_t (&x)[32], uint32_t see, float c,
+                                              float base) {
+  const uint64_t cc = pair(c, c), bb = pair(-base, -base);
+  uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 8 * k + 2 * i;
+      const float2 y = unpair(fma2(pair(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), cc, bb));
+      float p0 = ex2(y.x), p1 = ex2(y.y);
+      p0 = (see >> j) & 1 ? p0 : 0.0f;
+      p1 = (see >> j) & 2 ? p1 : 0.0f;
+      sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+      p[i] = pack_bf16(p0, p1);
+    }
+    *reinterpret_cast<uint4*>(to + (((4 * words + k) ^ swizzle) << 4)) =
+        make_uint4(p[0], p[1], p[2], p[3]);
+  }
+  const float2 t = unpair(add2(sum[0], sum[1]));
+  return t.x + t.y;
+}
+
 // Rows that see the whole tile: the same two steps, 64 scores at a time.
 __device__ __forceinline__ float extreme_all(uint32_t at, bool least) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -417,16 +470,19 @@ struct Pages {
   }
 };
 
-// The queries of a unit: one copy for each 128 rows and half of the head.
+// The queries of a unit: one copy for each 128 rows and half of the head, or
+// four of the same rows, one below the other, where units are narrow.
 template <int D>
 __device__ __forceinline__ void load_queries(const TcArgs& P, const Unit& u, const CUtensorMap* map,
                                              uint8_t* q_tile, uint64_t* full) {
-  const int copies = (1 + u.both) * Shape<D>::halves;
+  const int tiles = P.narrow ? 4 : 1 + u.both, copies = tiles * Shape<D>::halves;
+  const int step = P.narrow ? kNarrowRows * 128 : Shape<D>::tile_bytes;
   mbar_arrive_expect_tx(full, copies * P.q_tokens * P.a.group * 128);
 #pragma unroll 1
   for (int i = 0; i < copies; ++i) {
     const int tile = i / Shape<D>::halves, half = i - tile * Shape<D>::halves;
-    tma_5d(q_tile + i * kHalfBytes, map, full, half * 64, 0, u.h, u.t0 + tile * P.fit, u.b);
+    tma_5d(q_tile + tile * step + half * kHalfBytes, map, full, half * 64, 0, u.h,
+           P.narrow ? u.t0 : u.t0 + tile * P.fit, u.b);
   }
 }
 
@@ -497,7 +553,7 @@ __device__ __noinline__ bool fill_ring(const TcArgs& P, Control& sh, bool values
   return ok;
 }
 
-template <int D>
+template <int D, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,
@@ -505,12 +561,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   extern __shared__ uint8_t raw[];
   uint8_t* q_tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint8_t* k_ring = q_tile + P.q_tiles * S::tile_bytes;
+  Narrow& nar = *reinterpret_cast<Narrow*>(q_tile + P.q_tiles * S::tile_bytes);
+  uint8_t* k_ring = q_tile + P.q_tiles * S::tile_bytes + (kNarrow ? sizeof(Narrow) : 0);
   uint8_t* v_ring = k_ring + P.k_slots * S::tile_bytes;
   Control& sh = *reinterpret_cast<Control*>(q_tile + S::tiles * S::tile_bytes);
   const TreeArgs& a = P.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
+  // the next scores need not wait for the product of the weights
+  constexpr bool apart = S::apart || kNarrow;
   static_assert(offsetof(Control, v_all) == 31 * 8 && offsetof(Control, o_free) == 37 * 8, "barriers");
   if (warp == 0) {
     uint64_t* bar = sh.k_full;
@@ -552,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile), 16, 1024);
     const uint64_t k_desc = smem_desc_sw128(smem_u32(k_ring), 16, 1024);
     const uint64_t v_desc = smem_desc_sw128(smem_u32(v_ring), kHalfBytes, 1024);
+    const uint64_t p_desc = smem_desc_sw128(smem_u32(nar.weights), 16, 1024);
     uint32_t halved = 0, freed = 0;  // units that gave each stream half the rows
     uint32_t used[2] = {0, 0};       // tiles that a stream has weighed
     Place k{0, 0}, v{0, 0};
@@ -583,10 +643,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t add = !first || *(volatile uint32_t*)&sh.add_first[st];
       const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
       if (elect_one()) {
+        if (kNarrow) {
+          const uint64_t pd = p_desc + st * (sizeof(nar.weights[0]) >> 4);
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          mma_bf16_ta(tmem + S::o_col(st), tmem + S::p_col(st) + 8 * i, vd + i * (2048 >> 4),
-                      idesc_o, i != 0 ? 1u : add);
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_bf16(tmem + S::o_col(st), pd + (((i >> 2) * kNarrowRows * 128 + (i & 3) * 32) >> 4),
+                     vd + i * (2048 >> 4), idesc_o, i != 0 ? 1u : add);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_bf16_ta(tmem + S::o_col(st), tmem + S::p_col(st) + 8 * i, vd + i * (2048 >> 4),
+                        idesc_o, i != 0 ? 1u : add);
+        }
         mma_commit(&sh.pv_done[st]);
         if (free_values) mma_commit(&sh.v_empty[v.slot]);
       }
@@ -596,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int unit = 0; ok && units.next(sh, w, ok, lane); ++unit) {
       ok = wait_warp(&sh.q_full, unit & 1);
-      const bool both = w.both;
+      const bool both = !kNarrow && w.both;
       if (ok) keys();
       if (!ok) break;
       scores(0, 0, !both, w.n == 1 && !both);
@@ -610,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
       if (freed < halved) ok = ok && wait_warp(&sh.o_free[1], freed++ & 1);
       halved += both;
-      if (both && !S::apart) {  // bound by the products: as little as can be between them
+      if (both && !apart) {  // bound by the products: as little as can be between them
 #pragma unroll 1
         for (int i = 0; i < w.n && ok; ++i) {
           const bool more = i + 1 < w.n, last = i + 2 == w.n;
@@ -667,10 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             there = more && over_warp(&sh.k_full[k.slot], k.parity);
           }
           weighed(st);
-          if (S::apart && more && ok) next_scores();
+          if (apart && more && ok) next_scores();
           if (!ok) break;
           sums(st, i < (both ? 1 : 2), !both || h == 1);
-          if (!S::apart && more) next_scores();
+          if (!apart && more) next_scores();
         }
         v.step(P.v_slots);
       }
@@ -721,18 +789,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t used = 0, syncs = 0, alls = 0, joins = 0;  // phases of the barriers
     bool is_first = true;            // the block's first unit
     // the row's token and head within a query tile
-    const int r_token = (int)((uint32_t)r / (uint32_t)a.group), r_head = r - r_token * a.group;
+    const int row = kNarrow ? lane : r;
+    const int r_token = (int)((uint32_t)row / (uint32_t)a.group), r_head = row - r_token * a.group;
     UnitReader units;
     Unit w;
 #pragma unroll 1
     for (; ok && units.next(sh, w, ok, lane); g += w.n) {
       const int left = w.cnt - w.t0;
-      const bool both = w.both;                   // half the rows each
+      const bool both = !kNarrow && w.both;       // half the rows each
       const int t0 = w.t0 + (both && st ? P.fit : 0);
       const int more = w.cnt - t0, tokens = more < P.fit ? more : P.fit;
       const int rows = tokens * a.group;
       const int t = t0 + r_token;
-      const bool valid = r < rows, any = quarter * 32 < rows;
+      // narrow: all warps weigh, the first one has the sums
+      const bool valid = row < rows, any = kNarrow || quarter * 32 < rows;
+      const bool sums = kNarrow ? quarter == 0 : any;
       const uint64_t bits = valid ? tree_mask(a, w.b, t, w.cnt) : 0;
       const int len = w.len;
       const Sight sight{valid ? tree_window_lo(a, w.b, t, len) : 0, len, bits};
@@ -762,19 +833,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (any) {
-          float best = masked ? extreme_seen(s_at, c < 0.0f, j0, sight)
-                              : extreme_all(s_at, c < 0.0f);
+          uint32_t x[32], see = ~0u;  // narrow: 32 scores of the row
+          float best;
+          if (kNarrow) {
+            tmem_ld32(s_at + 32 * quarter, x);
+            if (masked) see = seen32(j0 + 32 * quarter, sight.lo, sight.len, sight.bits);
+            tmem_ld_wait();
+            best = extreme32(x, c < 0.0f, see);
+          } else {
+            best = masked ? extreme_seen(s_at, c < 0.0f, j0, sight) : extreme_all(s_at, c < 0.0f);
+          }
           best *= c;
-          if (S::apart && used > 0 && real) {  // the last product has read its weights
+          if (apart && used > 0 && real) {  // the last product has read its weights
             ok = wait_warp(&sh.pv_done[st], (used - 1) & 1);
             if (!ok) break;
             tc_fence_after();
           }
           const bool raise = valid && best > m + kRaise;  // m = -inf: any maximum
-          if (__any_sync(0xffffffffu, raise)) {
-            const float now = raise ? best : m;
-            const float f = raise ? ex2(m - now) : 1.0f;
-            if (tile > first) {  // the last product into O has ended
+          uint32_t raised = __any_sync(0xffffffffu, raise);
+          float now = raise ? best : m;
+          if (kNarrow) {  // the warps agree
+            if (raised) nar.top[st][quarter][lane] = now;
+            if (lane == 0) nar.raise[st][quarter] = raised;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.v_sync[st]);
+            ok = wait_warp(&sh.v_sync[st], syncs++ & 1);
+            if (!ok) break;
+            raised = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (!*(volatile uint32_t*)&nar.raise[st][i]) continue;
+              raised = 1;
+              now = fmaxf(now, *(volatile float*)&nar.top[st][i][lane]);
+            }
+          }
+          if (raised) {
+            const float f = now != m ? ex2(m - now) : 1.0f;
+            if (tile > first && sums) {  // the last product into O has ended
 #pragma unroll 1
               for (int i = 0; i < D / 8; ++i) {
                 uint32_t o[8];
@@ -789,7 +884,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = now;
           }
           const float base = m == -INFINITY ? 0.0f : m;
-          l += masked ? weigh_seen(s_at, p_at, c, base, j0, sight) : weigh_all(s_at, p_at, c, base);
+          if (kNarrow) {
+            l += weigh_narrow(nar.weights[st][quarter >> 1] + lane * 128, quarter & 1, lane & 7, x,
+                              see, c, base);
+            fence_proxy_async_smem();
+          } else {
+            l += masked ? weigh_seen(s_at, p_at, c, base, j0, sight) : weigh_all(s_at, p_at, c, base);
+          }
           tmem_st_wait();
         }
         if (!real) {
@@ -828,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             found |= rows_bad[i];
           }
           if (found) {
-            if (any) {
+            if (sums) {
               if (tile == first) {  // O starts from what is added here
 #pragma unroll 1
                 for (int d = 0; d < D; ++d) tmem_st1(o_at + d, 0);
@@ -839,8 +940,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t word = j < 64 ? (j < 32 ? rows_bad[0] : rows_bad[1])
                                              : (j < 96 ? rows_bad[2] : rows_bad[3]);
                 if (!((word >> (j & 31)) & 1)) continue;
-                const uint32_t pp = tmem_ld1(p_real + (j >> 1));
-                tmem_ld_wait();
+                uint32_t pp;
+                if (kNarrow) {
+                  pp = *reinterpret_cast<volatile uint32_t*>(
+                      nar.weights[st][j >> 6] + lane * 128 + ((((j & 63) >> 3) ^ (lane & 7)) << 4) +
+                      (j & 6) * 2);
+                } else {
+                  pp = tmem_ld1(p_real + (j >> 1));
+                  tmem_ld_wait();
+                }
                 const float p = __uint_as_float(j & 1 ? pp & 0xffff0000u : pp << 16);
                 const bool sees = seen32(j0 + j, sight.lo, sight.len, sight.bits) & 1;
 #pragma unroll 1
@@ -894,6 +1002,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
+      if (kNarrow && worked) {
+        nar.sum[st][quarter][lane] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_sync[st]);
+        ok = wait_warp(&sh.v_sync[st], syncs++ & 1);
+        if (!ok) break;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l += *(volatile float*)&nar.sum[st][i][lane];
+      }
       const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
       is_first = false;
       if (!both && st == 1) {
@@ -917,9 +1035,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = l * fa + o.y * fb;
           m = now;
         }
-        if (any) {
-          const size_t row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
-          const int part_row = (t0 - w.t0) * a.group + r;
+        if (sums) {
+          const size_t out_row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
+          const int part_row = (t0 - w.t0) * a.group + row;
           const float inv = w.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
@@ -937,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
             }
             if (valid && w.whole) {
-              char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * i);
+              char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + 32 * i);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 uint32_t p[8];
@@ -969,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               stats[0] = m;
               stats[1] = l;
             } else if (a.lse) {
-              a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+              a.lse[out_row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
             }
           }
         }
@@ -991,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 bool is_power_of_two(int x) { return (x & (x - 1)) == 0; }
 
-template <int D>
+template <int D, bool kNarrow>
 cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   static std::once_flag once[64];
   int dev = 0;
@@ -999,7 +1117,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::call_once(once[dev], [] {
-    cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          (int)smem_bytes<D>());
   });
   const auto encode = tensor_map_encoder();
@@ -1011,7 +1129,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   P.fit = kTreeRows / a.group;
   P.q_tokens = a.T < P.fit ? a.T : P.fit;
   P.q_tiles = a.T > P.fit ? 2 : 1;
-  const int slots = Shape<D>::tiles - P.q_tiles;
+  P.narrow = kNarrow;
+  const int slots = Shape<D>::tiles - P.q_tiles -
+                    (kNarrow ? (int)sizeof(Narrow) / Shape<D>::tile_bytes : 0);
   P.v_slots = slots / 2;
   P.k_slots = slots - P.v_slots;
   while ((1 << P.page_shift) < a.c.page_size) ++P.page_shift;
@@ -1041,7 +1161,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return launch_behind(tree_tc_kernel<D>, a.blocks, kThreads, smem_bytes<D>(), stream, P, mq, mk, mv);
+  return launch_behind(tree_tc_kernel<D, kNarrow>, a.blocks, kThreads, smem_bytes<D>(), stream, P, mq, mk, mv);
 }
 
 }  // namespace
@@ -1061,7 +1181,9 @@ cudaError_t launch_tree_tc(TreeArgs& a, int sms, cudaStream_t stream) {
   a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
   a.stat_log2 = 1.0f;
   a.stat_ln = kLn2;
-  return a.c.head_dim == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+  const bool narrow = a.slot_rows <= kNarrowRows;
+  if (a.c.head_dim == 64) return narrow ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+  return narrow ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
 }
 
 }  // namespace dspark
