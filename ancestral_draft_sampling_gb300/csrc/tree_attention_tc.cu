@@ -719,6 +719,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
+      if (kNarrow) {  // likewise
+#pragma unroll 1
+        for (int i = 0; i < w.n && ok; i += 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (i + h >= w.n) break;
+            const bool more = i + h + 2 < w.n;
+            ok = ok && wait_warp(&sh.v_full[v.slot], v.parity);
+            if (more) ok = ok && wait_warp(&sh.k_full[k.slot], k.parity);
+            const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
+            const uint64_t kd = k_desc + k.slot * (S::tile_bytes >> 4);
+            const uint64_t pd = p_desc + h * (sizeof(nar.weights[0]) >> 4);
+            uint64_t* const v_empty = &sh.v_empty[v.slot];
+            uint64_t* const k_empty = &sh.k_empty[k.slot];
+            const bool last = i + h + 3 == w.n;
+            v.step(P.v_slots);
+            if (more) k.step(P.k_slots);
+            ok = ok && wait_warp(&sh.p_ready[h], used[h]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t add = i > 0 || *(volatile uint32_t*)&sh.add_first[h];
+            if (elect_one()) {
+              if (more) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                  const uint32_t off = ((x >> 2) * kHalfBytes + (x & 3) * 32) >> 4;
+                  mma_bf16(tmem + S::s_col(h), q_desc + off, kd + off, idesc_s, x != 0);
+                }
+                mma_commit(&sh.s_full[h]);
+                mma_commit(k_empty);
+                if (last) mma_commit(&sh.q_empty);
+              }
+#pragma unroll
+              for (int x = 0; x < kTile / 16; ++x)
+                mma_bf16(tmem + S::o_col(h), pd + (((x >> 2) * kNarrowRows * 128 + (x & 3) * 32) >> 4),
+                         vd + x * (2048 >> 4), idesc_o, x != 0 ? 1u : add);
+              mma_commit(&sh.pv_done[h]);
+              mma_commit(v_empty);
+            }
+          }
+        }
+        continue;
+      }
       for (int i = 0; i < w.n && ok; ++i) {
         // a stream's next scores go before its sums where the weights lie
         // apart, else behind them
