@@ -15,8 +15,11 @@
 // lanes); the groups are joined at the unit's end.  The next tile, of whatever
 // unit, is copied (cp.async) while one is worked on, and the pages of the one
 // behind it are looked up.  Products are packed, two a lane.  Eight warps of
-// two keys a lane waited for shared memory and shuffles half of the time
-// (119 us for 8 x 8 tokens, 4 x 8 heads, 2000 keys of 128).
+// two keys a lane waited for shared memory and shuffles half of the time (121
+// us for 8 x 8 tokens, 4 x 8 heads, 2000 keys of 128; now 84, where the FFMA
+// units' rate allows 19: they are busy 24 % of the time, shared memory 50 %, the
+// issue slots 50 %, and the four warps a scheduler has wait for each other's
+// latencies).
 #include "dspark_common.cuh"
 #include "host_util.cuh"
 #include "sm100_ptx.cuh"

@@ -16,11 +16,28 @@
 // keys and values; a smaller unit gives each stream every other tile, and the
 // two results are joined at its end.
 //
+// Narrow units, of at most 32 rows (T * group <= 32: single tokens, short
+// chains), would leave three of a stream's four warps without rows.  Their
+// queries are loaded four times, one below the other, so that every warp finds
+// all the rows in its lanes and weighs a quarter of the tile's keys.  The
+// weights go to shared memory (the product takes 128 rows from there, of which
+// 32 count), the warps agree on m through shared memory where one of them
+// raises it, and add up l at the unit's end (88 contexts of 600 keys 51.6 ->
+// 49.2 us).
+//
 // Bound by HBM while rows * 4 flops for each key element stay below the
 // tensor cores' rate, that is up to about 285 rows a key head; the layout
 // follows from that: one block a multiprocessor, keys and values in rings of
-// 32 KB (16 KB) tiles that TMA fills straight from the pages, up to 192 KB in
-// flight, which covers the latency of HBM several times over.
+// 32 KB (16 KB) tiles that TMA fills straight from the pages, 160 KB or more
+// in flight, which covers the latency of HBM several times over.  Replays on
+// one GB300, 8 key heads: 88 x 8 tokens over up to 16000 keys of 128 dims 535
+// us, 6.8 TB/s, the rate of a copy; 44 single tokens with a window of 4096 keys
+// of 64 dims 77 us, 4.4 TB/s, bound by the product warp, whose waits and
+// bookkeeping do not run under the products (some 1000 of 1700 cycles a tile;
+// two product warps, both streams at once, and fewer waits were slower); 8
+// trees of 61 tokens, 64 query heads, 5000 keys 75.5 us, 700 TFLOP/s, bound by
+// the chain scores - softmax - sums of each stream and the product warp: a pair
+// of tiles takes 3470 cycles, of which the products take 2100.
 //   warps 0, 3   fill the rings of keys and of values, a copy for each page's
 //                rows and each half of the head (64 values, 128-byte swizzle);
 //                the page numbers come 32 at a time, one load ahead.  Warp 3
@@ -32,7 +49,8 @@
 //                longer, and code comes from memory: 160 KB in all, of which a
 //                unit of a few tiles waited for 9 us); tells the merge what to
 //                do.
-//   warps 4..7, 8..11  the streams' softmax: rows 32 (w % 4) .. + 31.
+//   warps 4..7, 8..11  the streams' softmax: rows 32 (w % 4) .. + 31, or keys
+//                32 (w % 4) .. + 31 of all rows of a narrow unit.
 // Tiles that some rows see and others do not (the drafted tokens, a window's
 // edge, the sequence's end) may hold NaN or infinities in places that weigh
 // nothing, and 0 * NaN would reach every row.  Their values are looked
