@@ -12,8 +12,8 @@
 // group, and the other half of a pair sits in the lane rot_dim / 2 values
 // away (or in the same lane, for neighbouring pairs).  A warp stays on one
 // token, so the rotation's cosines are loaded once for all its heads.  Two
-// prompts of 8191 and fewer tokens take 65 us, 5.1 TB/s (0.75 of a copy's rate;
-// arithmetic keeps the issue slots 59 % busy), one token 4.3 us a replay.  Rows
+// prompts of 8191 and fewer tokens take 59 us, 5.6 TB/s, 0.83 of a copy's rate
+// (five blocks a multiprocessor; four took 64 us), one token 4.3 us a replay.  Rows
 // that do not split that way (other head dims than 8, 16 or 32 lanes hold,
 // rotations that end inside a lane's words, unaligned tables) take the row
 // kernel: a warp for each row, through shared memory.
@@ -157,7 +157,7 @@ __device__ __forceinline__ void load_floats(const float* p, float* x) {
 // the first batch is under way before the token's place is looked up (97 us
 // when each warp took one batch and looked its token up first).
 template <typename T, int kLanes, int kPer, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int splits, int batches) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(AppendArgs a, int splits, int batches) {
   constexpr int N = Word<T>::n, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31;
   const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int spli
   float wq[N], wk[N];
   if (a.q_weight) load_floats<N>(a.q_weight + d0, wq);
   if (a.k_weight) load_floats<N>(a.k_weight + d0, wk);
+  auto two = [](const float (&f)[N], int e) { return pair(f[2 * e], f[2 * e + 1]); };
   char* q_out = a.q_out + (size_t)token * Hq * row + 16 * sub;
   const size_t step = (size_t)a.c.page_size * row;  // between a page's heads
   char* k_out = static_cast<char*>(a.c.pool) +
@@ -231,31 +232,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int spli
     for (int i = 0; i < kPer; ++i) {
       const int h = h0 + i * kRows;
       const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hk;
-      float x[N], y[N];
+      if (h - lane / kLanes >= Hq + Hk) {  // values only
+        if (h < Hq + 2 * Hk && k.page >= 0)
+          *reinterpret_cast<uint4*>(v_out + (h - Hq - Hk) * step) = word[i];
+        continue;
+      }
+      float x[N];
+      uint64_t x2[N / 2];
       Word<T>::load(word[i], x);
-      if (norm) {  // the butterfly is the whole warp's
-        float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum = fmaf(x[e], x[e], sum);
+      for (int e = 0; e < N / 2; ++e) x2[e] = two(x, e);
+      if (norm) {  // the butterfly is the whole warp's
+        uint64_t sum2 = 0;
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) sum2 = fma2(x2[e], x2[e], sum2);
+        const float2 halves = unpair(sum2);
+        float sum = halves.x + halves.y;
 #pragma unroll
         for (int m = kLanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         const float r = rsqrtf(sum * (1.0f / (kLanes * N)) + a.eps);
         if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) x[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
+          for (int e = 0; e < N / 2; ++e)
+            x2[e] = mul2(mul2(x2[e], pair(r, r)), is_q ? two(wq, e) : two(wk, e));
         }
       }
-      if (kInterleaved) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) y[e] = x[e ^ 1];
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
-      }
       // a value that is not turned keeps its bits (0 * infinity is no 0)
+      uint64_t y2[N / 2];
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {
+        const float2 f = unpair(x2[e]);
+        y2[e] = kInterleaved ? pair(f.y, f.x)
+                             : pair(__shfl_sync(0xffffffffu, f.x, partner),
+                                    __shfl_sync(0xffffffffu, f.y, partner));
+      }
       if (turn) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], cs[e], y[e] * sn[e]);
+        for (int e = 0; e < N / 2; ++e)
+          x2[e] = fma2(x2[e], two(cs, e), mul2(y2[e], two(sn, e)));
+      }
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {
+        const float2 f = unpair(x2[e]);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
       }
       if (is_q) {
         *reinterpret_cast<uint4*>(q_out + h * row) = Word<T>::store(x);
