@@ -17,6 +17,8 @@ from ._lib import BF16, F32, DsparkError
 CONTROL_WORDS = 64 + 2 * 1024  # DSPARK_CACHE_CONTROL_WORDS
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None)  # absent without CUDA
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _here = contextlib.nullcontext()
 
 
@@ -92,27 +94,31 @@ class PagedCache:
         self._ref = ctypes.byref(self._struct)
 
 
+_functions = {}  # of the library, by name
+
+
 def _call(cache, fn, stream, *args):
     """Calls the library on the cache's device and on `stream` (None: that
     device's current stream)."""
+    call = _functions.get(fn)
+    if call is None:
+        call = _functions[fn] = getattr(_lib.load(), fn)
     index = cache.index
     if index < 0:
         raise ValueError("the cache is not on a CUDA device")
-    if index == torch._C._cuda_getDevice():
-        handle = (torch._C._cuda_getCurrentRawStream(index) if stream is None
-                  else stream.cuda_stream)
-        status = getattr(_lib.load(), fn)(cache._ref, *args, handle)
+    if index == _device():
+        status = call(cache._ref, *args,
+                      _stream_of(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(index):
-            handle = (torch._C._cuda_getCurrentRawStream(index) if stream is None
-                      else stream.cuda_stream)
-            status = getattr(_lib.load(), fn)(cache._ref, *args, handle)
+            status = call(cache._ref, *args,
+                          _stream_of(index) if stream is None else stream.cuda_stream)
     if status != 0:
         raise DsparkError(fn, status)
 
 
 def _bad(cache, name, t, dtype, shape):
-    """Says what is wrong with a tensor that _fits refused."""
+    """Says what is wrong with a tensor that _ptr_of refused."""
     if t.dtype != dtype or t.shape != tuple(shape):
         raise TypeError(f"{name} must be {str(dtype)[6:]} {list(shape)}")
     if not t.is_contiguous():
@@ -120,17 +126,13 @@ def _bad(cache, name, t, dtype, shape):
     raise ValueError(f"{name} must be on the cache's device")
 
 
-def _fits(cache, t, dtype, shape) -> bool:
-    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == cache.index)
-
-
 def _ptr_of(cache, name, t, dtype, shape) -> Optional[int]:
     """The address of a tensor of this dtype and shape, contiguous on the
     cache's device; None stays None."""
     if t is None:
         return None
-    if not _fits(cache, t, dtype, shape):
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != cache.index):
         _bad(cache, name, t, dtype, shape)
     return t.data_ptr()
 
