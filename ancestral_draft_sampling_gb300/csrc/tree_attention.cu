@@ -562,15 +562,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 template <typename T, int ND, bool halves>
 cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
   using L = Tiles<T, ND>;
-  static std::once_flag once[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e =
+      cudaFuncSetAttribute(tree_ffma_kernel<T, ND, halves>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, L{ND * 128}.total());
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::call_once(once[dev], [] {
-    cudaFuncSetAttribute(tree_ffma_kernel<T, ND, halves>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         L{ND * 128}.total());
-  });
   a.tile_shift = L::kTile == 64 ? 6 : 5;
   a.row_tokens = L::kRows / a.group;
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;

@@ -778,9 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        continue;
       }
-      for (int i = 0; i < w.n && ok; ++i) {
+      for (int i = kNarrow ? w.n : 0; i < w.n && ok; ++i) {
         // a stream's next scores go before its sums where the weights lie
         // apart, else behind them
         const bool more = i + (both ? 1 : 2) < w.n, last = i + (both ? 2 : 3) == w.n;
@@ -1172,15 +1171,10 @@ bool is_power_of_two(int x) { return (x & (x - 1)) == 0; }
 
 template <int D, bool kNarrow>
 cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
-  static std::once_flag once[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e =
+      cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::call_once(once[dev], [] {
-    cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)smem_bytes<D>());
-  });
   const auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   TcArgs P{};
