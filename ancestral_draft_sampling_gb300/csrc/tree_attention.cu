@@ -461,11 +461,12 @@ __global__ void __launch_bounds__(kThreads)
 // for units of 32 rows over eight blocks).
 constexpr int kMergeWarps = 4;
 
-template <typename T, int ND, int kRows>
+template <typename T, int ND>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   follow();
   const TreeJoin j = a.join[blockIdx.x + 1];  // nothing cuts the line's start
+  constexpr int kRows = 1;
   const int lane = threadIdx.x & 31, D = a.c.head_dim;
   const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kRows;
   if (r0 >= j.rows) return;
@@ -559,6 +560,102 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
+// The same for units of many rows: a warp for four rows, with a lane for each
+// row of eight parts' statistics and the loads of four parts (two of wide
+// heads) in flight.  What is done for a row is done by one lane for all of it:
+// such a merge is several waves of warps, whose instructions bound it.
+template <typename T, int ND>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    tree_merge_rows_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kBatch = ND == 1 ? 4 : 2;
+  follow();
+  const TreeJoin j = a.join[blockIdx.x + 1];
+  const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane >> 2;
+  const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * 4;
+  if (r0 >= j.rows) return;
+  const int parts = j.last - j.first + 1, mine = r0 + (lane & 3);
+  auto slot_of = [&](int p) { return p == 0 ? j.slot : 2 * (j.first + p); };
+  auto stats = [&](int p) {
+    if (p >= parts || mine >= j.rows) return make_float2(-INFINITY, 0.0f);
+    return *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p)) + 2 * mine);
+  };
+  float2 st = stats(sub);
+  float M = st.x;
+#pragma unroll 1
+  for (int p = sub + 8; p < parts; p += 8) M = fmaxf(M, stats(p).x);
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float L = 0.0f;
+  float4 o[4][ND];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < ND; ++k) o[i][k] = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += 8) {
+    const int n = parts - p0 < 8 ? parts - p0 : 8;
+    float w = 0.0f;
+#pragma unroll 1
+    for (int p = 0; p < n; p += kBatch) {
+      float4 x[kBatch][4][ND];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const float* part = tree_part(a, slot_of(p0 + p + q)) + (size_t)r0 * D + lane * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < ND; ++k) {
+            x[q][i][k] = make_float4(0, 0, 0, 0);
+            if (p + q < n && k * 128 + lane * 4 < D && r0 + i < j.rows)
+              x[q][i][k] = load4(part + i * D + k * 128);
+          }
+      }
+      if (p == 0) {
+        if (p0 > 0) st = stats(p0 + sub);
+        // a part that saw nothing weighs nothing
+        w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f((st.x - M) * a.stat_log2);
+        L += w * st.y;
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        if (p + q >= n) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, (p + q) * 4 + i);
+#pragma unroll
+          for (int k = 0; k < ND; ++k) {
+            o[i][k].x = fmaf(wi, x[q][i][k].x, o[i][k].x);
+            o[i][k].y = fmaf(wi, x[q][i][k].y, o[i][k].y);
+            o[i][k].z = fmaf(wi, x[q][i][k].z, o[i][k].z);
+            o[i][k].w = fmaf(wi, x[q][i][k].w, o[i][k].w);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+  const uint32_t t = (uint32_t)mine / (uint32_t)a.group;
+  const size_t row =
+      ((size_t)j.b * a.T + j.t0 + t) * a.heads + j.h * a.group + (mine - t * a.group);
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  if (lane < 4 && mine < j.rows && a.lse)
+    a.lse[row] = L == 0.0f ? -INFINITY : M * a.stat_ln + logf(L);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = __shfl_sync(0xffffffffu, inv, i);
+    const size_t to = __shfl_sync(0xffffffffu, row, i);
+    if (r0 + i >= j.rows) break;
+#pragma unroll
+    for (int k = 0; k < ND; ++k) {
+      const int d = k * 128 + lane * 4;
+      if (d < D)
+        put4(static_cast<T*>(a.out) + to * D + d,
+             make_float4(o[i][k].x * f, o[i][k].y * f, o[i][k].z * f, o[i][k].w * f));
+    }
+  }
+}
+
 template <typename T, int ND, bool halves>
 cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
   using L = Tiles<T, ND>;
@@ -601,8 +698,8 @@ cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream) {
   const dim3 grid(a.blocks - 1, (a.slot_rows + rows - 1) / rows);
   const auto pick = [&](auto zero) {
     using T = decltype(zero);
-    return many ? (wide ? tree_merge_kernel<T, 2, 4> : tree_merge_kernel<T, 1, 4>)
-                : (wide ? tree_merge_kernel<T, 2, 1> : tree_merge_kernel<T, 1, 1>);
+    return many ? (wide ? tree_merge_rows_kernel<T, 2> : tree_merge_rows_kernel<T, 1>)
+                : (wide ? tree_merge_kernel<T, 2> : tree_merge_kernel<T, 1>);
   };
   return launch_behind(a.c.dtype == DSPARK_F32 ? pick(0.0f) : pick(__nv_bfloat16()), grid,
                        32 * kMergeWarps, 0, stream, a);
