@@ -28,6 +28,7 @@
 namespace dspark {
 namespace {
 
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kRowGroups = 8;
 constexpr int RW = 4;  // rows of a warp
 
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreads)
           st[0] = m[i];
           st[1] = l[i];
         } else if (a.lse) {
-          a.lse[row] = l[i] == 0.0f ? -INFINITY : m[i] * a.stat_ln + logf(l[i]);
+          a.lse[row] = l[i] == 0.0f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
         }
       }
     }
@@ -452,122 +453,93 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) tree_describe(a, share.walk);
 }
 
-// Joins the partial results of the units that several blocks worked on: a
-// warp for kRows rows, o = sum_c e^(m_c - M) o_c / sum_c e^(m_c - M) l_c over
-// the unit's blocks c in order, M the largest m_c.  Bound by latency, so the
-// loads of eight parts are in flight together: one row's of eight blocks, or,
-// where units have many rows, four rows' of two (a warp a row takes 18 us for
-// 150 units of 256 rows, against 11; four rows a warp take 5 us more than one
-// for units of 32 rows over eight blocks).
+// Joins the partial results of the units that several blocks worked on: o =
+// sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the unit's blocks c in
+// order, M the largest m_c.  Units of few rows are bound by latency: a warp for
+// each row, the loads of eight parts in flight together.
 constexpr int kMergeWarps = 4;
 
 template <typename T, int ND>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kBatch = 8;
   follow();
   const TreeJoin j = a.join[blockIdx.x + 1];  // nothing cuts the line's start
-  constexpr int kRows = 1;
   const int lane = threadIdx.x & 31, D = a.c.head_dim;
-  const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kRows;
-  if (r0 >= j.rows) return;
+  const uint32_t r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  if ((int)r >= j.rows) return;
   const int parts = j.last - j.first + 1;
-  auto slot_of = [&](int i) { return i == 0 ? j.slot : 2 * (j.first + i); };
-  float M[kRows], L[kRows];
-  float4 o[kRows][ND];
+  auto slot_of = [&](int p) { return p == 0 ? j.slot : 2 * (j.first + p); };
+  float M = -INFINITY, L = 0.0f;
+  float4 o[ND];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    M[i] = -INFINITY;
-    L[i] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < ND; ++k) o[i][k] = make_float4(0, 0, 0, 0);
-  }
+  for (int k = 0; k < ND; ++k) o[k] = make_float4(0, 0, 0, 0);
 #pragma unroll 1
-  for (int p0 = 0; p0 < parts; p0 += 32) {
+  for (int p = lane; p < parts; p += 32) M = fmaxf(M, tree_part_stats(a, slot_of(p))[2 * r]);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (p0 + lane < parts && r0 + i < j.rows)
-        M[i] = fmaxf(M[i], tree_part_stats(a, slot_of(p0 + lane))[2 * (r0 + i)]);
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], x));
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
 #pragma unroll 1
   for (int p0 = 0; p0 < parts; p0 += 32) {
     const int n = parts - p0 < 32 ? parts - p0 : 32;
-    float w[kRows], lw[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      w[i] = lw[i] = 0.0f;
-      if (lane < n && r0 + i < j.rows) {
-        const float2 st =
-            *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p0 + lane)) + 2 * (r0 + i));
-        // a part that saw nothing weighs nothing
-        if (M[i] != -INFINITY) w[i] = st.x == M[i] ? 1.0f : exp2f((st.x - M[i]) * a.stat_log2);
-        lw[i] = w[i] * st.y;
-      }
+    float w = 0.0f, lw = 0.0f;
+    if (lane < n && M != -INFINITY) {  // a part that saw nothing weighs nothing
+      const float2 st =
+          *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p0 + lane)) + 2 * r);
+      w = st.x == M ? 1.0f : exp2f(st.x - M);
+      lw = w * st.y;
     }
-    constexpr int kBatch = 8 / kRows;
 #pragma unroll 1
     for (int p = 0; p < n; p += kBatch) {
-      float4 x[kBatch][kRows][ND];
+      float4 x[kBatch][ND];
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const float* part = tree_part(a, slot_of(p0 + p + q)) + (size_t)r0 * D;
+        const float* part = tree_part(a, slot_of(p0 + p + q)) + (size_t)r * D;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-          for (int k = 0; k < ND; ++k) {
-            const int d = k * 128 + lane * 4;
-            x[q][i][k] = make_float4(0, 0, 0, 0);
-            if (p + q < n && d < D && r0 + i < j.rows) x[q][i][k] = load4(part + i * D + d);
-          }
+        for (int k = 0; k < ND; ++k) {
+          const int d = k * 128 + lane * 4;
+          x[q][k] = make_float4(0, 0, 0, 0);
+          if (p + q < n && d < D) x[q][k] = load4(part + d);
+        }
       }
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         if (p + q >= n) break;
+        const float wq = __shfl_sync(0xffffffffu, w, p + q);
+        L += __shfl_sync(0xffffffffu, lw, p + q);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w[i], p + q);
-          L[i] += __shfl_sync(0xffffffffu, lw[i], p + q);
-#pragma unroll
-          for (int k = 0; k < ND; ++k) {
-            o[i][k].x = fmaf(wi, x[q][i][k].x, o[i][k].x);
-            o[i][k].y = fmaf(wi, x[q][i][k].y, o[i][k].y);
-            o[i][k].z = fmaf(wi, x[q][i][k].z, o[i][k].z);
-            o[i][k].w = fmaf(wi, x[q][i][k].w, o[i][k].w);
-          }
+        for (int k = 0; k < ND; ++k) {
+          o[k].x = fmaf(wq, x[q][k].x, o[k].x);
+          o[k].y = fmaf(wq, x[q][k].y, o[k].y);
+          o[k].z = fmaf(wq, x[q][k].z, o[k].z);
+          o[k].w = fmaf(wq, x[q][k].w, o[k].w);
         }
       }
     }
   }
+  const uint32_t t = r / (uint32_t)a.group;
+  const size_t row = ((size_t)j.b * a.T + j.t0 + t) * a.heads + j.h * a.group + (r - t * a.group);
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const uint32_t r = r0 + i;
-    if ((int)r >= j.rows) break;
-    const uint32_t t = r / (uint32_t)a.group;
-    const size_t row = ((size_t)j.b * a.T + j.t0 + t) * a.heads + j.h * a.group + (r - t * a.group);
-    const float inv = L[i] == 0.0f ? 0.0f : 1.0f / L[i];
-#pragma unroll
-    for (int k = 0; k < ND; ++k) {
-      const int d = k * 128 + lane * 4;
-      if (d < D)
-        put4(static_cast<T*>(a.out) + row * D + d,
-             make_float4(o[i][k].x * inv, o[i][k].y * inv, o[i][k].z * inv, o[i][k].w * inv));
-    }
-    if (lane == 0 && a.lse)
-      a.lse[row] = L[i] == 0.0f ? -INFINITY : M[i] * a.stat_ln + logf(L[i]);
+  for (int k = 0; k < ND; ++k) {
+    const int d = k * 128 + lane * 4;
+    if (d < D)
+      put4(static_cast<T*>(a.out) + row * D + d,
+           make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
   }
+  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
 }
 
-// The same for units of many rows: a warp for four rows, with a lane for each
-// row of eight parts' statistics and the loads of four parts (two of wide
-// heads) in flight.  What is done for a row is done by one lane for all of it:
-// such a merge is several waves of warps, whose instructions bound it.
+// The same for units of many rows, several waves of warps whose instructions
+// bound it: a warp for four rows, with a lane for each row of eight parts'
+// statistics and for what is done once a row, and the loads of two parts in
+// flight (8 trees of 61 tokens: 15 us with a row's work done by all lanes, 9
+// so).  Joining in the attention's blocks, by the one of a unit that comes
+// last, instead of this launch took 4 us more for one request and 20 for wide
+// trees.
 template <typename T, int ND>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_rows_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int kBatch = ND == 1 ? 4 : 2;
+  constexpr int kBatch = 2;
   follow();
   const TreeJoin j = a.join[blockIdx.x + 1];
   const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane >> 2;
@@ -613,7 +585,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       if (p == 0) {
         if (p0 > 0) st = stats(p0 + sub);
         // a part that saw nothing weighs nothing
-        w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f((st.x - M) * a.stat_log2);
+        w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f(st.x - M);
         L += w * st.y;
       }
 #pragma unroll
@@ -640,7 +612,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       ((size_t)j.b * a.T + j.t0 + t) * a.heads + j.h * a.group + (mine - t * a.group);
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   if (lane < 4 && mine < j.rows && a.lse)
-    a.lse[row] = L == 0.0f ? -INFINITY : M * a.stat_ln + logf(L);
+    a.lse[row] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float f = __shfl_sync(0xffffffffu, inv, i);
@@ -668,8 +640,6 @@ cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
   a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
   a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
-  a.stat_log2 = 1.0f;
-  a.stat_ln = 0.6931471805599453f;
   // warps side by side over the rows that a unit has; the rest share the keys
   int groups = ND;  // at least four keys a warp
   while (groups < kRowGroups && groups * RW < a.slot_rows) groups *= 2;

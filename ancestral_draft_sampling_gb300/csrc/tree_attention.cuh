@@ -47,9 +47,10 @@ struct TreeArgs {
   int row_tokens;  // drafted tokens of a row tile
   int row_tiles;   // of T tokens
   int slot_rows;   // rows of a partial result
-  float stat_log2, stat_ln;  // a partial maximum's unit in log2 and in ln units
   struct TreeJoin* join;  // [G] what block c of the merge has to do
-  float* part;        // [2 G][slot_rows][D] sums, then [2 G][slot_rows][2]
+  // [2 G][slot_rows][D] sums, then [2 G][slot_rows][2]: maxima (in units of
+  // log2) and sums of weights
+  float* part;
 };
 
 constexpr int kTreeMaxBlocks = 160;   // blocks of a call (the GPU has 152 SMs)

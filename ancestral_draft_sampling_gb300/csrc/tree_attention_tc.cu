@@ -1234,8 +1234,6 @@ cudaError_t launch_tree_tc(TreeArgs& a, int sms, cudaStream_t stream) {
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
   a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
   a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
-  a.stat_log2 = 1.0f;
-  a.stat_ln = kLn2;
   const bool narrow = a.slot_rows <= kNarrowRows;
   if (a.c.head_dim == 64) return narrow ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
   return narrow ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
