@@ -470,37 +470,42 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   if ((int)r >= j.rows) return;
   const int parts = j.last - j.first + 1;
   auto slot_of = [&](int p) { return p == 0 ? j.slot : 2 * (j.first + p); };
-  float M = -INFINITY, L = 0.0f;
+  auto stats = [&](int p) {
+    if (p >= parts) return make_float2(-INFINITY, 0.0f);
+    return *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p)) + 2 * r);
+  };
+  float4 x[kBatch][ND];
+  auto load_parts = [&](int p) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const float* part = tree_part(a, slot_of(p + q)) + (size_t)r * D;
+#pragma unroll
+      for (int k = 0; k < ND; ++k) {
+        const int d = k * 128 + lane * 4;
+        x[q][k] = make_float4(0, 0, 0, 0);
+        if (p + q < parts && d < D) x[q][k] = load4(part + d);
+      }
+    }
+  };
+  float2 st = stats(lane);
+  load_parts(0);  // under way while the weights are made
+  float M = st.x, L = 0.0f;
   float4 o[ND];
 #pragma unroll
   for (int k = 0; k < ND; ++k) o[k] = make_float4(0, 0, 0, 0);
 #pragma unroll 1
-  for (int p = lane; p < parts; p += 32) M = fmaxf(M, tree_part_stats(a, slot_of(p))[2 * r]);
+  for (int p = lane + 32; p < parts; p += 32) M = fmaxf(M, stats(p).x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
 #pragma unroll 1
   for (int p0 = 0; p0 < parts; p0 += 32) {
     const int n = parts - p0 < 32 ? parts - p0 : 32;
-    float w = 0.0f, lw = 0.0f;
-    if (lane < n && M != -INFINITY) {  // a part that saw nothing weighs nothing
-      const float2 st =
-          *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p0 + lane)) + 2 * r);
-      w = st.x == M ? 1.0f : exp2f(st.x - M);
-      lw = w * st.y;
-    }
+    if (p0 > 0) st = stats(p0 + lane);
+    // a part that saw nothing weighs nothing
+    const float w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f(st.x - M), lw = w * st.y;
 #pragma unroll 1
     for (int p = 0; p < n; p += kBatch) {
-      float4 x[kBatch][ND];
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const float* part = tree_part(a, slot_of(p0 + p + q)) + (size_t)r * D;
-#pragma unroll
-        for (int k = 0; k < ND; ++k) {
-          const int d = k * 128 + lane * 4;
-          x[q][k] = make_float4(0, 0, 0, 0);
-          if (p + q < n && d < D) x[q][k] = load4(part + d);
-        }
-      }
+      if (p0 + p > 0) load_parts(p0 + p);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         if (p + q >= n) break;
@@ -551,7 +556,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (p >= parts || mine >= j.rows) return make_float2(-INFINITY, 0.0f);
     return *reinterpret_cast<const float2*>(tree_part_stats(a, slot_of(p)) + 2 * mine);
   };
+  float4 x[kBatch][4][ND];
+  auto load_parts = [&](int p) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const float* part = tree_part(a, slot_of(p + q)) + (size_t)r0 * D + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < ND; ++k) {
+          x[q][i][k] = make_float4(0, 0, 0, 0);
+          if (p + q < parts && k * 128 + lane * 4 < D && r0 + i < j.rows)
+            x[q][i][k] = load4(part + i * D + k * 128);
+        }
+    }
+  };
   float2 st = stats(sub);
+  load_parts(0);  // under way while the weights are made
   float M = st.x;
 #pragma unroll 1
   for (int p = sub + 8; p < parts; p += 8) M = fmaxf(M, stats(p).x);
@@ -566,28 +587,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll 1
   for (int p0 = 0; p0 < parts; p0 += 8) {
     const int n = parts - p0 < 8 ? parts - p0 : 8;
-    float w = 0.0f;
+    if (p0 > 0) st = stats(p0 + sub);
+    // a part that saw nothing weighs nothing
+    const float w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f(st.x - M);
+    L += w * st.y;
 #pragma unroll 1
     for (int p = 0; p < n; p += kBatch) {
-      float4 x[kBatch][4][ND];
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const float* part = tree_part(a, slot_of(p0 + p + q)) + (size_t)r0 * D + lane * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < ND; ++k) {
-            x[q][i][k] = make_float4(0, 0, 0, 0);
-            if (p + q < n && k * 128 + lane * 4 < D && r0 + i < j.rows)
-              x[q][i][k] = load4(part + i * D + k * 128);
-          }
-      }
-      if (p == 0) {
-        if (p0 > 0) st = stats(p0 + sub);
-        // a part that saw nothing weighs nothing
-        w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f(st.x - M);
-        L += w * st.y;
-      }
+      if (p0 + p > 0) load_parts(p0 + p);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         if (p + q >= n) break;
