@@ -30,12 +30,12 @@
 // follows from that: one block a multiprocessor, keys and values in rings of
 // 32 KB (16 KB) tiles that TMA fills straight from the pages, 160 KB or more
 // in flight, which covers the latency of HBM several times over.  Replays on
-// one GB300, 8 key heads: 88 x 8 tokens over up to 16000 keys of 128 dims 535
+// one GB300, 8 key heads: 88 x 8 tokens over up to 16000 keys of 128 dims 534
 // us, 6.8 TB/s, the rate of a copy; 44 single tokens with a window of 4096 keys
-// of 64 dims 77 us, 4.4 TB/s, bound by the product warp, whose waits and
+// of 64 dims 76 us, 4.5 TB/s, bound by the product warp, whose waits and
 // bookkeeping do not run under the products (some 1000 of 1700 cycles a tile;
 // two product warps, both streams at once, and fewer waits were slower); 8
-// trees of 61 tokens, 64 query heads, 5000 keys 75.5 us, 700 TFLOP/s, bound by
+// trees of 61 tokens, 64 query heads, 5000 keys 70 us, 760 TFLOP/s, bound by
 // the chain scores - softmax - sums of each stream and the product warp: a pair
 // of tiles takes 3470 cycles, of which the products take 2100.
 //   warps 0, 3   fill the rings of keys and of values, a copy for each page's
