@@ -525,16 +525,20 @@ __device__ __noinline__ bool fill_ring(const TcArgs& P, Control& sh, bool values
   Unit next{}, cur{};
   Pages next_pages{}, pages{};
   bool some = units.next(sh, next, ok, lane);
+  if (some && values && lane == 0)  // the first queries go before the pages are known
+    load_queries<D>(P, next, map_q, q_tile, &sh.q_full);
   if (some) next_pages.set(P, next, lane);
 #pragma unroll 1
   while (some && ok) {
     cur = next;
     pages = next_pages;
     if (values) {
-      if (unit > 0) ok = wait_warp(&sh.q_empty, (unit - 1) & 1);
-      if (!ok) break;
-      if (lane == 0) load_queries<D>(P, cur, map_q, q_tile, &sh.q_full);
-      __syncwarp();
+      if (unit > 0) {
+        ok = wait_warp(&sh.q_empty, (unit - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) load_queries<D>(P, cur, map_q, q_tile, &sh.q_full);
+        __syncwarp();
+      }
       ++unit;
     }
     int ids2 = pages.load(P, pages.first + 32 + lane);
