@@ -9,17 +9,18 @@
 // Scores are in units of log2, so that a weight is one ex2.
 //
 // Sixteen warps share a tile of 64 keys (32 where head_dim is above 128) in
-// shared memory.  A warp holds four rows, and two to sixteen groups
-// of warps take the same rows and part of the keys each, with statistics of
-// their own (a row's maximum is the warp's; its sum stays spread over the
-// lanes); the groups are joined at the unit's end.  The next tile, of whatever
-// unit, is copied (cp.async) while one is worked on, and the pages of the one
-// behind it are looked up.  Products are packed, two a lane.  Eight warps of
-// two keys a lane waited for shared memory and shuffles half of the time (121
-// us for 8 x 8 tokens, 4 x 8 heads, 2000 keys of 128; now 84, where the FFMA
-// units' rate allows 19: they are busy 24 % of the time, shared memory 50 %, the
-// issue slots 50 %, and the four warps a scheduler has wait for each other's
-// latencies).
+// shared memory.  A warp holds four rows (eight warps with eight rows each where
+// there are enough), and two to sixteen groups of warps take the same rows and
+// part of the keys each, with statistics of their own (a row's maximum is the
+// warp's; its sum stays spread over the lanes); the groups are joined at the
+// unit's end.  The next tile, of whatever unit, is copied (cp.async) while one is
+// worked on, and the pages of the one behind it are looked up.  Products are
+// packed, two a lane.  For 8 x 8 tokens, 4 x 8 heads, 2000 keys of 128 dims: 81
+// us, where the FFMA units' rate allows 19.  A tile takes some 11000 cycles:
+// scores 3500 and sums 3500, of which the products are 2000 each and the rest
+// loads from shared memory (a load that all lanes share costs as much as one of
+// their own of the same width), softmax 1500, the copies' issue 1850.  Loads one
+// step ahead, copies of whole rows in bulk and a lane for each key were slower.
 #include "dspark_common.cuh"
 #include "host_util.cuh"
 #include "sm100_ptx.cuh"
@@ -29,8 +30,7 @@ namespace dspark {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 16, kThreads = 32 * kWarps, kRowGroups = 8;
-constexpr int RW = 4;  // rows of a warp
+constexpr int kRows = 32;  // of a unit
 
 __device__ __forceinline__ float4 load4(const float* p) {
   return *reinterpret_cast<const float4*>(p);
@@ -63,10 +63,10 @@ __device__ __forceinline__ void copy16(void* to, const void* from, bool there) {
 }
 
 // Shared memory of a block, in bytes.
-template <typename T, int ND>
+template <typename T, int ND, int RW>
 struct Tiles {
+  static constexpr int kWarps = 2 * kRows / RW, kThreads = 32 * kWarps;
   static constexpr int kTile = ND == 1 ? 64 : 32;  // keys
-  static constexpr int kRows = kRowGroups * RW;    // rows of a unit
   int D;
   __host__ __device__ int pad() const { return D + 16 / (int)sizeof(T); }  // rows on different banks
   __host__ __device__ int key_bytes() const { return kTile * pad() * (int)sizeof(T); }
@@ -75,7 +75,7 @@ struct Tiles {
   // the queries, and at a unit's end the parts that groups leave each other
   __host__ __device__ int q_at() const { return 2 * stage(); }
   __host__ __device__ int p_at() const { return q_at() + kRows * (D + 4) * 4; }
-  __host__ __device__ int where_at() const { return p_at() + kWarps * (kTile / 2) * RW * 8; }
+  __host__ __device__ int where_at() const { return p_at() + kWarps * (kTile / 2) * RW * 4; }
   __host__ __device__ int total() const { return where_at() + 2 * kTile * 8; }
 };
 
@@ -94,22 +94,21 @@ struct NextTile {
 // ND: chunks of 128 dims that a warp's four each cover (1: D <= 128, 2: D <=
 // 256); halves: half a warp covers them (D <= 64), so the other half of it takes
 // the sums over every other key (60 tokens over 1500 keys of 64: 116 -> 96 us).
-template <typename T, int ND, bool halves>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int ND, bool halves, int RW>
+__global__ void __launch_bounds__(Tiles<T, ND, RW>::kThreads)
     tree_ffma_kernel(const __grid_constant__ TreeArgs a, int row_groups) {
-  using L = Tiles<T, ND>;
-  constexpr int kTile = L::kTile;
+  using L = Tiles<T, ND, RW>;
+  constexpr int kTile = L::kTile, kWarps = L::kWarps, kThreads = L::kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ TreeShare share;
-  __shared__ uchar2 row_of[L::kRows];  // a row's token and head
+  __shared__ uchar2 row_of[kRows];  // a row's token and head
   const int D = a.c.head_dim, DP = D + 4;
   const L layout{D};
   const int pad = layout.pad(), words = D * (int)sizeof(T) / 16;
   float* qs = reinterpret_cast<float*>(smem + layout.q_at());  // [kRows][DP], scaled
   long long* where = reinterpret_cast<long long*>(smem + layout.where_at());  // [2][kTile]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // weights, each twice: the pair that a packed product takes
-  uint64_t* pw = reinterpret_cast<uint64_t*>(smem + layout.p_at()) + warp * (kTile / 2) * RW;
+  float* pw = reinterpret_cast<float*>(smem + layout.p_at()) + warp * (kTile / 2) * RW;  // weights
   // the warp's rows and keys
   const int key_groups = kWarps / row_groups, rg = warp & (row_groups - 1), kg = warp / row_groups;
   const int keys = kTile / key_groups, key0 = kg * keys;
@@ -129,7 +128,7 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int key_step = halves ? 2 : 1;
   const T* q = static_cast<const T*>(a.q);
   const char* pool = static_cast<const char*>(a.c.pool);
-  if (threadIdx.x < L::kRows) {
+  if (threadIdx.x < kRows) {
     const uint32_t t = threadIdx.x / (uint32_t)a.group;
     row_of[threadIdx.x] = make_uchar2(t, threadIdx.x - t * a.group);
   }
@@ -327,14 +326,19 @@ __global__ void __launch_bounds__(kThreads)
           o[i][x][0] = mul2(o[i][x][0], pair(keep, keep));
           o[i][x][1] = mul2(o[i][x][1], pair(keep, keep));
         }
-        if (lane < keys) pw[lane_key * RW + i] = pair(p, p);
+        if (lane < keys) pw[lane_key * RW + i] = p;
       }
       __syncwarp();
       auto add = [&](int j, bool every) {
-        ulonglong2 p[RW / 2];
+        float p[RW];
 #pragma unroll
-        for (int i = 0; i < RW / 2; ++i)
-          p[i] = *reinterpret_cast<const ulonglong2*>(pw + j * RW + 2 * i);
+        for (int i = 0; i < RW; i += 4) {
+          const float4 x = load4(pw + j * RW + i);
+          p[i] = x.x;
+          p[i + 1] = x.y;
+          p[i + 2] = x.z;
+          p[i + 3] = x.w;
+        }
 #pragma unroll
         for (int x = 0; x < ND; ++x) {
           const int d = x * 128 + dim;
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
               if (!every && !((seen[i] >> holder(j)) & 1)) continue;
-              const uint64_t pi = i & 1 ? p[i / 2].y : p[i / 2].x;
+              const uint64_t pi = pair(p[i], p[i]);
               o[i][x][0] = fma2(pi, v0, o[i][x][0]);
               o[i][x][1] = fma2(pi, v1, o[i][x][1]);
             }
@@ -634,37 +638,46 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
-template <typename T, int ND, bool halves>
+template <typename T, int ND, bool halves, int RW>
 cudaError_t launch_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
-  using L = Tiles<T, ND>;
+  using L = Tiles<T, ND, RW>;
   const cudaError_t e =
-      cudaFuncSetAttribute(tree_ffma_kernel<T, ND, halves>,
+      cudaFuncSetAttribute(tree_ffma_kernel<T, ND, halves, RW>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, L{ND * 128}.total());
   if (e != cudaSuccess) return e;
   a.tile_shift = L::kTile == 64 ? 6 : 5;
-  a.row_tokens = L::kRows / a.group;
+  a.row_tokens = kRows / a.group;
   a.row_tiles = (a.T + a.row_tokens - 1) / a.row_tokens;
   a.slot_rows = (a.T < a.row_tokens ? a.T : a.row_tokens) * a.group;
   a.blocks = sms < kTreeMaxBlocks ? sms : kTreeMaxBlocks;
   // warps side by side over the rows that a unit has; the rest share the keys
-  int groups = ND;  // at least four keys a warp
-  while (groups < kRowGroups && groups * RW < a.slot_rows) groups *= 2;
-  return launch_behind(tree_ffma_kernel<T, ND, halves>, a.blocks, kThreads, L{a.c.head_dim}.total(),
+  int groups = RW == 4 ? ND : 1;  // at least four keys a warp
+  while (groups < kRows / RW && groups * RW < a.slot_rows) groups *= 2;
+  return launch_behind(tree_ffma_kernel<T, ND, halves, RW>, a.blocks, L::kThreads, L{a.c.head_dim}.total(),
                        stream, a, groups);
 }
 
-template <typename T>
+template <typename T, int RW>
 cudaError_t launch_ffma_dims(TreeArgs& a, int sms, cudaStream_t stream) {
-  if (a.c.head_dim > 128) return launch_ffma<T, 2, false>(a, sms, stream);
-  return a.c.head_dim > 64 ? launch_ffma<T, 1, false>(a, sms, stream)
-                           : launch_ffma<T, 1, true>(a, sms, stream);
+  if (a.c.head_dim > 128) return launch_ffma<T, 2, false, RW>(a, sms, stream);
+  return a.c.head_dim > 64 ? launch_ffma<T, 1, false, RW>(a, sms, stream)
+                           : launch_ffma<T, 1, true, RW>(a, sms, stream);
+}
+
+// Eight rows a warp read keys and values half as often from shared memory, but
+// leave two warps a scheduler: 81 us against 83 for 8 x 8 tokens with 4 heads
+// each, 90 against 96 for 60 tokens, 82 against 78 for 3 tokens with 6.
+template <typename T>
+cudaError_t launch_ffma_rows(TreeArgs& a, int sms, cudaStream_t stream) {
+  return a.T * a.group > 24 ? launch_ffma_dims<T, 8>(a, sms, stream)
+                            : launch_ffma_dims<T, 4>(a, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream) {
-  return a.c.dtype == DSPARK_F32 ? launch_ffma_dims<float>(a, sms, stream)
-                                 : launch_ffma_dims<__nv_bfloat16>(a, sms, stream);
+  return a.c.dtype == DSPARK_F32 ? launch_ffma_rows<float>(a, sms, stream)
+                                 : launch_ffma_rows<__nv_bfloat16>(a, sms, stream);
 }
 
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream) {
