@@ -543,7 +543,8 @@ DSPARK_API dspark_status dspark_cache_accept(
  *                pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) when
  *                `interleaved`: (a, b) -> (a c - b s, b c + a s).
  *   position     [B,T] int32 rows of cos_sin.
- *   token_count  [B] int32 or NULL (T): tokens of sequence b; later rows of
+ *   token_count  [B] int32 or NULL (T): tokens of sequence b (below 0: none,
+ *                above T: T); later rows of
  *                q_out and later places of the cache are left as they are.
  *   q_out        [B,T,heads,D] dense (may be q when that is dense).
  * Everything runs in float32 and is rounded once; values are copied.  A token
@@ -576,7 +577,8 @@ DSPARK_API size_t dspark_tree_workspace_bytes(int B, int T, int heads,
  *                t itself, all tokens in a block that sees itself whole.
  *                mask_stride words lie between two sequences (0: one tree for
  *                all).  NULL: token t sees tokens 0..t.
- *   token_count  [B] int32 or NULL (T): drafted tokens of sequence b.  Later
+ *   token_count  [B] int32 or NULL (T): drafted tokens of sequence b (below 0:
+ *                none, above T: T).  Later
  *                rows of out and lse are left as they are, later keys are not
  *                read.
  *   window       0, or the number of positions that a token sees: token t

@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import ancestral_draft_sampling_gb300 as dspark
 from tests.cache_ref import place
 from tests.test_gpu_tree_attention import Case
 
@@ -83,3 +84,29 @@ def test_units_over_several_blocks(cuda, dtype, D, group):
     a, b = s.run(), s.run()
     s.check(*a)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype,D,group", [(BF, 128, 5), (BF, 64, 32), (F32, 64, 8)])
+def test_nothing_to_do(cuda, dtype, D, group):
+    """Counts of zero and below for all, and lengths of zero: nothing is
+    written, or a token sees itself alone."""
+    s = Case(dtype, D, 1, group, 6, [300, 40, 0], 16, "causal", seed=11)
+    for none in (0, -1, -(2 ** 31)):
+        out, lse = torch.full_like(s.q, 3.0), torch.full((3, 6, group), 3.0, device="cuda")
+        s.count = [none] * 3
+        s.run(out=out, lse=lse)
+        assert (out == 3).all() and (lse == 3).all()
+        dspark.read_device_error(s.c)
+    s = Case(dtype, D, 1, group, 1, [0, 0], 16, "causal", seed=12)
+    s.check(*s.run())
+    assert torch.equal(s.run()[0][0, 0], s.v[0][0, 0].to("cuda").expand(group, D))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_counts_beyond_the_call(cuda, dtype):
+    """A count above T is T."""
+    s = Case(dtype, 64, 1, 2, 4, [30, 10, 60], 16, "causal", seed=13)
+    good = s.run()[0]
+    s.count = [4, 5, 2 ** 31 - 1]
+    assert torch.equal(s.run()[0], good)
+    assert dspark.read_device_error(s.c) == 0
