@@ -32,12 +32,13 @@
 // in flight, which covers the latency of HBM several times over.  Replays on
 // one GB300, 8 key heads: 88 x 8 tokens over up to 16000 keys of 128 dims 534
 // us, 6.8 TB/s, the rate of a copy; 44 single tokens with a window of 4096 keys
-// of 64 dims 76 us, 4.5 TB/s, bound by the product warp, whose waits and
-// bookkeeping do not run under the products (some 1000 of 1700 cycles a tile;
-// two product warps, both streams at once, and fewer waits were slower); 8
-// trees of 61 tokens, 64 query heads, 5000 keys 70 us, 760 TFLOP/s, bound by
-// the chain scores - softmax - sums of each stream and the product warp: a pair
-// of tiles takes 3470 cycles, of which the products take 2100.
+// of 64 dims 76 us, 4.5 TB/s: 1400 cycles a tile, which the chain scores -
+// softmax - sums of each stream and the product warp bound alike (the same with
+// the keys in L2; two product warps, both streams at once and waits handed to
+// the softmax warps were no faster), and 8000 at each of a block's two or three
+// unit ends; 8 trees of 61 tokens, 64 query heads, 5000 keys 70 us, 760 TFLOP/s,
+// bound by the same chain: a pair of tiles takes 3470 cycles, of which the
+// products take 2100.
 //   warps 0, 3   fill the rings of keys and of values, a copy for each page's
 //                rows and each half of the head (64 values, 128-byte swizzle);
 //                the page numbers come 32 at a time, one load ahead.  Warp 3
