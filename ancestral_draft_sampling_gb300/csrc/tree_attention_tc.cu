@@ -36,7 +36,7 @@
 // softmax - sums of each stream and the product warp bound alike (the same with
 // the keys in L2; two product warps, both streams at once and waits handed to
 // the softmax warps were no faster), and 8000 at each of a block's two or three
-// unit ends; 8 trees of 61 tokens, 64 query heads, 5000 keys 70 us, 760 TFLOP/s,
+// unit ends; 8 trees of 61 tokens, 64 query heads, 5000 keys 69 us, 770 TFLOP/s,
 // bound by the same chain: a pair of tiles takes 3470 cycles, of which the
 // products take 2100.
 //   warps 0, 3   fill the rings of keys and of values, a copy for each page's
@@ -857,29 +857,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = kNarrow ? lane : r;
     const int r_token = (int)((uint32_t)row / (uint32_t)a.group), r_head = row - r_token * a.group;
     UnitReader units;
-    Unit w;
-#pragma unroll 1
-    for (; ok && units.next(sh, w, ok, lane); g += w.n) {
+    // A unit, and what hides keys from this thread's row of it.  The next one's
+    // is loaded before this one's results are written.
+    struct View {
+      Unit w;
+      int t0, rows;
+      Sight sight;
+      int lo_most;  // committed keys below this are hidden from some row
+    };
+    auto look_at = [&](View& x) {
+      const Unit& w = x.w;
       const int left = w.cnt - w.t0;
+      x.t0 = w.t0 + (!kNarrow && w.both && st ? P.fit : 0);
+      const int more = w.cnt - x.t0, tokens = more < P.fit ? more : P.fit;
+      x.rows = tokens * a.group;
+      const int t = x.t0 + r_token;
+      const bool valid = row < x.rows;
+      x.sight = Sight{valid ? tree_window_lo(a, w.b, t, w.len) : 0, w.len,
+                      valid ? tree_mask(a, w.b, t, w.cnt) : 0};
+      x.lo_most = 0;
+      if (a.window > 0) {
+        for (int i = lane; i < left && i < a.row_tokens; i += 32) {
+          const int lo = tree_window_lo(a, w.b, w.t0 + i, w.len);
+          x.lo_most = lo > x.lo_most ? lo : x.lo_most;
+        }
+      }
+    };
+    View cur, next;
+    bool some = units.next(sh, cur.w, ok, lane);
+    if (some) look_at(cur);
+#pragma unroll 1
+    for (; ok && some; g += cur.w.n, cur = next) {
+      const Unit& w = cur.w;
       const bool both = !kNarrow && w.both;       // half the rows each
-      const int t0 = w.t0 + (both && st ? P.fit : 0);
-      const int more = w.cnt - t0, tokens = more < P.fit ? more : P.fit;
-      const int rows = tokens * a.group;
-      const int t = t0 + r_token;
+      const int t0 = cur.t0, rows = cur.rows, t = t0 + r_token, len = w.len;
       // narrow: all warps weigh, the first one has the sums
       const bool valid = row < rows, any = kNarrow || quarter * 32 < rows;
       const bool sums = kNarrow ? quarter == 0 : any;
-      const uint64_t bits = valid ? tree_mask(a, w.b, t, w.cnt) : 0;
-      const int len = w.len;
-      const Sight sight{valid ? tree_window_lo(a, w.b, t, len) : 0, len, bits};
-      int lo_most = 0;  // committed keys below this are hidden from some row
-      if (a.window > 0) {
-        for (int i = lane; i < left && i < a.row_tokens; i += 32) {
-          const int x = tree_window_lo(a, w.b, w.t0 + i, len);
-          lo_most = x > lo_most ? x : lo_most;
-        }
-        lo_most = __reduce_max_sync(0xffffffffu, lo_most);
-      }
+      const Sight sight = cur.sight;
+      const int lo_most = a.window > 0 ? __reduce_max_sync(0xffffffffu, cur.lo_most) : 0;
       float m = -INFINITY, l = 0.0f;
       const int first = both ? 0 : st, step = both ? 1 : 2;
       // The block's first tile is rehearsed while its data are on their way:
@@ -1062,6 +1078,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool worked = first < w.n;  // the stream had a tile of this unit
+      some = units.next(sh, next.w, ok, lane);
+      if (!ok) break;
+      if (some) look_at(next);
       if (worked) {
         ok = wait_warp(&sh.pv_done[st], (used - 1) & 1);
         if (!ok) break;
