@@ -110,3 +110,17 @@ def test_counts_beyond_the_call(cuda, dtype):
     s.count = [4, 5, 2 ** 31 - 1]
     assert torch.equal(s.run()[0], good)
     assert dspark.read_device_error(s.c) == 0
+
+
+WIDE_FFMA = [  # dtype, head_dim, key heads, group, tokens, lengths, page: the FFMA kernel, many rows
+    (F32, 256, 1, 8, 5, [100, 33], 16), (BF, 256, 2, 32, 3, [70, 0], 24), (BF, 96, 1, 16, 4, [130], 12),
+    (F32, 72, 1, 7, 9, [90, 1], 5), (F32, 8, 1, 32, 4, [77], 3), (F32, 128, 1, 25, 1, [200, 64], 16),
+    (BF, 200, 1, 17, 2, [65], 7), (F32, 64, 2, 6, 64, [50], 16), (F32, 160, 1, 3, 9, [31, 32, 33], 32)]
+
+
+@pytest.mark.parametrize("dtype,D,kv,group,T,length,page", WIDE_FFMA)
+def test_many_rows_of_any_width(cuda, dtype, D, kv, group, T, length, page):
+    s = Case(dtype, D, kv, group, T, length, page, "tree", seed=D + T)
+    s.check(*s.run())
+    s.window = 40
+    s.check(*s.run())
