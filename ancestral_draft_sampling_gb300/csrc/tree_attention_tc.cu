@@ -115,7 +115,10 @@ struct Control {  // shared memory behind the tiles
   uint64_t p_ready[2], v_sync[2];  // of each stream
   // sums have been read: by the first stream at the end of every unit (both
   // streams' where it joins them), by the second where it has rows of its own.
-  // Nobody arrives without work in the unit, so no phase is run ahead of.
+  // Nobody arrives without work in the unit, so no phase is run ahead of.  The
+  // products wait for them, and so does the second stream before it adds to its
+  // sums by hand: a unit's first scores are there before the last unit's sums
+  // have been read.
   uint64_t o_free[2];
   uint64_t u_full[kUnits], u_empty[kUnits];
   Unit units[kUnits];
@@ -850,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t o_at = lanes + S::o_col(st), p_real = lanes + S::p_col(st);
     const float c = a.scale * kLog2e;
-    int g = 0;                       // tiles of the units before
+    int g = 0, unit = 0;             // tiles of the units before, and those units
     uint32_t used = 0, syncs = 0, alls = 0, joins = 0;  // phases of the barriers
     bool is_first = true;            // the block's first unit
     // the row's token and head within a query tile
@@ -887,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool some = units.next(sh, cur.w, ok, lane);
     if (some) look_at(cur);
 #pragma unroll 1
-    for (; ok && some; g += cur.w.n, cur = next) {
+    for (; ok && some; g += cur.w.n, ++unit, cur = next) {
       const Unit& w = cur.w;
       const bool both = !kNarrow && w.both;       // half the rows each
       const int t0 = cur.t0, rows = cur.rows, t = t0 + r_token, len = w.len;
@@ -1010,6 +1013,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             found |= rows_bad[i];
           }
           if (found) {
+            if (st == 1 && tile == first && unit > 0) {
+              // the first stream may still be reading the last unit's sums, its
+              // join with these; it cannot end this unit before this stream has
+              // gone on, so the phase is the last one or this one
+              ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
             if (sums) {
               if (tile == first) {  // O starts from what is added here
 #pragma unroll 1
