@@ -43,6 +43,17 @@ dspark_status check_heads(int heads, int kv_heads) {
   return DSPARK_OK;
 }
 
+// Whether one of n rows of `row` bytes, `step` (>= row) bytes apart, has a byte
+// of the `bytes` ones at `to`.  The rows of a token are parts of a projection's
+// output, and what lies between them is not theirs.
+bool rows_meet(const void* rows, __int128 step, __int128 row, __int128 n, const void* to,
+               __int128 bytes) {
+  const __int128 from = reinterpret_cast<uintptr_t>(rows), at = reinterpret_cast<uintptr_t>(to);
+  // the first row that ends behind `at`
+  const __int128 i = from + row > at ? 0 : (at - from - row) / step + 1;
+  return i < n && from + i * step < at + bytes;
+}
+
 // The workspace of the attention: what the merge has to do, then the partial
 // results, two a block; no kernel has larger units than the tensor-core one.
 struct TreeLayout {
@@ -149,6 +160,13 @@ dspark_status dspark_cache_append(
   // q_out may be q only where both lie alike
   if (q_out == q && q_stride != (int64_t)heads * D) return DSPARK_ERR_INVALID_ARG;
   if ((long long)B * T >= (1 << 24) || heads > 32768) return DSPARK_ERR_UNSUPPORTED;
+  // warps read rows while others write queries
+  const int64_t tokens = (int64_t)B * T, elt = dtype_bytes(cache->dtype);
+  const int64_t q_row = heads * D * elt, kv_row = cache->kv_heads * D * elt;
+  if ((q_out != q && rows_meet(q, q_stride * (__int128)elt, q_row, tokens, q_out, tokens * q_row)) ||
+      rows_meet(k, k_stride * (__int128)elt, kv_row, tokens, q_out, tokens * q_row) ||
+      rows_meet(v, v_stride * (__int128)elt, kv_row, tokens, q_out, tokens * q_row))
+    return DSPARK_ERR_INVALID_ARG;
   AppendArgs a{};
   a.c = *cache;
   a.layer = layer;

@@ -546,7 +546,8 @@ DSPARK_API dspark_status dspark_cache_accept(
  *   token_count  [B] int32 or NULL (T): tokens of sequence b (below 0: none,
  *                above T: T); later rows of
  *                q_out and later places of the cache are left as they are.
- *   q_out        [B,T,heads,D] dense (may be q when that is dense).
+ *   q_out        [B,T,heads,D] dense.  It may be q when that is dense; else it
+ *                must not overlap a token's rows of q, k or v.
  * Everything runs in float32 and is rounded once; values are copied.  A token
  * whose page is not held is not stored (error 7); one with a position outside
  * the table is not rotated (error 10).  One launch, B * T < 2^24.
