@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 #include <utility>
 
@@ -32,6 +33,17 @@ inline int sm_count() {
     cache[dev].store(n, std::memory_order_relaxed);
   }
   return n;
+}
+
+// DSPARK_TEST_STALL_WAIT=1 (tests of the failure path only): the tensor-core
+// kernels' product issuers wait, with a limit of kStallPolls polls, for a
+// barrier phase that nothing completes and that guards no copy (the draft
+// block's: the second phase of the barrier of u, once u is ready), so that the
+// wait runs out, the kernel records kDevErrTimeout and takes its abort path.
+constexpr uint32_t kStallPolls = 1u << 12;
+inline bool stall_first_wait_requested() {
+  const char* env = std::getenv("DSPARK_TEST_STALL_WAIT");
+  return env != nullptr && env[0] == '1';
 }
 
 inline dspark_status from_cuda(cudaError_t e) {

@@ -53,8 +53,6 @@
 // Every mbarrier wait is bounded; on a timeout the kernel records an error
 // in the workspace control word, stops issuing work, waits (bounded) for
 // its in-flight copies and MMAs, frees its TMEM and returns.
-#include <cstdlib>
-#include <mutex>
 
 #include "dspark_common.cuh"
 #include "host_util.cuh"
@@ -82,7 +80,6 @@ constexpr int kMaxRows = (kMaxBpad + kComputeWarps - 1) / kComputeWarps;  // req
 constexpr uint32_t kTmemCols = 256;                // two accumulators
 constexpr uint32_t kAccCols = 128;
 constexpr uint32_t kSpin = 1u << 22;
-constexpr uint32_t kStallPolls = 1u << 12;  // the stalled wait's poll limit
 // Fewest Wb stages the kernel runs with.  Two is what bf16 drafter logits
 // leave at r = 256 and 81..96 requests (one staging tile): 519 us for a
 // B=88, K=7, V=200064 block, against 4255 us on the FFMA kernel.
@@ -993,16 +990,6 @@ position_tc_kernel(const __grid_constant__ CUtensorMap wb_map,
 }
 
 // ------------------------------------------------------------ host side
-// DSPARK_TEST_STALL_WAIT=1 (tests of the failure path only): once u is
-// ready, the MMA issuer waits for the u barrier's second phase, which
-// nothing completes, with a short poll limit, so that the wait runs out,
-// the kernel records kDevErrTimeout and takes its abort path.  That wait
-// guards no copy.
-bool stall_first_wait_requested() {
-  const char* env = std::getenv("DSPARK_TEST_STALL_WAIT");
-  return env != nullptr && env[0] == '1';
-}
-
 struct Layout {
   int bpad, stages, stage_bufs;
   uint32_t u_off, tile_off, stage_off, rows_off, rstate_off, bar_off;

@@ -282,6 +282,7 @@ struct TcArgs {
   int page_shift;        // log2 of the page size
   int out32;             // out is aligned to 32 bytes
   int narrow;            // at most 32 rows a unit: the kernel's other form
+  int stall;             // failure-path test: the product warp's wait runs out
 };
 
 // A role's place in a ring: the slot, and the parity of its phase.
@@ -704,6 +705,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
       if (freed < halved) ok = ok && wait_warp(&sh.o_free[1], freed++ & 1);
       halved += both;
+      // failure-path test: scores are on their way, and nothing completes this
+      // phase but the abort path itself
+      if (P.stall) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.drain, 0, kStallPolls));
       if (both && !apart) {  // bound by the products: as little as can be between them
 #pragma unroll 1
         for (int i = 0; i < w.n && ok; ++i) {
@@ -1220,6 +1224,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   P.q_tokens = a.T < P.fit ? a.T : P.fit;
   P.q_tiles = a.T > P.fit ? 2 : 1;
   P.narrow = kNarrow;
+  P.stall = stall_first_wait_requested();
   const int slots = Shape<D>::tiles - P.q_tiles -
                     (kNarrow ? (int)sizeof(Narrow) / Shape<D>::tile_bytes : 0);
   P.v_slots = slots / 2;
