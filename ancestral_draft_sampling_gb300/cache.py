@@ -17,8 +17,11 @@ from ._lib import BF16, F32, DsparkError
 CONTROL_WORDS = 64 + 2 * 1024  # DSPARK_CACHE_CONTROL_WORDS
 
 
-_device = getattr(torch._C, "_cuda_getDevice", None)  # absent without CUDA
-_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and a device's current stream, as a number: torch's own
+# functions behind the public ones, which cost less, where it has them.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_of = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+              or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 _here = contextlib.nullcontext()
 
 
