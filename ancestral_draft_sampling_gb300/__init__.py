@@ -436,10 +436,11 @@ def noise_words(seed: int, offset: int, k: int, stream_id: int, n: int,
 
 def read_device_error(workspace, stream=None) -> int:
     """Reads and clears the device error word of a DraftWorkspace or a
-    PagedCache (synchronises)."""
+    PagedCache (synchronises `stream`, or its device's current one)."""
     code = ctypes.c_int(0)
-    st = _lib.load().dspark_read_device_error(
-        _ptr(workspace.buffer), ctypes.byref(code), _stream(stream))
+    with _torch().cuda.device(workspace.buffer.device):
+        st = _lib.load().dspark_read_device_error(
+            _ptr(workspace.buffer), ctypes.byref(code), _stream(stream))
     if st not in (0, 5):
         _lib.check("dspark_read_device_error", st)
     return code.value

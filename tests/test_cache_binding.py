@@ -5,6 +5,7 @@ import importlib.util
 import pytest
 import torch
 
+import ancestral_draft_sampling_gb300 as dspark
 import ancestral_draft_sampling_gb300.cache as binding
 from ancestral_draft_sampling_gb300 import _lib
 from tests.test_cache_abi import host_cache
@@ -73,3 +74,24 @@ def test_calls_without_torchs_private_functions(fake, monkeypatch, missing, inde
     cache._call(c, "dspark_cache_init", Stream(index, 7))
     assert [(name, args[-1], device) for name, args, device in fake.calls] == [
         ("dspark_cache_init", 100 + index, index), ("dspark_cache_init", 7, index)]
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_the_error_word_is_read_on_its_own_device(fake, index):
+    """On the stream that the calls on that device run on, whichever device is
+    the current one: another device's stream is not ordered behind them."""
+    class Buffer:
+        device = torch.device("cuda", index)
+
+        def get_device(self):
+            return index
+
+        def data_ptr(self):
+            return 4096
+
+    class Held:
+        buffer = Buffer()
+    assert dspark.read_device_error(Held()) == 0
+    assert dspark.read_device_error(Held(), stream=Stream(index, 7)) == 0
+    assert [(name, args[0], args[2], device) for name, args, device in fake.calls] == [
+        ("dspark_read_device_error", 4096, 100 + index, index), ("dspark_read_device_error", 4096, 7, index)]
