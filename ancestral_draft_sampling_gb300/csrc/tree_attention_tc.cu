@@ -662,30 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && wait_warp(&sh.k_full[k.slot], k.parity);
       tc_fence_after();
     };
-    auto weighed = [&](int st) {
-      ok = ok && wait_warp(&sh.p_ready[st], used[st]++ & 1);
-      tc_fence_after();
-    };
-    auto sums = [&](int st, bool first, bool free_values) {
-      const uint32_t add = !first || *(volatile uint32_t*)&sh.add_first[st];
-      const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
-      if (elect_one()) {
-        if (kNarrow) {
-          const uint64_t pd = p_desc + st * (sizeof(nar.weights[0]) >> 4);
-#pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_bf16(tmem + S::o_col(st), pd + (((i >> 2) * kNarrowRows * 128 + (i & 3) * 32) >> 4),
-                     vd + i * (2048 >> 4), idesc_o, i != 0 ? 1u : add);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_bf16_ta(tmem + S::o_col(st), tmem + S::p_col(st) + 8 * i, vd + i * (2048 >> 4),
-                        idesc_o, i != 0 ? 1u : add);
-        }
-        mma_commit(&sh.pv_done[st]);
-        if (free_values) mma_commit(&sh.v_empty[v.slot]);
-      }
-    };
     UnitReader units;
     Unit w;
 #pragma unroll 1
@@ -791,28 +767,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      for (int i = kNarrow ? w.n : 0; i < w.n && ok; ++i) {
-        // a stream's next scores go before its sums where the weights lie
-        // apart, else behind them
-        const bool more = i + (both ? 1 : 2) < w.n, last = i + (both ? 2 : 3) == w.n;
-        bool there = false;  // the next keys
-        for (int h = 0; h < (both ? 2 : 1) && ok; ++h) {
-          const int st = both ? h : i & 1;
-          auto next_scores = [&]() {
-            if (h == 0 && !there) keys();  // both streams use the same ones
-            if (ok) scores(st, both ? h : 0, !both || h == 1, last && (!both || h == 1));
-          };
-          if (h == 0) {  // behind the weights nothing should be waited for
-            ok = wait_warp(&sh.v_full[v.slot], v.parity);
-            there = more && over_warp(&sh.k_full[k.slot], k.parity);
+      if constexpr (!kNarrow) {
+        auto weighed = [&](int st) {
+          ok = ok && wait_warp(&sh.p_ready[st], used[st]++ & 1);
+          tc_fence_after();
+        };
+        auto sums = [&](int st, bool first, bool free_values) {
+          const uint32_t add = !first || *(volatile uint32_t*)&sh.add_first[st];
+          const uint64_t vd = v_desc + v.slot * (S::tile_bytes >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i)
+              mma_bf16_ta(tmem + S::o_col(st), tmem + S::p_col(st) + 8 * i, vd + i * (2048 >> 4),
+                          idesc_o, i != 0 ? 1u : add);
+            mma_commit(&sh.pv_done[st]);
+            if (free_values) mma_commit(&sh.v_empty[v.slot]);
           }
-          weighed(st);
-          if (apart && more && ok) next_scores();
-          if (!ok) break;
-          sums(st, i < (both ? 1 : 2), !both || h == 1);
-          if (!apart && more) next_scores();
+        };
+        for (int i = 0; i < w.n && ok; ++i) {
+          // a stream's next scores go before its sums where the weights lie
+          // apart, else behind them
+          const bool more = i + (both ? 1 : 2) < w.n, last = i + (both ? 2 : 3) == w.n;
+          bool there = false;  // the next keys
+          for (int h = 0; h < (both ? 2 : 1) && ok; ++h) {
+            const int st = both ? h : i & 1;
+            auto next_scores = [&]() {
+              if (h == 0 && !there) keys();  // both streams use the same ones
+              if (ok) scores(st, both ? h : 0, !both || h == 1, last && (!both || h == 1));
+            };
+            if (h == 0) {  // behind the weights nothing should be waited for
+              ok = wait_warp(&sh.v_full[v.slot], v.parity);
+              there = more && over_warp(&sh.k_full[k.slot], k.parity);
+            }
+            weighed(st);
+            if (apart && more && ok) next_scores();
+            if (!ok) break;
+            sums(st, i < (both ? 1 : 2), !both || h == 1);
+            if (!apart && more) next_scores();
+          }
+          v.step(P.v_slots);
         }
-        v.step(P.v_slots);
       }
     }
     if (!ok) {
