@@ -264,8 +264,8 @@ def tree_attention(cache: PagedCache, layer: int, q, length, *, mask=None, token
     ``layer``, their own keys and values (cache_append) included: all
     committed tokens (the last ``window`` positions if given), and the drafted
     tokens that mask allows: int64 words [B, T] or [T], bit j of word t says
-    that token t sees drafted token j (None: tokens 0..t).  scale defaults to
-    1 / sqrt(D).  Returns (out, lse); lse is None unless asked for."""
+    that token t sees drafted token j (None: tokens 0..t, whatever the window).
+    scale defaults to 1 / sqrt(D).  Returns (out, lse); lse is None unless asked for."""
     if q.dim() != 4:
         raise ValueError("q must be [B, T, heads, D]")
     B, T, heads, D = q.shape

@@ -12,11 +12,19 @@
 // group, and the other half of a pair sits in the lane rot_dim / 2 values
 // away (or in the same lane, for neighbouring pairs).  A warp stays on one
 // token, so the rotation's cosines are loaded once for all its heads.  Two
-// prompts of 8191 and fewer tokens take 59 us, 5.6 TB/s, 0.83 of a copy's rate
-// (five blocks a multiprocessor; four took 64 us), one token 4.3 us a replay.  Rows
-// that do not split that way (other head dims than 8, 16 or 32 lanes hold,
-// rotations that end inside a lane's words, unaligned tables) take the row
-// kernel: a warp for each row, through shared memory.
+// prompts of 8191 and fewer tokens, 8 x 4 heads of 128 dims, take 59 us with
+// neighbouring pairs, 5.6 TB/s, 0.83 of a copy's rate, and 76.5 with pairs half a
+// rotation apart, whose partners come from other lanes; one token 4.3 us a replay.
+// Five blocks a multiprocessor, four in brackets, us a replay: neighbouring pairs
+// 60.4 (62.0), 64 dims 34.9 (36.4), 256 dims 112.7 (116.2); half-split pairs 76.5
+// (80.0), 64 dims 43.4 (45.1), 256 dims 143.4 (147.6), although five blocks' 96
+// registers spill 56 to 64 bytes there; the drafts of a full batch 8.3 (9.7);
+// float32, whose lanes hold half the values and spill nothing either way, 73.5
+// (71.8) and with neighbouring pairs 63.0 (62.4).  Rows that do not split that way
+// (other head dims than 8, 16 or 32 lanes hold, rotations that end inside a lane's
+// words, unaligned tables) take the row kernel: a warp for each row, through shared
+// memory, one value a load: 332 us for such prompts with heads of 96 dims (0.75
+// TB/s), bound by its instructions, and 6.2 us for one token.
 #include "cache.cuh"
 #include "host_util.cuh"
 

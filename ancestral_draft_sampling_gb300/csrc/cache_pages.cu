@@ -108,6 +108,10 @@ __device__ __noinline__ int give_many(const dspark_cache& c, const GiveList& g, 
 // minimum, so the stack is the same on every run).  There is nothing to
 // compete for where each page either had one hold or still has some, and no
 // places to count where all go on the stack.
+// Up to four entries a thread are walked once and held in registers (4096
+// entries: 13 us with the launch, where the general form takes 22); longer lists
+// take the general form, a chain of four walks in one block: 4160 entries 25 us,
+// 22000 pages of 88 sequences 84 us.  A sequence gives up so many pages once.
 constexpr int kPer = 4;  // entries of a thread, their loads in flight together
 
 __device__ void give_pages(const dspark_cache& c, const GiveList& g, int B,

@@ -584,7 +584,9 @@ DSPARK_API size_t dspark_tree_workspace_bytes(int B, int T, int heads,
  *                read.
  *   window       0, or the number of positions that a token sees: token t
  *                sees committed token j if position[b][t] - j < window.  The
- *                mask alone rules the drafted tokens.
+ *                mask alone rules the drafted tokens: with a NULL mask and a
+ *                window below T a token sees drafted ones beyond the window, and
+ *                a caller that wants them hidden leaves their bits out.
  *   position     [B,T] int32 or NULL (length[b] + t), used with a window; a
  *                position below length[b] counts as length[b].
  *   scale        of the scores q.k, finite.
@@ -596,8 +598,10 @@ DSPARK_API size_t dspark_tree_workspace_bytes(int B, int T, int heads,
  *   workspace    dspark_tree_workspace_bytes(...) bytes, 256-byte aligned; its
  *                contents need not be initialised.  Two calls in flight at
  *                the same time must not share it.
- * Scores, softmax statistics and sums are float32; bfloat16 inputs multiply
- * weights rounded to bfloat16 (relative error 2^-8 each).  Keys and values of
+ * Scores, softmax statistics and sums are float32.  The tensor cores multiply
+ * weights rounded to bfloat16 (relative error 2^-8 at most each, the sum of the
+ * weights being that of the unrounded ones); the FFMA kernel multiplies float32
+ * weights, also of bfloat16 inputs.  Keys and values of
  * places that a token does not see never reach its result, whatever they
  * hold.  A sequence whose length or pages are out of range is not computed
  * (error 6 or 7; its rows are left as they are); a table entry that names no
