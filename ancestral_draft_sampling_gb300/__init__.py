@@ -20,20 +20,23 @@ __all__ = ["draft_block", "draft_block_per_request", "draft_block_noalloc",
            "draft_block_host", "HostWorkspace", "verify_standard", "verify_block",
            "PagedCache", "TreeWorkspace", "cache_reserve", "cache_release",
            "cache_fork", "cache_accept", "cache_append", "tree_attention",
+           "cache_bounds", "select_pages", "SelectWorkspace",
            "noise_words", "workspace_bytes", "read_device_error",
            "DraftWorkspace", "DsparkError", "F32", "BF16", "version"]
 
 
 _CACHE = ("PagedCache", "TreeWorkspace", "cache_reserve", "cache_release",
           "cache_fork", "cache_accept", "cache_append", "tree_attention")
+_PART = ("cache_bounds", "select_pages", "SelectWorkspace")
 
 
 def __getattr__(name):
-    """The paged cache (cache.py) is loaded, and torch with it, when it is
-    first asked for."""
-    if name in _CACHE:
-        from . import cache
+    """The paged cache (cache.py, part.py) is loaded, and torch with it, when it
+    is first asked for."""
+    if name in _CACHE or name in _PART:
+        from . import cache, part
         globals().update({n: getattr(cache, n) for n in _CACHE})
+        globals().update({n: getattr(part, n) for n in _PART})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

@@ -46,6 +46,9 @@ EXPORTED = (
     "dspark_cache_append",
     "dspark_tree_workspace_bytes",
     "dspark_tree_attention",
+    "dspark_cache_bounds",
+    "dspark_select_workspace_bytes",
+    "dspark_select_pages",
     "dspark_noise_words",
     "dspark_noise_words_folded",
     "dspark_read_device_error",
@@ -137,7 +140,13 @@ def load() -> ctypes.CDLL:
         lib.dspark_tree_attention.argtypes = [
             C, I, P, P, P, P, P, I64, P, I, F, I, I, I, P, P, P,
             ctypes.c_size_t, P]
-        for name in ("init", "reserve", "release", "fork", "accept", "append"):
+        lib.dspark_cache_bounds.argtypes = [C, P, P, P, I, P, P]
+        lib.dspark_select_workspace_bytes.argtypes = [C, I, I, I]
+        lib.dspark_select_workspace_bytes.restype = ctypes.c_size_t
+        lib.dspark_select_pages.argtypes = [
+            C, I, P, P, P, P, P, I, I, I, I, I, I, I, P, P, ctypes.c_size_t, P]
+        lib.dspark_select_pages.restype = I
+        for name in ("init", "reserve", "release", "fork", "accept", "append", "bounds"):
             getattr(lib, "dspark_cache_" + name).restype = I
         lib.dspark_tree_attention.restype = I
         lib.dspark_tree_workspace_bytes.argtypes = [I, I, I, I, I]

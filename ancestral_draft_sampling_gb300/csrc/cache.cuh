@@ -149,6 +149,34 @@ __device__ __forceinline__ int block_exclusive(int v, int* warps, int& total) {
   return warps[warp] + x - v;
 }
 
+// The row of flat entry e of rows that begin at offset[0 .. B - 1].
+__device__ __forceinline__ int row_of(const int* offset, int B, int e) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offset[mid] <= e) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// offset[] from each row's count (thread b holds row b's; B <= blockDim
+// passes of blockDim rows otherwise).
+__device__ __forceinline__ void row_offsets(int* offset, const int* counts,
+                                            int B, int* warps) {
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    const int n = b < B ? counts[b] : 0;
+    int total;
+    const int x = block_exclusive(n, warps, total);
+    if (b < B) offset[b] = base + x;
+    base += total;
+  }
+  if (threadIdx.x == 0) offset[B] = base;
+  __syncthreads();
+}
+
 cudaError_t launch_cache_init(const dspark_cache& c, cudaStream_t stream);
 cudaError_t launch_cache_reserve(const dspark_cache& c, const int32_t* seq,
                                  const int32_t* length, int tokens, int B,
@@ -179,5 +207,21 @@ struct AppendArgs {
   char* q_out;
 };
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
+
+// Bytes from the start of the bounds to those of a page and head of a layer:
+// head_dim minima, then head_dim maxima.
+__host__ __device__ __forceinline__ size_t bounds_row(const dspark_cache& c, int layer, int page,
+                                                      int head) {
+  return (((size_t)layer * c.num_pages + page) * c.kv_heads + head) *
+         ((size_t)2 * c.head_dim * dtype_bytes(c.dtype));
+}
+
+struct BoundsArgs {
+  dspark_cache c;
+  const int32_t *seq, *start, *length;
+  int B;
+  char* bounds;
+};
+cudaError_t launch_cache_bounds(const BoundsArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace dspark

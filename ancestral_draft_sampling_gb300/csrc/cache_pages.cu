@@ -30,34 +30,6 @@ struct GiveList {
   int offset[kMaxB + 1];
 };
 
-// The row of flat entry e.
-__device__ __forceinline__ int row_of(const int* offset, int B, int e) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (offset[mid] <= e) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
-// offset[] from each row's count (thread b holds row b's; B <= blockDim
-// passes of blockDim rows otherwise).
-__device__ __forceinline__ void row_offsets(int* offset, const int* counts,
-                                            int B, int* warps) {
-  int base = 0;
-  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    const int n = b < B ? counts[b] : 0;
-    int total;
-    const int x = block_exclusive(n, warps, total);
-    if (b < B) offset[b] = base + x;
-    base += total;
-  }
-  if (threadIdx.x == 0) offset[B] = base;
-  __syncthreads();
-}
-
 // The same for a list of any length: the entries are walked anew in each step.
 __device__ __noinline__ int give_many(const dspark_cache& c, const GiveList& g, int B, int top,
                                       int* warps) {

@@ -619,6 +619,75 @@ DSPARK_API dspark_status dspark_tree_attention(
     int window, float scale, int B, int T, int heads, void* out, float* lse,
     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------- reading part of the cache
+ *
+ * A long context costs a query its whole length.  The calls below let it read
+ * less: dspark_cache_bounds keeps the smallest and largest keys of every full
+ * page, dspark_select_pages chooses pages for each query by them, and
+ * dspark_sparse_attention attends over the chosen ones; and
+ * dspark_prefix_attention reads what several sequences share (dspark_cache_fork)
+ * once for all of them.
+ *
+ * The caller owns the bounds: [layers][num_pages][kv_heads][2][head_dim] of the
+ * cache's dtype, 16-byte aligned, the smallest keys and then the largest.  They
+ * are kept by page, so sequences that share a page share its bounds.  A page
+ * counts as full, and is chosen, when all its tokens are committed. */
+
+/*
+ * dspark_cache_bounds -- the bounds, in every layer, of the pages that the
+ * sequences have filled between `start` [B] and `length` [B] committed tokens:
+ * those whose last token lies in [start, length).  A call behind each
+ * dspark_cache_accept or prompt, with the lengths before and after it, keeps
+ * them; a length below its start fills nothing.  Other bounds are left as they
+ * are.  A NaN among a page's keys makes the bounds of its dimension NaN.  A
+ * sequence that holds fewer than `length` tokens is left out (error 7).  One
+ * launch.
+ */
+DSPARK_API dspark_status dspark_cache_bounds(const dspark_cache* cache,
+                                             const int32_t* seq,
+                                             const int32_t* start,
+                                             const int32_t* length, int B,
+                                             void* bounds, cudaStream_t stream);
+
+/* Device workspace of dspark_select_pages (0 if unsupported). */
+DSPARK_API size_t dspark_select_workspace_bytes(const dspark_cache* cache, int B,
+                                                int T, int shared);
+
+/*
+ * dspark_select_pages -- for each drafted token and key head (or, with
+ * `shared`, for all of a sequence's tokens together) the `count` full pages of
+ * the sequence whose keys can have the largest products with the queries.
+ *
+ *   q            [B,T,heads,D] dense, the cache's dtype, 16-byte aligned.
+ *   bounds       of every layer, as dspark_cache_bounds keeps them.
+ *   token_count  [B] int32 or NULL (T), as in dspark_tree_attention: lists of
+ *                later tokens are left as they are, and a shared list goes by
+ *                the tokens that there are.
+ *   first, last  so many of the sequence's first and of its last full pages
+ *                are always taken; they count.  first + last <= count.
+ *   pages        [B,T,kv_heads,count] int32 out ([B,1,kv_heads,count] with
+ *                `shared`): the pages' numbers within the sequence (tokens
+ *                page * page_size ..), ascending, then -1 where the sequence
+ *                has fewer full pages.
+ * A page's score is the largest, over the query heads of the key head (and over
+ * the tokens with `shared`), of sum_d max(q_d min_d, q_d max_d): no product of
+ * q with a key of the page exceeds it.  (For attention with scale > 0.)  The
+ * choice is that of exact scores: where float32 leaves it open, pages are
+ * scored in 64 bits, whose sums are off by 2^-53 of their terms.  Equal scores
+ * go to the lower page; a score that is not a number counts as infinite.
+ * 1 <= T <= 64, group <= 32.  A sequence whose length is out of range is left out
+ * (error 6 or 7); a table entry that names no page has the lowest score (error
+ * 7).  Two launches, graph capturable; the same result on every run.  The
+ * workspace's contents need not be initialised; two calls in flight at the
+ * same time must not share it.
+ */
+DSPARK_API dspark_status dspark_select_pages(
+    const dspark_cache* cache, int layer, const int32_t* seq,
+    const int32_t* length, const int32_t* token_count, const void* q,
+    const void* bounds, int count, int first, int last, int shared, int B, int T,
+    int heads, int32_t* pages, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
 /*
  * dspark_noise_words -- diagnostic: writes the n raw Philox words the
  * sampler uses for elements 0..n-1 of (seed, offset, position k, stream),

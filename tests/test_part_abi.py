@@ -1,0 +1,88 @@
+"""CPU-only checks of the calls that read part of the cache: what they refuse,
+with a status and before any launch (the fake device addresses are never read),
+and what the Python functions refuse."""
+import ctypes
+
+import pytest
+import torch
+
+import ancestral_draft_sampling_gb300 as dspark
+from tests.test_cache_abi import (BAD_CACHES, FAKE, INVALID, UNSUPPORTED, WORKSPACE, host_cache, lib, struct)  # noqa: F401
+
+
+def bounds(lib, c=None, **over):
+    a = dict(c=c or ctypes.byref(struct()), seq=None, start=FAKE, length=FAKE, B=2, bounds=FAKE)
+    a.update(over)
+    return lib.dspark_cache_bounds(a["c"], a["seq"], a["start"], a["length"], a["B"], a["bounds"], None)
+
+
+def select(lib, c=None, **over):
+    c = c or ctypes.byref(struct())
+    a = dict(layer=0, seq=None, length=FAKE, tokens=None, q=FAKE, bounds=FAKE, count=4, first=0, last=0, shared=0,
+             B=2, T=4, heads=4, pages=FAKE, ws=FAKE,
+             bytes=lib.dspark_select_workspace_bytes(ctypes.byref(struct()), 2, 4, 0))
+    a.update(over)
+    return lib.dspark_select_pages(
+        c, a["layer"], a["seq"], a["length"], a["tokens"], a["q"], a["bounds"], a["count"], a["first"], a["last"],
+        a["shared"], a["B"], a["T"], a["heads"], a["pages"], a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("over,want", BAD_CACHES)
+def test_every_call_checks_the_cache(lib, over, want):
+    c = ctypes.byref(struct(**over))
+    assert bounds(lib, c=c) == want and select(lib, c=c) == want
+    assert lib.dspark_select_workspace_bytes(c, 2, 4, 0) == 0
+
+
+@pytest.mark.parametrize("B,want", [(0, INVALID), (-3, INVALID), (1025, UNSUPPORTED)])
+def test_batch_limits(lib, B, want):
+    assert bounds(lib, B=B) == want and select(lib, B=B) == want
+    assert lib.dspark_select_workspace_bytes(ctypes.byref(struct()), B, 4, 0) == 0
+
+
+@pytest.mark.parametrize("over", [dict(start=None), dict(length=None), dict(bounds=None), dict(seq=FAKE + 2),
+                                  dict(start=FAKE + 1), dict(length=FAKE + 2), dict(bounds=FAKE + 8)])
+def test_bounds_refuses(lib, over):
+    assert bounds(lib, **over) == INVALID
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(length=None), INVALID), (dict(q=None), INVALID), (dict(bounds=None), INVALID), (dict(pages=None), INVALID),
+    (dict(layer=2), INVALID), (dict(layer=-1), INVALID), (dict(T=0), INVALID), (dict(heads=5), INVALID),
+    (dict(heads=0), INVALID), (dict(count=0), INVALID), (dict(first=-1), INVALID), (dict(last=-1), INVALID),
+    (dict(first=5), INVALID), (dict(first=2, last=3), INVALID), (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), INVALID),
+    (dict(q=FAKE + 8), INVALID), (dict(bounds=FAKE + 8), INVALID), (dict(pages=FAKE + 2), INVALID),
+    (dict(tokens=FAKE + 1), INVALID), (dict(seq=FAKE + 1), INVALID), (dict(T=65), UNSUPPORTED),
+    (dict(heads=66), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 64), WORKSPACE),
+    (dict(bytes=1000), WORKSPACE), (dict(shared=1, bytes=100), WORKSPACE),
+])
+def test_select_refuses(lib, over, want):
+    assert select(lib, **over) == want
+
+
+def test_select_workspace_bytes(lib):
+    c = ctypes.byref(struct())
+    f = lib.dspark_select_workspace_bytes
+    assert 0 < f(c, 2, 4, 1) < f(c, 2, 4, 0) and f(c, 2, 4, 0) % 256 == 0
+    assert f(c, 2, 65, 0) == 0 and f(c, 2, 0, 0) == 0
+    assert f(ctypes.byref(struct(kv_heads=1024, max_seqs=1, max_pages=1 << 27, page_size=1)), 1024, 1, 0) == 0
+
+
+def test_python_refuses_tensors_that_do_not_fit(lib):
+    c = host_cache()
+    i32 = torch.int32
+    one, q = torch.zeros(1, dtype=i32), torch.zeros(1, 3, 4, 8)
+    b = torch.zeros(1, 6, 2, 2, 8)
+    with pytest.raises(ValueError):  # a cache in host memory is not launched on
+        dspark.cache_bounds(c, one, one, bounds=b)
+    for bad in (dict(start=one.long()), dict(length=torch.zeros(2, dtype=i32)), dict(bounds=b[:, :5]),
+                dict(bounds=b.double()), dict(bounds=b.transpose(3, 4).contiguous().transpose(3, 4)), dict(seq=one.long())):
+        a = dict(start=one, length=one, bounds=b) | bad
+        with pytest.raises((TypeError, ValueError)):
+            dspark.cache_bounds(c, a.pop("start"), a.pop("length"), **a)
+    for bad in (dict(q=q[0]), dict(q=q.double()), dict(bounds=b[0]), dict(length=one.long()),
+                dict(pages=torch.zeros(1, 3, 2, 5, dtype=i32)), dict(pages=torch.zeros(1, 3, 2, 4)),
+                dict(pages=torch.zeros(1, 3, 2, 4, dtype=i32), shared=True), dict(token_count=one.long())):
+        a = dict(bounds=b, q=q, length=one, pages=torch.zeros(1, 3, 2, 4, dtype=i32)) | bad
+        with pytest.raises((TypeError, ValueError)):
+            dspark.select_pages(c, 0, a.pop("bounds"), a.pop("q"), a.pop("length"), 4, **a)
