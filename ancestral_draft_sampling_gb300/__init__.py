@@ -20,14 +20,16 @@ __all__ = ["draft_block", "draft_block_per_request", "draft_block_noalloc",
            "draft_block_host", "HostWorkspace", "verify_standard", "verify_block",
            "PagedCache", "TreeWorkspace", "cache_reserve", "cache_release",
            "cache_fork", "cache_accept", "cache_append", "tree_attention",
-           "cache_bounds", "select_pages", "SelectWorkspace",
+           "cache_bounds", "select_pages", "SelectWorkspace", "sparse_attention",
+           "SparseWorkspace", "prefix_attention", "PrefixWorkspace",
            "noise_words", "workspace_bytes", "read_device_error",
            "DraftWorkspace", "DsparkError", "F32", "BF16", "version"]
 
 
 _CACHE = ("PagedCache", "TreeWorkspace", "cache_reserve", "cache_release",
           "cache_fork", "cache_accept", "cache_append", "tree_attention")
-_PART = ("cache_bounds", "select_pages", "SelectWorkspace")
+_PART = ("cache_bounds", "select_pages", "SelectWorkspace", "sparse_attention",
+         "SparseWorkspace", "prefix_attention", "PrefixWorkspace")
 
 
 def __getattr__(name):

@@ -49,6 +49,10 @@ EXPORTED = (
     "dspark_cache_bounds",
     "dspark_select_workspace_bytes",
     "dspark_select_pages",
+    "dspark_sparse_workspace_bytes",
+    "dspark_sparse_attention",
+    "dspark_prefix_workspace_bytes",
+    "dspark_prefix_attention",
     "dspark_noise_words",
     "dspark_noise_words_folded",
     "dspark_read_device_error",
@@ -146,6 +150,15 @@ def load() -> ctypes.CDLL:
         lib.dspark_select_pages.argtypes = [
             C, I, P, P, P, P, P, I, I, I, I, I, I, I, P, P, ctypes.c_size_t, P]
         lib.dspark_select_pages.restype = I
+        lib.dspark_sparse_workspace_bytes.argtypes = [C, I, I, I, I]
+        lib.dspark_prefix_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.dspark_sparse_attention.argtypes = [
+            C, I, P, P, P, P, P, I, I, P, I64, F, I, I, I, P, P, P, ctypes.c_size_t, P]
+        lib.dspark_prefix_attention.argtypes = [
+            C, I, P, P, P, P, P, P, I, P, I64, F, I, I, I, P, P, P, ctypes.c_size_t, P]
+        for name in ("sparse", "prefix"):
+            getattr(lib, f"dspark_{name}_workspace_bytes").restype = ctypes.c_size_t
+            getattr(lib, f"dspark_{name}_attention").restype = I
         for name in ("init", "reserve", "release", "fork", "accept", "append", "bounds"):
             getattr(lib, "dspark_cache_" + name).restype = I
         lib.dspark_tree_attention.restype = I

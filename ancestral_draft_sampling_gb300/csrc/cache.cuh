@@ -25,6 +25,7 @@ enum CacheError : int {
   kCacheErrPath = 9,
   kCacheErrPosition = 10,
   kCacheErrFork = 11,
+  kCacheErrGroup = 12,
 };
 
 __device__ __forceinline__ void cache_error(const dspark_cache& c, int code) {

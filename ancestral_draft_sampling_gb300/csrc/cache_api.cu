@@ -213,8 +213,14 @@ dspark_status dspark_tree_attention(
   a.lse = lse;
   a.join = static_cast<TreeJoin*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.part);
-  cudaError_t e = tree_tc_supported(a) ? launch_tree_tc(a, sm_count(), stream)
-                                       : launch_tree_ffma(a, sm_count(), stream);
+  cudaError_t e;
+  if (tree_tc_supported(a)) {
+    tree_tc_plan(a, T, sm_count());
+    e = launch_tree_tc(a, stream);
+  } else {
+    tree_ffma_plan(a, T, sm_count());
+    e = launch_tree_ffma(a, stream);
+  }
   if (e == cudaSuccess) e = launch_tree_merge(a, stream);
   return from_cuda(e);
 }

@@ -1,8 +1,10 @@
 // part_api.cu -- the C ABI of what reads part of the cache (include/dspark.h):
-// bounds of pages and their selection.
+// bounds of pages, their selection, the attention over selected pages and that
+// over shared prefixes.
 #include <cmath>
 
 #include "cache_check.cuh"
+#include "part_attention.cuh"
 #include "select_pages.cuh"
 
 namespace {
@@ -36,6 +38,122 @@ dspark_status select_sizes(const dspark_cache* c, int B, int T) {
       (long long)B * c->kv_heads * ((c->max_pages + kScoreChunk - 1) / kScoreChunk) >= (1LL << 31))
     return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
+}
+
+// The checks of the attention's sizes.
+dspark_status attention_sizes(int B, int T, int heads, int kv_heads, int D) {
+  if (B <= 0 || T <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0) return DSPARK_ERR_INVALID_ARG;
+  if (B > DSPARK_CACHE_MAX_B || T > DSPARK_TREE_MAX_TOKENS || kv_heads > 1024 ||
+      heads / kv_heads > DSPARK_TREE_MAX_GROUP || D < 8 || D > 256 || D % 8 != 0)
+    return DSPARK_ERR_UNSUPPORTED;
+  return DSPARK_OK;
+}
+
+// What the attention needs for units of up to `tokens` tokens, `items` of them:
+// the merge's work, partial results (two a block), the items and their work.
+struct ItemLayout {
+  size_t part, items, work, end;
+};
+
+ItemLayout item_layout(long long tokens, size_t items, int group, int D) {
+  ItemLayout L;
+  L.part = align_up((size_t)2 * kTreeMaxBlocks * sizeof(TreeJoin), 256);
+  const int fit = 2 * (kTreeRows / group);  // tokens of a tensor-core unit, the largest
+  const size_t rows = (size_t)(tokens < fit ? tokens : fit) * group * 2 * kTreeMaxBlocks;
+  L.items = align_up(L.part + rows * (D + 2) * sizeof(float), 256);
+  L.work = align_up(L.items + items * sizeof(TreeItem), 256);
+  L.end = align_up(L.work + items * sizeof(long long), 256);
+  return L;
+}
+
+struct SparseLayout {
+  ItemLayout items;
+  int room;
+  size_t list, bits, total;
+};
+
+SparseLayout sparse_layout(const dspark_cache& c, int B, int T, int heads, int count) {
+  SparseLayout L;
+  const size_t n = (size_t)B * c.kv_heads;
+  L.items = item_layout(T, n, heads / c.kv_heads, c.head_dim);
+  const long long named = (long long)count * T;
+  L.room = (int)(named < c.max_pages ? named : c.max_pages) + T / c.page_size + 2;
+  L.list = L.items.end;
+  L.bits = align_up(L.list + n * L.room * sizeof(int32_t), 256);
+  L.total = align_up(L.bits + n * L.room * sizeof(uint64_t), 256);
+  return L;
+}
+
+struct PrefixLayout {
+  ItemLayout items;
+  size_t base, group_of, whole, total;
+};
+
+PrefixLayout prefix_layout(int B, int T, int heads, int kv_heads, int D) {
+  PrefixLayout L;
+  L.items = item_layout((long long)B * T, (size_t)2 * B, heads / kv_heads, D);
+  L.base = L.items.end;
+  L.group_of = align_up(L.base + ((size_t)2 * B + 1) * sizeof(long long), 256);
+  L.whole = align_up(L.group_of + (size_t)B * sizeof(int32_t), 256);
+  L.total = align_up(L.whole + (size_t)2 * B * T * heads * (D + 2) * sizeof(float), 256);
+  return L;
+}
+
+// What both attentions check, and the arguments that they share.
+dspark_status fill_attention(TreeArgs& a, const dspark_cache* cache, int layer, const int32_t* seq,
+                             const int32_t* length, const int32_t* token_count, const void* q,
+                             const uint64_t* mask, int64_t mask_stride, float scale, int B, int T,
+                             int heads, void* out, float* lse) {
+  dspark_status st = check_cache(cache);
+  if (st == DSPARK_OK) st = check_batch(B);
+  if (st == DSPARK_OK) st = check_heads(heads, cache->kv_heads);
+  if (st != DSPARK_OK) return st;
+  if (!length || !q || !out || T <= 0 || layer < 0 || layer >= cache->layers ||
+      !std::isfinite(scale) || (mask && mask_stride != 0 && mask_stride < T))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(out, 16) || (mask && !aligned_to(mask, 8)))
+    return DSPARK_ERR_INVALID_ARG;
+  const void* p4[] = {seq, length, token_count, lse};
+  for (const void* p : p4)
+    if (!is4(p)) return DSPARK_ERR_INVALID_ARG;
+  st = attention_sizes(B, T, heads, cache->kv_heads, cache->head_dim);
+  if (st != DSPARK_OK) return st;
+  // blocks read queries while others write results
+  const uintptr_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(out);
+  const size_t bytes = (size_t)B * T * heads * cache->head_dim * dtype_bytes(cache->dtype);
+  if (from < to + bytes && to < from + bytes) return DSPARK_ERR_INVALID_ARG;
+  a.c = *cache;
+  a.layer = layer;
+  a.seq = seq;
+  a.length = length;
+  a.count = token_count;
+  a.mask = mask;
+  a.mask_stride = mask_stride;
+  a.scale = scale;
+  a.B = B;
+  a.T = T;
+  a.heads = heads;
+  a.group = heads / cache->kv_heads;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  return DSPARK_OK;
+}
+
+void fill_items(TreeArgs& a, const ItemLayout& L, char* ws) {
+  a.join = reinterpret_cast<TreeJoin*>(ws);
+  a.part = reinterpret_cast<float*>(ws + L.part);
+  a.items = reinterpret_cast<TreeItem*>(ws + L.items);
+  a.item_work = reinterpret_cast<long long*>(ws + L.work);
+}
+
+void plan(TreeArgs& a, int tokens) {
+  if (tree_tc_supported(a)) tree_tc_plan(a, tokens, sm_count());
+  else tree_ffma_plan(a, tokens, sm_count());
+}
+
+cudaError_t launch_items(const TreeArgs& a, cudaStream_t stream) {
+  return tree_tc_supported(a) ? launch_items_tc(a, stream) : launch_items_ffma(a, stream);
 }
 
 }  // namespace
@@ -114,6 +232,82 @@ dspark_status dspark_select_pages(const dspark_cache* cache, int layer, const in
   a.reach_q = reinterpret_cast<float*>(ws + L.reach_q);
   a.reach_k = reinterpret_cast<float*>(ws + L.reach_k);
   return from_cuda(launch_select_pages(a, sm_count(), stream));
+}
+
+size_t dspark_sparse_workspace_bytes(const dspark_cache* cache, int B, int T, int heads, int count) {
+  if (check_cache(cache) != DSPARK_OK || count <= 0 || (long long)count * T > (1 << 24) ||
+      attention_sizes(B, T, heads, cache->kv_heads, cache->head_dim) != DSPARK_OK)
+    return 0;
+  return sparse_layout(*cache, B, T, heads, count).total;
+}
+
+dspark_status dspark_sparse_attention(const dspark_cache* cache, int layer, const int32_t* seq,
+                                      const int32_t* length, const int32_t* token_count, const void* q,
+                                      const int32_t* pages, int count, int shared, const uint64_t* mask,
+                                      int64_t mask_stride, float scale, int B, int T, int heads,
+                                      void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream) {
+  SparseArgs p{};
+  const dspark_status st = fill_attention(p.a, cache, layer, seq, length, token_count, q, mask,
+                                          mask_stride, scale, B, T, heads, out, lse);
+  if (st != DSPARK_OK) return st;
+  if (!pages || !is4(pages) || count <= 0) return DSPARK_ERR_INVALID_ARG;
+  if ((long long)count * T > (1 << 24)) return DSPARK_ERR_UNSUPPORTED;
+  const SparseLayout L = sparse_layout(*cache, B, T, heads, count);
+  if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
+    return DSPARK_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  fill_items(p.a, L.items, ws);
+  p.a.item_count = B * cache->kv_heads;
+  p.a.page_list = reinterpret_cast<int32_t*>(ws + L.list);
+  p.a.page_bits = reinterpret_cast<uint64_t*>(ws + L.bits);
+  p.pages = pages;
+  p.count = count;
+  p.lists = shared ? 1 : T;
+  p.room = L.room;
+  plan(p.a, T);
+  cudaError_t e = launch_sparse_items(p, stream);
+  if (e == cudaSuccess) e = launch_items(p.a, stream);
+  if (e == cudaSuccess) e = launch_tree_merge(p.a, stream);
+  return from_cuda(e);
+}
+
+size_t dspark_prefix_workspace_bytes(int B, int T, int heads, int kv_heads, int head_dim) {
+  if (attention_sizes(B, T, heads, kv_heads, head_dim) != DSPARK_OK) return 0;
+  return prefix_layout(B, T, heads, kv_heads, head_dim).total;
+}
+
+dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, const int32_t* seq,
+                                      const int32_t* length, const int32_t* token_count, const void* q,
+                                      const int32_t* group_start, const int32_t* prefix, int groups,
+                                      const uint64_t* mask, int64_t mask_stride, float scale, int B,
+                                      int T, int heads, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+  PrefixArgs p{};
+  const dspark_status st = fill_attention(p.a, cache, layer, seq, length, token_count, q, mask,
+                                          mask_stride, scale, B, T, heads, out, lse);
+  if (st != DSPARK_OK) return st;
+  if (!group_start || !prefix || !is4(group_start) || !is4(prefix) || groups <= 0 || groups > B)
+    return DSPARK_ERR_INVALID_ARG;
+  if ((long long)B * T * heads >= (1LL << 31)) return DSPARK_ERR_UNSUPPORTED;
+  const PrefixLayout L = prefix_layout(B, T, heads, cache->kv_heads, cache->head_dim);
+  if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
+    return DSPARK_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  fill_items(p.a, L.items, ws);
+  p.a.item_count = groups + B;
+  p.a.item_base = reinterpret_cast<long long*>(ws + L.base);
+  p.a.page_list = cache->block_table;
+  p.a.whole = reinterpret_cast<float*>(ws + L.whole);
+  p.group_start = group_start;
+  p.prefix = prefix;
+  p.groups = groups;
+  p.group_of = reinterpret_cast<int32_t*>(ws + L.group_of);
+  plan(p.a, B * T);
+  cudaError_t e = launch_prefix_items(p, stream);
+  if (e == cudaSuccess) e = launch_items(p.a, stream);
+  if (e == cudaSuccess) e = launch_prefix_join(p, stream);
+  return from_cuda(e);
 }
 
 }  // extern "C"

@@ -29,6 +29,27 @@ struct TreeJoin {
   int first, last, slot, unused;
 };
 
+// What part of the cache a unit's rows attend to where that is not a sequence's
+// whole one: an item, made by a kernel before the attention.  Its keys are those
+// of a list of pages, in the list's order; of them the first `hide` are not seen
+// (kind kTreeOwn) or ruled page by page (TreeArgs::page_bits), the others to `len`
+// are seen, and behind these lie `cnt` drafted ones, ruled by the mask.
+struct TreeItem {
+  long long list;  // its first page in TreeArgs::page_list
+  int lo;          // first tile
+  int hide;        // see above
+  int len, cnt;
+  int tokens;      // of rows: the first is token 0 of sequence b
+  int tiles, row_tiles;
+  int b;
+  int h;           // its key head; -1: all
+  int kind;
+};
+static_assert(sizeof(TreeItem) == 48, "three 16-byte loads");
+constexpr int kTreeSparse = 0;  // selected pages: results like those of a sequence
+constexpr int kTreeShared = 1;  // a prefix that sequences share, and
+constexpr int kTreeOwn = 2;     // what a sequence has behind it: partial results
+
 struct TreeArgs {
   dspark_cache c;
   int layer;
@@ -47,10 +68,21 @@ struct TreeArgs {
   int row_tokens;  // drafted tokens of a row tile
   int row_tiles;   // of T tokens
   int slot_rows;   // rows of a partial result
+  int most;        // drafted tokens of a sequence or item, at most
   struct TreeJoin* join;  // [G] what block c of the merge has to do
   // [2 G][slot_rows][D] sums, then [2 G][slot_rows][2]: maxima (in units of
   // log2) and sums of weights
   float* part;
+  // items (the kernels' other form)
+  const TreeItem* items;
+  const long long* item_work;  // tiles of each
+  int item_count;
+  const int32_t* page_list;
+  const uint64_t* page_bits;   // beside page_list: bit t: token t sees the page
+  long long* item_base;        // out, or null: [item_count + 1] the line's tile where an item starts
+  // kinds kTreeShared and kTreeOwn: results of units that one block has whole,
+  // by row [B][T][heads] and kind: sums [2][rows][D], maxima and sums [2][rows][2]
+  float* whole;
 };
 
 constexpr int kTreeMaxBlocks = 160;   // blocks of a call (the GPU has 152 SMs)
@@ -62,6 +94,16 @@ __host__ __device__ __forceinline__ float* tree_part(const TreeArgs& a, int slot
 __host__ __device__ __forceinline__ float* tree_part_stats(const TreeArgs& a, int slot) {
   return a.part + (size_t)2 * a.blocks * a.slot_rows * a.c.head_dim +
          (size_t)slot * a.slot_rows * 2;
+}
+
+__device__ __forceinline__ size_t tree_rows(const TreeArgs& a) {
+  return (size_t)a.B * a.T * a.heads;
+}
+__device__ __forceinline__ float* tree_whole(const TreeArgs& a, int kind, size_t row) {
+  return a.whole + ((kind - 1) * tree_rows(a) + row) * a.c.head_dim;
+}
+__device__ __forceinline__ float* tree_whole_stats(const TreeArgs& a, int kind, size_t row) {
+  return a.whole + 2 * tree_rows(a) * a.c.head_dim + ((kind - 1) * tree_rows(a) + row) * 2;
 }
 
 // One sequence of a call.
@@ -117,6 +159,47 @@ __device__ __forceinline__ long long tree_work(const TreeArgs& a, const TreeSeq&
   return (long long)(r.row_tiles * a.c.kv_heads) * r.tiles;
 }
 
+// Where a walk's units come from: the sequences of a call, or items.
+template <bool kItems>
+struct TreeSource {
+  using Raw = TreeRaw;
+  using Seq = TreeSeq;
+  static __device__ __forceinline__ int count(const TreeArgs& a) { return a.B; }
+  static __device__ __forceinline__ Raw load(const TreeArgs& a, int b) { return tree_load(a, b); }
+  static __device__ __forceinline__ Seq make(const TreeArgs& a, const Raw& r) { return tree_seq(a, r, false); }
+  static __device__ __forceinline__ long long work(const TreeArgs& a, int b) {
+    return tree_work(a, tree_seq(a, tree_load(a, b), blockIdx.x == 0));
+  }
+  static __device__ __forceinline__ int work(const TreeArgs& a, const Seq& q) {
+    return q.row_tiles * a.c.kv_heads * q.tiles;
+  }
+  static __device__ __forceinline__ int head(const Seq&) { return 0; }
+  static __device__ __forceinline__ int tokens(const Seq& q) { return q.cnt; }
+  static __device__ __forceinline__ int row(const Seq&, int b) { return b; }
+};
+template <>
+struct TreeSource<true> {
+  using Raw = TreeItem;
+  using Seq = TreeItem;
+  static __device__ __forceinline__ int count(const TreeArgs& a) { return a.item_count; }
+  static __device__ __forceinline__ Raw load(const TreeArgs& a, int b) {
+    Raw r;
+    const int4* p = reinterpret_cast<const int4*>(a.items + b);
+    reinterpret_cast<int4*>(&r)[0] = p[0];
+    reinterpret_cast<int4*>(&r)[1] = p[1];
+    reinterpret_cast<int4*>(&r)[2] = p[2];
+    return r;
+  }
+  static __device__ __forceinline__ Seq make(const TreeArgs&, const Raw& r) { return r; }
+  static __device__ __forceinline__ long long work(const TreeArgs& a, int b) { return a.item_work[b]; }
+  static __device__ __forceinline__ int work(const TreeArgs& a, const Seq& q) {
+    return q.row_tiles * q.tiles * (q.h < 0 ? a.c.kv_heads : 1);
+  }
+  static __device__ __forceinline__ int head(const Seq& q) { return q.h < 0 ? 0 : q.h; }
+  static __device__ __forceinline__ int tokens(const Seq& q) { return q.tokens; }
+  static __device__ __forceinline__ int row(const Seq& q, int) { return q.b; }
+};
+
 // The line's tiles are counted in 32 bits (more than 2^31 of them, some ten
 // seconds of work, are refused): code comes from memory while a block waits
 // for it, and a 64-bit division is a hundred instructions.
@@ -128,13 +211,15 @@ __device__ __forceinline__ int tree_first(int W, int G, int c) {
 }
 
 // A block's walk over its share, one unit at a time.
+template <bool kItems>
 struct TreeWalk {
+  using Source = TreeSource<kItems>;
   int pos, end;        // tiles of the line
   int base;            // first tile of sequence b
   int W;               // tiles of the line
   int b;
-  TreeSeq q;
-  TreeRaw ahead;       // of sequence b + 1
+  typename Source::Seq q;
+  typename Source::Raw ahead;       // of sequence b + 1
   // the current unit
   int h, rt;           // key head and row tile
   int first, n;        // its tiles here: first .. first + n - 1, counted from
@@ -143,13 +228,13 @@ struct TreeWalk {
 
   __device__ __forceinline__ bool next(const TreeArgs& a) {
     if (pos >= end) return false;
-    int work = q.row_tiles * a.c.kv_heads * q.tiles;
+    int work = Source::work(a, q);
     while (pos >= base + work) {
       base += work;
-      if (++b >= a.B) return false;
-      q = tree_seq(a, ahead, false);
-      if (b + 1 < a.B) ahead = tree_load(a, b + 1);
-      work = q.row_tiles * a.c.kv_heads * q.tiles;
+      if (++b >= Source::count(a)) return false;
+      q = Source::make(a, ahead);
+      if (b + 1 < Source::count(a)) ahead = Source::load(a, b + 1);
+      work = Source::work(a, q);
     }
     const uint32_t at = (uint32_t)(pos - base);
     const int unit = (int)(at / (uint32_t)q.tiles);
@@ -160,6 +245,7 @@ struct TreeWalk {
       h = (int)((uint32_t)unit / (uint32_t)q.row_tiles);
       rt = unit - h * q.row_tiles;
     }
+    h += Source::head(q);
     const int left = end - pos;
     n = q.tiles - first;
     if (n > left) n = left;
@@ -170,23 +256,26 @@ struct TreeWalk {
 };
 
 // What the threads of a block tell each other when they find its share.
+template <bool kItems>
 struct TreeShare {
-  long long sums[32];
-  TreeWalk walk;
+  long long sums[16];  // of the block's warps
+  TreeWalk<kItems> walk;
 };
 
 // Every thread of the block calls this (blockDim.x a multiple of 32): sums the
 // work of the sequences and finds where this block's share starts.  Leaves the
 // walk in sh, on its first unit (n = 0: there is none), which one thread finds
 // for all.  The block is synchronised twice.
-__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare& sh) {
-  const int n = blockDim.x, t = threadIdx.x;
-  const int per = a.B <= n ? 1 : (int)((uint32_t)(a.B + n - 1) / (uint32_t)n);
-  const int b0 = t * per, b1 = b0 + per < a.B ? b0 + per : a.B;
+template <bool kItems>
+__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>& sh) {
+  using Source = TreeSource<kItems>;
+  const int n = blockDim.x, t = threadIdx.x, B = Source::count(a);
+  const int per = B <= n ? 1 : (int)((uint32_t)(B + n - 1) / (uint32_t)n);
+  const int b0 = t * per, b1 = b0 + per < B ? b0 + per : B;
   long long work = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b)
-    work += tree_work(a, tree_seq(a, tree_load(a, b), blockIdx.x == 0));
+    work += Source::work(a, b);
   const int lane = t & 31, warp = t >> 5;
   long long x = work;
 #pragma unroll
@@ -203,7 +292,16 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare& sh) {
     if (i < warp) before += v;
     all += v;
   }
-  TreeWalk w{};
+  if (kItems && a.item_base && blockIdx.x == 0) {
+    long long at = before;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      a.item_base[b] = at;
+      at += Source::work(a, b);
+    }
+    if (t == 0) a.item_base[B] = all;
+  }
+  TreeWalk<kItems> w{};
   if (all > 0x7fffffffLL) {
     if (blockIdx.x == 0 && t == 0) cache_error(a.c, kCacheErrPage);
     all = 0;
@@ -217,8 +315,8 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare& sh) {
     if (w.pos >= before && w.pos < before + work) {  // one thread
       w.base = (int)before;
       w.b = b0;
-      w.q = tree_seq(a, tree_load(a, b0), false);
-      if (b0 + 1 < a.B) w.ahead = tree_load(a, b0 + 1);
+      w.q = Source::make(a, Source::load(a, b0));
+      if (b0 + 1 < B) w.ahead = Source::load(a, b0 + 1);
       w.next(a);
       sh.walk = w;
     }
@@ -232,17 +330,20 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare& sh) {
 // of the merge has to do.  The share's start cuts a unit when the first unit
 // does not begin there; the unit is this block's to join when the share before
 // it holds the unit's beginning.
-__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk& w) {
+template <bool kItems>
+__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk<kItems>& w) {
+  using Source = TreeSource<kItems>;
   TreeJoin j{};
   const int c = blockIdx.x;
   if (w.n > 0 && w.first > 0) {
     const int G = w.W < a.blocks ? w.W : a.blocks;
     const int us = w.pos - w.n - w.first, before = tree_first(w.W, G, c - 1);
     if (before <= us) {
-      j.b = w.b;
+      j.b = Source::row(w.q, w.b);
       j.h = w.h;
       j.t0 = w.rt * a.row_tokens;
-      const int tokens = w.q.cnt - j.t0 < a.row_tokens ? w.q.cnt - j.t0 : a.row_tokens;
+      const int left = Source::tokens(w.q) - j.t0;
+      const int tokens = left < a.row_tokens ? left : a.row_tokens;
       j.rows = tokens * a.group;
       j.first = c - 1;
       j.slot = 2 * (c - 1) + (before == us ? 0 : 1);
@@ -276,9 +377,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Whether the tensor-core kernel takes a cache.
 bool tree_tc_supported(const TreeArgs& a);
-cudaError_t launch_tree_tc(TreeArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_tree_ffma(TreeArgs& a, int sms, cudaStream_t stream);
+// How the work is cut up, for units of up to `tokens` tokens.
+void tree_tc_plan(TreeArgs& a, int tokens, int sms);
+void tree_ffma_plan(TreeArgs& a, int tokens, int sms);
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_ffma(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_items_tc(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_items_ffma(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream);
 
 }  // namespace dspark

@@ -432,7 +432,8 @@ DSPARK_API dspark_status dspark_sample_temperature(
  * be used; 6: a seq outside [0, max_seqs); 7: a length or page outside what the
  * sequence holds; 8: no free page left, or more pages than a table row has;
  * 9: an accepted path or length that is not one; 10: a position outside the
- * rotation table; 11: a fork whose child is a parent, or twice a child).
+ * rotation table; 11: a fork whose child is a parent, or twice a child; 12: a
+ * group of sequences that is none, or whose prefix one of them does not have).
  * Calls on one cache must follow one another (one stream, or ordered by the
  * caller); calls on different caches are independent. */
 typedef struct {
@@ -688,6 +689,69 @@ DSPARK_API dspark_status dspark_select_pages(
     int heads, int32_t* pages, void* workspace, size_t workspace_bytes,
     cudaStream_t stream);
 
+/* Device workspace of dspark_sparse_attention (0 if unsupported). */
+DSPARK_API size_t dspark_sparse_workspace_bytes(const dspark_cache* cache, int B,
+                                                int T, int heads, int count);
+
+/*
+ * dspark_sparse_attention -- attention of T drafted tokens of each of B
+ * sequences over part of the cache of `layer`: the full pages that a list
+ * names, the committed tokens behind the last full page, and the drafted tokens
+ * that the mask allows.
+ *
+ *   pages        [B,T,kv_heads,count] int32, or [B,1,kv_heads,count] with
+ *                `shared`: for each key head the pages of a token (or of all
+ *                tokens), by their numbers within the sequence, as
+ *                dspark_select_pages writes them.  Any order; entries below 0 are
+ *                passed over, and a page named twice counts once.  An entry at
+ *                or behind the sequence's full pages is passed over too (error
+ *                7).  Lists of tokens behind the last one are not read.
+ * All else is as for dspark_tree_attention: q, mask, token_count, scale, out, lse,
+ * what a token sees that sees nothing, the workspace, the roundings, the shapes
+ * that run on the tensor cores, and the errors.  Keys and values that a token
+ * does not see never reach its result, those of pages that only other tokens'
+ * lists name among them.  count * T <= 2^24.  Three launches, graph capturable, no
+ * synchronisation.
+ */
+DSPARK_API dspark_status dspark_sparse_attention(
+    const dspark_cache* cache, int layer, const int32_t* seq,
+    const int32_t* length, const int32_t* token_count, const void* q,
+    const int32_t* pages, int count, int shared, const uint64_t* mask,
+    int64_t mask_stride, float scale, int B, int T, int heads, void* out,
+    float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Device workspace of dspark_prefix_attention (0 if unsupported). */
+DSPARK_API size_t dspark_prefix_workspace_bytes(int B, int T, int heads,
+                                                int kv_heads, int head_dim);
+
+/*
+ * dspark_prefix_attention -- dspark_tree_attention without a window for
+ * sequences that share prefixes: the shared keys and values are read once for
+ * all the sequences of a group, not once for each.
+ *
+ *   group_start  [groups + 1] int32: group g is rows group_start[g] ..
+ *                group_start[g + 1] - 1 of the call, not decreasing; rows in no
+ *                group are attended by themselves.  1 <= groups <= B.
+ *   prefix       [groups] int32: committed tokens that the group's sequences
+ *                share.  They are read through the pages of the group's first
+ *                row, which the other rows need not hold themselves; their
+ *                table entries there are not looked at.
+ * A row whose sequence has fewer committed tokens than its group's prefix is
+ * attended by itself, as all rows are where group_start is no such list, and a
+ * group's where its first row does not hold the prefix (error 12).  Results do
+ * not depend on it where the pages hold the same tokens, but for the order of the
+ * sums.  All else is as for dspark_tree_attention; partial results of both kinds
+ * are float32.  B * T * heads < 2^31.  Three launches, graph capturable, no
+ * synchronisation.
+ */
+DSPARK_API dspark_status dspark_prefix_attention(
+    const dspark_cache* cache, int layer, const int32_t* seq,
+    const int32_t* length, const int32_t* token_count, const void* q,
+    const int32_t* group_start, const int32_t* prefix, int groups,
+    const uint64_t* mask, int64_t mask_stride, float scale, int B, int T,
+    int heads, void* out, float* lse, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
 /*
  * dspark_noise_words -- diagnostic: writes the n raw Philox words the
  * sampler uses for elements 0..n-1 of (seed, offset, position k, stream),
@@ -721,7 +785,7 @@ DSPARK_API dspark_status dspark_noise_words_folded(uint64_t seed, uint64_t offse
  * DSPARK_ERR_DEVICE (and *code != 0) if one did.  Every draft-block and
  * sampler call clears the word when it starts, so the code describes the
  * last call only; the calls on a cache never clear its word (control), which
- * this call reads likewise: their codes 2 and 6 to 11 are described there.
+ * this call reads likewise: their codes 2 and 6 to 12 are described there.
  * Codes: 1 a d0 outside [0, V) (token 0 used), 2 a bounded
  * wait inside a kernel ran out, 3 a per-request temperature that is not
  * finite and positive (1 used), 4 a proposal slot outside [0, num_slots),

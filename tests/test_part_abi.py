@@ -27,16 +27,40 @@ def select(lib, c=None, **over):
         a["shared"], a["B"], a["T"], a["heads"], a["pages"], a["ws"], a["bytes"], None)
 
 
+def attention(lib, fn, c=None, **over):
+    """dspark_sparse_attention or dspark_prefix_attention."""
+    c = c or ctypes.byref(struct())
+    B, T, heads = over.get("B", 2), over.get("T", 4), over.get("heads", 4)
+    b, t = max(1, min(B, 1024)), max(1, min(T, 64))
+    if fn == "sparse":
+        nbytes = lib.dspark_sparse_workspace_bytes(ctypes.byref(struct()), b, t, 4, 5)
+    else:
+        nbytes = lib.dspark_prefix_workspace_bytes(b, t, 4, 2, 64)
+    a = dict(layer=0, seq=None, length=FAKE, count=None, q=FAKE, pages=FAKE, width=5, shared=0, start=FAKE, prefix=FAKE,
+             groups=1, mask=None, stride=0, scale=0.1, out=FAKE + (1 << 30), lse=None, ws=FAKE, bytes=nbytes)
+    a.update(over)
+    special = ((a["pages"], a["width"], a["shared"]) if fn == "sparse" else (a["start"], a["prefix"], a["groups"]))
+    return getattr(lib, f"dspark_{fn}_attention")(
+        c, a["layer"], a["seq"], a["length"], a["count"], a["q"], *special, a["mask"], a["stride"], a["scale"],
+        B, T, heads, a["out"], a["lse"], a["ws"], a["bytes"], None)
+
+
+BOTH = ("sparse", "prefix")
+
+
 @pytest.mark.parametrize("over,want", BAD_CACHES)
 def test_every_call_checks_the_cache(lib, over, want):
     c = ctypes.byref(struct(**over))
     assert bounds(lib, c=c) == want and select(lib, c=c) == want
+    assert all(attention(lib, fn, c=c) == want for fn in BOTH)
     assert lib.dspark_select_workspace_bytes(c, 2, 4, 0) == 0
+    assert lib.dspark_sparse_workspace_bytes(c, 2, 4, 4, 5) == 0
 
 
 @pytest.mark.parametrize("B,want", [(0, INVALID), (-3, INVALID), (1025, UNSUPPORTED)])
 def test_batch_limits(lib, B, want):
     assert bounds(lib, B=B) == want and select(lib, B=B) == want
+    assert all(attention(lib, fn, B=B) == want for fn in BOTH)
     assert lib.dspark_select_workspace_bytes(ctypes.byref(struct()), B, 4, 0) == 0
 
 
@@ -68,6 +92,49 @@ def test_select_workspace_bytes(lib):
     assert f(ctypes.byref(struct(kv_heads=1024, max_seqs=1, max_pages=1 << 27, page_size=1)), 1024, 1, 0) == 0
 
 
+@pytest.mark.parametrize("fn", BOTH)
+@pytest.mark.parametrize("over,want", [
+    (dict(length=None), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(layer=2), INVALID),
+    (dict(layer=-1), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(T=0), INVALID), (dict(heads=5), INVALID), (dict(heads=0), INVALID), (dict(mask=FAKE + 4), INVALID),
+    (dict(mask=FAKE, stride=3), INVALID), (dict(mask=FAKE, stride=-1), INVALID), (dict(q=FAKE + 8), INVALID),
+    (dict(out=FAKE + 8), INVALID), (dict(out=FAKE), INVALID), (dict(out=FAKE + 16), INVALID), (dict(lse=FAKE + 1), INVALID),
+    (dict(seq=FAKE + 2), INVALID), (dict(count=FAKE + 2), INVALID), (dict(T=65), UNSUPPORTED),
+    (dict(heads=66), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 64), WORKSPACE),
+    (dict(bytes=1000), WORKSPACE),
+])
+def test_attentions_refuse(lib, fn, over, want):
+    assert attention(lib, fn, **over) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(pages=None), INVALID), (dict(pages=FAKE + 2), INVALID), (dict(width=0), INVALID), (dict(width=-1), INVALID),
+    (dict(width=1 << 23), UNSUPPORTED), (dict(width=500), WORKSPACE)])
+def test_sparse_refuses(lib, over, want):
+    assert attention(lib, "sparse", **over) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(start=None), INVALID), (dict(prefix=None), INVALID), (dict(start=FAKE + 2), INVALID),
+    (dict(prefix=FAKE + 1), INVALID), (dict(groups=0), INVALID), (dict(groups=-1), INVALID), (dict(groups=3), INVALID)])
+def test_prefix_refuses(lib, over, want):
+    assert attention(lib, "prefix", **over) == want
+
+
+def test_attention_workspace_bytes(lib):
+    c = ctypes.byref(struct(max_pages=4096, page_size=16))
+    f = lib.dspark_sparse_workspace_bytes
+    assert f(c, 2, 4, 4, 100) > f(c, 2, 4, 4, 10) > 0 and f(c, 2, 4, 4, 100) >= f(c, 1, 4, 4, 100)
+    assert f(c, 2, 4, 4, 5000) == f(c, 2, 4, 4, 6000)  # a list names no page twice
+    for bad in [(0, 4, 4, 5), (2, 0, 4, 5), (2, 65, 4, 5), (2, 4, 5, 5), (2, 4, 66, 5), (2, 4, 4, 0), (1025, 4, 4, 5)]:
+        assert f(c, *bad) == 0, bad
+    f = lib.dspark_prefix_workspace_bytes
+    assert f(88, 8, 32, 8, 128) > f(8, 4, 32, 8, 128) > 0 and f(88, 8, 32, 8, 128) % 256 == 0
+    for bad in [(0, 8, 32, 8, 128), (8, 0, 32, 8, 128), (8, 65, 32, 8, 128), (8, 8, 33, 8, 128), (8, 8, 66, 2, 128),
+                (8, 8, 32, 8, 260), (8, 8, 32, 8, 100), (2000, 8, 32, 8, 128), (8, 8, 32, 0, 128)]:
+        assert f(*bad) == 0, bad
+
+
 def test_python_refuses_tensors_that_do_not_fit(lib):
     c = host_cache()
     i32 = torch.int32
@@ -86,3 +153,17 @@ def test_python_refuses_tensors_that_do_not_fit(lib):
         a = dict(bounds=b, q=q, length=one, pages=torch.zeros(1, 3, 2, 4, dtype=i32)) | bad
         with pytest.raises((TypeError, ValueError)):
             dspark.select_pages(c, 0, a.pop("bounds"), a.pop("q"), a.pop("length"), 4, **a)
+    pages, start = torch.zeros(1, 3, 2, 5, dtype=i32), torch.zeros(2, dtype=i32)
+    for bad in (dict(q=q.double()), dict(q=q[0]), dict(mask=torch.zeros(3)), dict(lse=torch.zeros(1, 3)),
+                dict(mask=torch.zeros(2, 3, dtype=torch.int64)), dict(out=q[:, :2]), dict(length=one.long()),
+                dict(q=q.transpose(2, 3).contiguous().transpose(2, 3)), dict(token_count=start)):
+        for fn, more in ((dspark.sparse_attention, (pages,)), (dspark.prefix_attention, (start, one))):
+            a = dict(q=q, length=one) | bad
+            with pytest.raises((TypeError, ValueError)):
+                fn(c, 0, a.pop("q"), a.pop("length"), *more, **a)
+    for bad in (pages[0], pages.long(), pages[:, :2], pages[:, :, :1], pages.transpose(1, 2)):
+        with pytest.raises((TypeError, ValueError)):
+            dspark.sparse_attention(c, 0, q, one, bad)
+    for bad in ((start.long(), one), (start[:1], one), (start, one.long()), (start, start), (start[None], one)):
+        with pytest.raises((TypeError, ValueError)):
+            dspark.prefix_attention(c, 0, q, one, *bad)
