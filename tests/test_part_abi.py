@@ -109,7 +109,7 @@ def test_attentions_refuse(lib, fn, over, want):
 
 @pytest.mark.parametrize("over,want", [
     (dict(pages=None), INVALID), (dict(pages=FAKE + 2), INVALID), (dict(width=0), INVALID), (dict(width=-1), INVALID),
-    (dict(width=1 << 23), UNSUPPORTED), (dict(width=500), WORKSPACE)])
+    (dict(width=1 << 23), UNSUPPORTED)])
 def test_sparse_refuses(lib, over, want):
     assert attention(lib, "sparse", **over) == want
 
