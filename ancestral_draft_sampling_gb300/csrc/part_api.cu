@@ -16,27 +16,25 @@ size_t align_up(size_t x, size_t n) { return (x + n - 1) / n * n; }
 // The workspace of the selection: the scores of every list, the exact ones of
 // many pages near the border, and what bounds the scores' errors.
 struct SelectLayout {
-  int stride, chunks;
+  int stride, reaches;
   size_t border, reach_q, reach_k, total;
 };
 
-SelectLayout select_layout(const dspark_cache& c, int B, int lists) {
+SelectLayout select_layout(const dspark_cache& c, int B, int T, int lists) {
   SelectLayout L;
   L.stride = (c.max_pages + 3) / 4 * 4;
-  L.chunks = (c.max_pages + kScoreChunk - 1) / kScoreChunk;
+  L.reaches = (c.max_pages + 15) / 16 * 16 / kReachPages;  // of whole warps' 16 pages
   const size_t rows = (size_t)B * lists * c.kv_heads;
   L.border = align_up(rows * L.stride * sizeof(float), 256);
-  L.reach_q = align_up(L.border + rows * L.stride * sizeof(double), 256);
-  L.reach_k = align_up(L.reach_q + rows * sizeof(float), 256);
-  L.total = align_up(L.reach_k + (size_t)B * c.kv_heads * L.chunks * sizeof(float), 256);
+  L.reach_q = align_up(L.border + rows * L.stride * sizeof(uint64_t), 256);
+  L.reach_k = align_up(L.reach_q + (size_t)B * T * c.kv_heads * sizeof(float), 256);
+  L.total = align_up(L.reach_k + (size_t)B * c.kv_heads * L.reaches * sizeof(float), 256);
   return L;
 }
 
-dspark_status select_sizes(const dspark_cache* c, int B, int T) {
+dspark_status select_sizes(int B, int T) {
   if (B <= 0 || T <= 0) return DSPARK_ERR_INVALID_ARG;
-  if (B > DSPARK_CACHE_MAX_B || T > DSPARK_TREE_MAX_TOKENS ||
-      (long long)B * c->kv_heads * ((c->max_pages + kScoreChunk - 1) / kScoreChunk) >= (1LL << 31))
-    return DSPARK_ERR_UNSUPPORTED;
+  if (B > DSPARK_CACHE_MAX_B || T > DSPARK_TREE_MAX_TOKENS) return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
 }
 
@@ -180,8 +178,8 @@ dspark_status dspark_cache_bounds(const dspark_cache* cache, const int32_t* seq,
 }
 
 size_t dspark_select_workspace_bytes(const dspark_cache* cache, int B, int T, int shared) {
-  if (check_cache(cache) != DSPARK_OK || select_sizes(cache, B, T) != DSPARK_OK) return 0;
-  return select_layout(*cache, B, shared ? 1 : T).total;
+  if (check_cache(cache) != DSPARK_OK || select_sizes(B, T) != DSPARK_OK) return 0;
+  return select_layout(*cache, B, T, shared ? 1 : T).total;
 }
 
 dspark_status dspark_select_pages(const dspark_cache* cache, int layer, const int32_t* seq,
@@ -200,11 +198,11 @@ dspark_status dspark_select_pages(const dspark_cache* cache, int layer, const in
   const void* p4[] = {seq, length, token_count, pages};
   for (const void* p : p4)
     if (!is4(p)) return DSPARK_ERR_INVALID_ARG;
-  st = select_sizes(cache, B, T);
+  st = select_sizes(B, T);
   if (st == DSPARK_OK && heads / cache->kv_heads > DSPARK_TREE_MAX_GROUP) st = DSPARK_ERR_UNSUPPORTED;
   if (st != DSPARK_OK) return st;
   const int lists = shared ? 1 : T;
-  const SelectLayout L = select_layout(*cache, B, lists);
+  const SelectLayout L = select_layout(*cache, B, T, lists);
   if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
     return DSPARK_ERR_WORKSPACE;
   SelectArgs a{};
@@ -225,10 +223,10 @@ dspark_status dspark_select_pages(const dspark_cache* cache, int layer, const in
   a.group = heads / cache->kv_heads;
   a.pages = pages;
   a.stride = L.stride;
-  a.chunks = L.chunks;
+  a.reaches = L.reaches;
   char* ws = static_cast<char*>(workspace);
   a.scores = reinterpret_cast<float*>(ws);
-  a.border = reinterpret_cast<double*>(ws + L.border);
+  a.border = reinterpret_cast<uint64_t*>(ws + L.border);
   a.reach_q = reinterpret_cast<float*>(ws + L.reach_q);
   a.reach_k = reinterpret_cast<float*>(ws + L.reach_k);
   return from_cuda(launch_select_pages(a, sm_count(), stream));

@@ -24,6 +24,7 @@
 // and the bounds are bfloat16 numbers: nothing is rounded but the sums.)  Tiles in
 // shared memory and tcgen05 would buy nothing: a page's 512 bytes a head are used by
 // at most a few hundred rows.
+#include <climits>
 #include <cmath>
 
 #include "dspark_common.cuh"
@@ -32,8 +33,6 @@
 
 namespace dspark {
 namespace {
-
-constexpr int kMaxB = DSPARK_CACHE_MAX_B;
 
 // One sequence: its table row and its full pages; F < 0: there is an error.
 struct Seq {
@@ -62,37 +61,9 @@ __device__ __forceinline__ size_t list_row(const SelectArgs& a, int b, int t, in
 }
 
 // ------------------------------------------------------------------ scores
+// A block takes a sequence's key head and a stretch of its pages, one after the
+// other if the table is long; a warp scores 16 pages (8 on the FFMA units) at a time.
 constexpr int kScoreThreads = 128, kScoreWarps = kScoreThreads / 32;
-
-// The chunks of all sequences and key heads, in the order b, head, chunk.
-struct Line {
-  int offset[kMaxB + 1];
-  int warps[33];
-};
-struct Chunk {
-  int b, h, i;  // sequence, key head, chunk of its pages
-  Seq q;
-};
-
-__device__ __forceinline__ int line_start(const SelectArgs& a, Line& sh) {
-  for (int b = threadIdx.x; b < a.B; b += kScoreThreads) {
-    const Seq q = find_seq(a, b, blockIdx.x == 0);
-    sh.offset[b] = q.F > 0 && q.tokens > 0
-                       ? (q.F + kScoreChunk - 1) / kScoreChunk * a.c.kv_heads : 0;
-  }
-  __syncthreads();
-  row_offsets(sh.offset, sh.offset, a.B, sh.warps);
-  return sh.offset[a.B];
-}
-__device__ __forceinline__ Chunk line_at(const SelectArgs& a, const Line& sh, int unit) {
-  Chunk c;
-  c.b = row_of(sh.offset, a.B, unit);
-  c.q = find_seq(a, c.b, false);
-  const int n = (c.q.F + kScoreChunk - 1) / kScoreChunk, at = unit - sh.offset[c.b];
-  c.h = at / n;
-  c.i = at - c.h * n;
-  return c;
-}
 
 // A score as it is kept: what is not a number counts as the highest.
 __device__ __forceinline__ float kept(float s) { return s == s ? s : INFINITY; }
@@ -113,162 +84,6 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return d;
 }
 
-// c += a b: a 16 rows of 16, b 16 x 8, bfloat16, sums in float32.
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// NT: tiles of 8 query rows that are worked on together.
-template <int NT>
-__global__ void __launch_bounds__(kScoreThreads)
-    score_mma_kernel(const __grid_constant__ SelectArgs a) {
-  constexpr int kRows = 8 * NT, kPitch = kRows + 1;
-  __shared__ Line sh;
-  __shared__ float slab[kScoreWarps][16 * kPitch];
-  follow();
-  const int units = line_start(a, sh);
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  float* const mine = slab[threadIdx.x >> 5];
-  const int D = a.c.head_dim, fit = kRows / a.group;  // tokens of a row tile
-  const bool together = a.lists == 1;
-#pragma unroll 1
-  for (int unit = blockIdx.x * kScoreWarps + (threadIdx.x >> 5); unit < units;
-       unit += gridDim.x * kScoreWarps) {
-    const Chunk u = line_at(a, sh, unit);
-    const int page0 = u.i * kScoreChunk, pages = u.q.F - page0 < kScoreChunk ? u.q.F - page0 : kScoreChunk;
-    // the pages: two a lane
-    int ids[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = lane + 32 * i;
-      ids[i] = j < pages ? cache_page(a.c, u.q.s, page0 + j, a.c.max_pages) : -1;
-      if (j < pages && ids[i] < 0) cache_error(a.c, kCacheErrPage);
-    }
-    auto query = [&](int t0, int tokens, int n) {  // row n of a tile, this lane's part
-      const int r = 8 * n + gid;
-      if (r >= tokens * a.group) return (const uint4*)nullptr;
-      const size_t row = ((size_t)u.b * a.T + t0) * a.heads + (size_t)u.h * a.group;
-      const int t = r / a.group;
-      return reinterpret_cast<const uint4*>(a.q + (row + (size_t)t * a.heads + (r - t * a.group)) * D * 2) + tig;
-    };
-    uint32_t top = 0;  // the largest |bound|
-    if (u.i == 0) {    // the sums of |q|: products with ones
-      float most = 0.0f;
-#pragma unroll 1
-      for (int t0 = 0; t0 < u.q.tokens; t0 += fit) {
-        const int tokens = u.q.tokens - t0 < fit ? u.q.tokens - t0 : fit;
-#pragma unroll 1
-        for (int n = 0; n < NT; ++n) {
-          const uint4* q = query(t0, tokens, n);
-          float c[4] = {0, 0, 0, 0};
-          const uint32_t one = 0x3f803f80u;
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (q) x = q[4 * k];
-            mma16816(c, one, one, one, one, x.x & 0x7fff7fffu, x.y & 0x7fff7fffu);
-            mma16816(c, one, one, one, one, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu);
-          }
-          if (gid == 0) {
-            mine[8 * n + 2 * tig] = c[0];
-            mine[8 * n + 2 * tig + 1] = c[1];
-          }
-        }
-        __syncwarp();
-        for (int t = lane; t < tokens; t += 32) {
-          float best = 0.0f;
-          for (int g = 0; g < a.group; ++g) best = max_nan(best, mine[t * a.group + g]);
-          if (together) most = max_nan(most, best);
-          else a.reach_q[list_row(a, u.b, t0 + t, u.h)] = best;
-        }
-        __syncwarp();
-      }
-      if (together) {
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, x));
-        if (lane == 0) a.reach_q[list_row(a, u.b, 0, u.h)] = most;
-      }
-    }
-#pragma unroll 1
-    for (int sub = 0; sub < pages; sub += 16) {
-      const int word = sub >= 32 ? ids[1] : ids[0];
-      const int id0 = __shfl_sync(0xffffffffu, word, (sub + gid) & 31);
-      const int id1 = __shfl_sync(0xffffffffu, word, (sub + gid + 8) & 31);
-      const int out_id = __shfl_sync(0xffffffffu, word, (sub + (lane & 15)) & 31);
-      const uint4* k0 = id0 < 0 ? nullptr
-          : reinterpret_cast<const uint4*>(a.bounds + bounds_row(a.c, a.layer, id0, u.h)) + tig;
-      const uint4* k1 = id1 < 0 ? nullptr
-          : reinterpret_cast<const uint4*>(a.bounds + bounds_row(a.c, a.layer, id1, u.h)) + tig;
-      float run = -INFINITY;
-#pragma unroll 1
-      for (int t0 = 0; t0 < u.q.tokens; t0 += fit) {
-        const int tokens = u.q.tokens - t0 < fit ? u.q.tokens - t0 : fit;
-        const uint4* q[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) q[n] = query(t0, tokens, n);
-        float c[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < D / 32; ++k) {
-          const uint4 none = make_uint4(0, 0, 0, 0);
-          const uint4 l0 = k0 ? k0[4 * k] : none, l1 = k1 ? k1[4 * k] : none;
-          const uint4 h0 = k0 ? k0[D / 8 + 4 * k] : none, h1 = k1 ? k1[D / 8 + 4 * k] : none;
-          if (t0 == 0) {
-            const uint32_t m = 0x7fff7fffu;
-            const uint32_t w[16] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w,
-                                    h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = max_nan2(top, w[i] & m);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 x = q[n] ? q[n][4 * k] : none;
-            mma16816(c[n], l0.x, l1.x, l0.y, l1.y, min_nan2(x.x, 0), min_nan2(x.y, 0));
-            mma16816(c[n], l0.z, l1.z, l0.w, l1.w, min_nan2(x.z, 0), min_nan2(x.w, 0));
-            mma16816(c[n], h0.x, h1.x, h0.y, h1.y, max_nan2(x.x, 0), max_nan2(x.y, 0));
-            mma16816(c[n], h0.z, h1.z, h0.w, h1.w, max_nan2(x.z, 0), max_nan2(x.w, 0));
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mine[(gid + (i >> 1) * 8) * kPitch + 8 * n + 2 * tig + (i & 1)] = c[n][i];
-        __syncwarp();
-        // the largest of a token's heads: a page a lane, every other token
-        const int j = lane & 15;
-        for (int t = lane >> 4; t < tokens; t += 2) {
-          float best = -INFINITY;
-          for (int g = 0; g < a.group; ++g) best = fmaxf(best, kept(mine[j * kPitch + t * a.group + g]));
-          if (out_id < 0) best = -INFINITY;
-          if (together) run = fmaxf(run, best);
-          else if (sub + j < pages)
-            a.scores[list_row(a, u.b, t0 + t, u.h) * a.stride + page0 + sub + j] = best;
-        }
-        __syncwarp();
-      }
-      if (together) {
-        run = fmaxf(run, __shfl_xor_sync(0xffffffffu, run, 16));
-        if (lane < 16 && sub + lane < pages)
-          a.scores[list_row(a, u.b, 0, u.h) * a.stride + page0 + sub + lane] = run;
-      }
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = max_nan2(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0)
-      a.reach_k[((size_t)u.b * a.c.kv_heads + u.h) * a.chunks + u.i] =
-          max_nan(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
-  }
-}
-
-// The same on the FFMA units: a page a lane, the queries read alike by all lanes,
-// eight rows at a time.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
 template <>
@@ -282,111 +97,233 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
                      __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
+// The sums of |q|: tokens blockIdx.x, + gridDim.x .. of the block's key head, a
+// warp for each.
+template <typename T>
+__device__ __forceinline__ void sum_queries(const SelectArgs& a, int b, int h, int tokens) {
+  const int lane = threadIdx.x & 31, D = a.c.head_dim;
+#pragma unroll 1
+  for (int t = blockIdx.x + gridDim.x * (threadIdx.x >> 5); t < tokens; t += gridDim.x * kScoreWarps) {
+    const size_t token = (size_t)b * a.T + t;
+    const T* q = reinterpret_cast<const T*>(a.q) + (token * a.heads + (size_t)h * a.group) * D;
+    float best = 0.0f;
+#pragma unroll 4
+    for (int g = 0; g < a.group; ++g) {
+      float x = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int d = 4 * lane + 128 * k;
+        if (d < D) {
+          const float4 v = load4<T>(q + (size_t)g * D + d);
+          x += fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w);
+        }
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+      best = max_nan(best, x);
+    }
+    if (lane == 0) a.reach_q[token * a.c.kv_heads + h] = best;
+  }
+}
+
+// c += a b: a 16 rows of 16, b 16 x 8, bfloat16, sums in float32.
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: tiles of 8 query rows that are worked on together; KD: head_dim / 32, or 0:
+// any.
+template <int NT, int KD>
+__global__ void __launch_bounds__(kScoreThreads)
+    score_mma_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kRows = 8 * NT, kPitch = kRows + 1;
+  __shared__ float slab[kScoreWarps][16 * kPitch];
+  follow();
+  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const Seq seq = find_seq(a, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+  if (seq.F <= 0 || seq.tokens == 0) return;
+  float* const mine = slab[warp];
+  const int D = KD ? 32 * KD : a.c.head_dim, fit = kRows / a.group;  // tokens of a row tile
+  const bool together = a.lists == 1;
+  sum_queries<__nv_bfloat16>(a, b, h, seq.tokens);
+#pragma unroll 1
+  for (int page0 = (blockIdx.x * kScoreWarps + warp) * 16; page0 < seq.F; page0 += gridDim.x * kScoreWarps * 16) {
+    const int j = lane & 15, pages = seq.F - page0;
+    const int id = j < pages ? cache_page(a.c, seq.s, page0 + j, a.c.max_pages) : -1;
+    if (j < pages && id < 0) cache_error(a.c, kCacheErrPage);
+    const int id0 = __shfl_sync(0xffffffffu, id, gid), id1 = __shfl_sync(0xffffffffu, id, gid + 8);
+    const uint4* k0 = reinterpret_cast<const uint4*>(a.bounds + bounds_row(a.c, a.layer, id0 < 0 ? 0 : id0, h)) + tig;
+    const uint4* k1 = reinterpret_cast<const uint4*>(a.bounds + bounds_row(a.c, a.layer, id1 < 0 ? 0 : id1, h)) + tig;
+    uint32_t top0 = 0, top1 = 0;  // the largest |bound| of both pages
+    float run = -INFINITY;
+#pragma unroll 1
+    for (int t0 = 0; t0 < seq.tokens; t0 += fit) {
+      const int tokens = seq.tokens - t0 < fit ? seq.tokens - t0 : fit;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      const uint4* q[NT];  // row 8 n + gid of the tile
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int r = 8 * n + gid, t = r / a.group;
+        const size_t row = ((size_t)b * a.T + t0 + t) * a.heads + (size_t)h * a.group + (r - t * a.group);
+        q[n] = t < tokens ? reinterpret_cast<const uint4*>(a.q + row * D * 2) + tig : nullptr;
+      }
+      float c[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < D / 32; ++k) {
+        uint4 l0 = none, l1 = none, h0 = none, h1 = none;
+        if (id0 >= 0) {
+          l0 = k0[4 * k];
+          h0 = k0[D / 8 + 4 * k];
+        }
+        if (id1 >= 0) {
+          l1 = k1[4 * k];
+          h1 = k1[D / 8 + 4 * k];
+        }
+        if (t0 == 0) {
+          const uint32_t m = 0x7fff7fffu;
+          const uint32_t x[8] = {l0.x, l0.y, l0.z, l0.w, h0.x, h0.y, h0.z, h0.w};
+          const uint32_t y[8] = {l1.x, l1.y, l1.z, l1.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            top0 = max_nan2(top0, x[i] & m);
+            top1 = max_nan2(top1, y[i] & m);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 x = q[n] ? q[n][4 * k] : none;
+          mma16816(c[n], l0.x, l1.x, l0.y, l1.y, min_nan2(x.x, 0), min_nan2(x.y, 0));
+          mma16816(c[n], l0.z, l1.z, l0.w, l1.w, min_nan2(x.z, 0), min_nan2(x.w, 0));
+          mma16816(c[n], h0.x, h1.x, h0.y, h1.y, max_nan2(x.x, 0), max_nan2(x.y, 0));
+          mma16816(c[n], h0.z, h1.z, h0.w, h1.w, max_nan2(x.z, 0), max_nan2(x.w, 0));
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mine[(gid + (i >> 1) * 8) * kPitch + 8 * n + 2 * tig + (i & 1)] = c[n][i];
+      __syncwarp();
+      // the largest of a token's heads: a page a lane, every other token
+      for (int t = lane >> 4; t < tokens; t += 2) {
+        float best = -INFINITY;
+        for (int g = 0; g < a.group; ++g) best = fmaxf(best, kept(mine[j * kPitch + t * a.group + g]));
+        if (id < 0) best = -INFINITY;
+        if (together) run = fmaxf(run, best);
+        else if (j < pages) a.scores[list_row(a, b, t0 + t, h) * a.stride + page0 + j] = best;
+      }
+      __syncwarp();
+    }
+    if (together) {
+      run = fmaxf(run, __shfl_xor_sync(0xffffffffu, run, 16));
+      if (lane < 16 && j < pages) a.scores[list_row(a, b, 0, h) * a.stride + page0 + j] = run;
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+      top0 = max_nan2(top0, __shfl_xor_sync(0xffffffffu, top0, x));
+      top1 = max_nan2(top1, __shfl_xor_sync(0xffffffffu, top1, x));
+    }
+    if (lane < 2) {
+      const uint32_t x = lane ? top1 : top0;
+      a.reach_k[((size_t)b * a.c.kv_heads + h) * a.reaches + page0 / kReachPages + lane] =
+          max_nan(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    }
+  }
+}
+
 // s + max(q lo, q hi) for finite numbers; where the bounds or q are not, every
 // page is scored in 64 bits.
 __device__ __forceinline__ float reach(float q, float lo, float hi, float s) {
   return fmaf(q, q < 0.0f ? lo : hi, s);
 }
 
+// The same on the FFMA units: four lanes share a page, and take eight query rows
+// at a time.
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads)
     score_ffma_kernel(const __grid_constant__ SelectArgs a) {
-  constexpr int kTake = 8;
-  __shared__ Line sh;
+  constexpr int kTake = 8, kPages = 8;
+  static_assert(kPages == kReachPages, "a warp's pages");
   follow();
-  const int units = line_start(a, sh);
-  const int lane = threadIdx.x & 31;
-  const int D = a.c.head_dim;
+  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3, D = a.c.head_dim;
+  const Seq seq = find_seq(a, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+  if (seq.F <= 0 || seq.tokens == 0) return;
   const bool together = a.lists == 1;
+  sum_queries<T>(a, b, h, seq.tokens);
+  const int rows = seq.tokens * a.group;
+  const T* q = reinterpret_cast<const T*>(a.q) + ((size_t)b * a.T * a.heads + (size_t)h * a.group) * D;
 #pragma unroll 1
-  for (int unit = blockIdx.x * kScoreWarps + (threadIdx.x >> 5); unit < units;
-       unit += gridDim.x * kScoreWarps) {
-    const Chunk u = line_at(a, sh, unit);
-    const int page0 = u.i * kScoreChunk, pages = u.q.F - page0 < kScoreChunk ? u.q.F - page0 : kScoreChunk;
-    const int rows = u.q.tokens * a.group;
-    const T* q = reinterpret_cast<const T*>(a.q) +
-                 ((size_t)u.b * a.T * a.heads + (size_t)u.h * a.group) * D;
-    if (u.i == 0) {  // the sums of |q|
-      float most = 0.0f;
+  for (int page0 = (blockIdx.x * kScoreWarps + warp) * kPages; page0 < seq.F;
+       page0 += gridDim.x * kScoreWarps * kPages) {
+    const int j = page0 + gid;
+    const int id = j < seq.F ? cache_page(a.c, seq.s, j, a.c.max_pages) : -1;
+    if (j < seq.F && id < 0) cache_error(a.c, kCacheErrPage);
+    const T* lo = reinterpret_cast<const T*>(a.bounds + bounds_row(a.c, a.layer, id < 0 ? 0 : id, h));
+    float top = 0.0f, best = -INFINITY;
+    int g = 0, t = 0;  // of the row that is next
 #pragma unroll 1
-      for (int t = 0; t < u.q.tokens; ++t) {
-        float best = 0.0f;
-#pragma unroll 1
-        for (int g = 0; g < a.group; ++g) {
-          float x = 0.0f;
-          for (int d = 4 * lane; d < D; d += 128) {
-            const float4 v = load4<T>(q + ((size_t)t * a.heads + g) * D + d);
-            x += fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w);
-          }
+    for (int r0 = 0; r0 < rows; r0 += kTake) {
+      float s[kTake];
+      const T* at[kTake];
+      int ta = t, ga = g;
 #pragma unroll
-          for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-          best = max_nan(best, x);
+      for (int i = 0; i < kTake; ++i) {
+        s[i] = 0.0f;
+        at[i] = q + ((size_t)ta * a.heads + ga) * D;
+        if (r0 + i + 1 < rows && ++ga == a.group) {
+          ga = 0;
+          ++ta;
         }
-        most = max_nan(most, best);
-        if (!together && lane == 0) a.reach_q[list_row(a, u.b, t, u.h)] = best;
       }
-      if (together && lane == 0) a.reach_q[list_row(a, u.b, 0, u.h)] = most;
-    }
-    float top = 0.0f;
-#pragma unroll 1
-    for (int sub = 0; sub < pages; sub += 32) {
-      const int j = sub + lane;
-      const int id = j < pages ? cache_page(a.c, u.q.s, page0 + j, a.c.max_pages) : -1;
-      if (j < pages && id < 0) cache_error(a.c, kCacheErrPage);
-      const T* lo = reinterpret_cast<const T*>(a.bounds + bounds_row(a.c, a.layer, id < 0 ? 0 : id, u.h));
-      float best = -INFINITY;
-      int g = 0, t = 0;  // of the row that is next
-#pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += kTake) {
-        float s[kTake];
-        const T* at[kTake];
-        int ta = t, ga = g;
-#pragma unroll
-        for (int i = 0; i < kTake; ++i) {
-          s[i] = 0.0f;
-          at[i] = q + ((size_t)ta * a.heads + ga) * D;
-          if (r0 + i + 1 < rows && ++ga == a.group) {
-            ga = 0;
-            ++ta;
-          }
-        }
-#pragma unroll 2
-        for (int d = 0; d < D; d += 4) {
-          const float4 l = load4<T>(lo + d), h = load4<T>(lo + D + d);
-          if (r0 == 0 && id >= 0) {
-            top = max_nan(top, max_nan(max_nan(fabsf(l.x), fabsf(l.y)), max_nan(fabsf(l.z), fabsf(l.w))));
-            top = max_nan(top, max_nan(max_nan(fabsf(h.x), fabsf(h.y)), max_nan(fabsf(h.z), fabsf(h.w))));
-          }
-#pragma unroll
-          for (int i = 0; i < kTake; ++i) {
-            const float4 x = load4<T>(at[i] + d);
-            s[i] = reach(x.x, l.x, h.x, s[i]);
-            s[i] = reach(x.y, l.y, h.y, s[i]);
-            s[i] = reach(x.z, l.z, h.z, s[i]);
-            s[i] = reach(x.w, l.w, h.w, s[i]);
-          }
+#pragma unroll 4
+      for (int d = 4 * tig; d < D; d += 16) {
+        const float4 l = load4<T>(lo + d), u = load4<T>(lo + D + d);
+        if (r0 == 0 && id >= 0) {
+          top = max_nan(top, max_nan(max_nan(fabsf(l.x), fabsf(l.y)), max_nan(fabsf(l.z), fabsf(l.w))));
+          top = max_nan(top, max_nan(max_nan(fabsf(u.x), fabsf(u.y)), max_nan(fabsf(u.z), fabsf(u.w))));
         }
 #pragma unroll
         for (int i = 0; i < kTake; ++i) {
-          if (r0 + i >= rows) break;
-          best = fmaxf(best, kept(s[i]));
-          if (++g == a.group) {
-            if (!together) {
-              if (j < pages)
-                a.scores[list_row(a, u.b, t, u.h) * a.stride + page0 + j] = id < 0 ? -INFINITY : best;
-              best = -INFINITY;
-            }
-            g = 0;
-            ++t;
-          }
+          const float4 x = load4<T>(at[i] + d);
+          s[i] = reach(x.x, l.x, u.x, s[i]);
+          s[i] = reach(x.y, l.y, u.y, s[i]);
+          s[i] = reach(x.z, l.z, u.z, s[i]);
+          s[i] = reach(x.w, l.w, u.w, s[i]);
         }
       }
-      if (together && j < pages)
-        a.scores[list_row(a, u.b, 0, u.h) * a.stride + page0 + j] = id < 0 ? -INFINITY : best;
+#pragma unroll
+      for (int i = 0; i < kTake; ++i) {
+        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 1);
+        s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);
+      }
+#pragma unroll
+      for (int i = 0; i < kTake; ++i) {
+        if (r0 + i >= rows) break;
+        best = fmaxf(best, kept(s[i]));
+        if (++g == a.group) {
+          if (!together) {
+            if (tig == 0 && j < seq.F) a.scores[list_row(a, b, t, h) * a.stride + j] = id < 0 ? -INFINITY : best;
+            best = -INFINITY;
+          }
+          g = 0;
+          ++t;
+        }
+      }
     }
+    if (together && tig == 0 && j < seq.F)
+      a.scores[list_row(a, b, 0, h) * a.stride + j] = id < 0 ? -INFINITY : best;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0) a.reach_k[((size_t)u.b * a.c.kv_heads + u.h) * a.chunks + u.i] = top;
+    if (lane == 0) a.reach_k[((size_t)b * a.c.kv_heads + h) * a.reaches + page0 / kPages] = top;
   }
 }
 
@@ -405,7 +342,7 @@ struct Team {
   struct Shared {
     uint32_t part[2][W];
     int n, near[kNear];
-    double exact[kNear];
+    uint64_t exact[kNear];
   };
   Shared& sh;
   int thread, turn = 0;
@@ -436,40 +373,73 @@ struct Team {
   }
 };
 
-// max(q lo, q hi), exact; not a number if one of them is none.
+// q times the bound that makes the larger product, exact.
 __device__ __forceinline__ double larger(float q, float lo, float hi) {
-  const double x = (double)q * lo, y = (double)q * hi;
-  return x >= y ? x : y >= x ? y : nan("");
+  return (double)q * (q < 0.0f ? lo : hi);
+}
+// The same as whole multiples of 1 / scale (a power of two): the products of
+// bfloat16 numbers are exact in float32, and those of float32 numbers with the
+// remainder, which a fused product gives.
+template <typename T>
+__device__ __forceinline__ long long larger_fixed(float q, float lo, float hi, float scale) {
+  const float x = q < 0.0f ? lo : hi, p = q * x;
+  long long n = __float2ll_rn(p * scale);
+  if (sizeof(T) == 4) n += __float2ll_rn(fmaf(q, x, -p) * scale);
+  return n;
 }
 
-// The score of one page in 64 bits, by a whole warp.
+// The score of one page in 64 bits, by a whole warp: as a whole number of 1 / scale,
+// whose sums are exact, or where scale is 0 (infinities, extreme sizes) in double.
+// The 64-bit floating-point units have a thirty-second of the integer units' rate
+// and bounded the selection: 5632 lists of 250 pages 67 -> 20 us.
 template <typename T>
-__device__ __noinline__ double exact_score(const SelectArgs& a, int b, int t0, int tokens, int h,
-                                           int page, int lane) {
-  if (page < 0) return -INFINITY;
+__device__ __noinline__ uint64_t exact_score(const SelectArgs& a, int b, int t0, int tokens, int h,
+                                             int page, float scale, int lane) {
   const int D = a.c.head_dim;
-  const T* lo = reinterpret_cast<const T*>(a.bounds + bounds_row(a.c, a.layer, page, h));
+  const T* lo = reinterpret_cast<const T*>(a.bounds + bounds_row(a.c, a.layer, page < 0 ? 0 : page, h));
+  long long most = LLONG_MIN;
   double best = -INFINITY;
 #pragma unroll 1
   for (int t = t0; t < t0 + tokens; ++t) {
     const T* q = reinterpret_cast<const T*>(a.q) +
                  (((size_t)b * a.T + t) * a.heads + (size_t)h * a.group) * D;
-#pragma unroll 2
-    for (int g = 0; g < a.group; ++g) {
-      double s = 0.0;
-      for (int d = 4 * lane; d < D; d += 128) {
-        const float4 x = load4<T>(q + (size_t)g * D + d), l = load4<T>(lo + d), u = load4<T>(lo + D + d);
-        s += larger(x.x, l.x, u.x);
-        s += larger(x.y, l.y, u.y);
-        s += larger(x.z, l.z, u.z);
-        s += larger(x.w, l.w, u.w);
-      }
+    if (scale > 0.0f) {
+#pragma unroll 4
+      for (int g = 0; g < a.group; ++g) {
+        long long s = 0;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      best = s == s ? fmax(best, s) : INFINITY;
+        for (int k = 0; k < 2; ++k) {
+          const int d = 4 * lane + 128 * k;
+          if (d < D) {
+            const float4 x = load4<T>(q + (size_t)g * D + d), l = load4<T>(lo + d), u = load4<T>(lo + D + d);
+            s += larger_fixed<T>(x.x, l.x, u.x, scale) + larger_fixed<T>(x.y, l.y, u.y, scale) +
+                 larger_fixed<T>(x.z, l.z, u.z, scale) + larger_fixed<T>(x.w, l.w, u.w, scale);
+          }
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+        most = s > most ? s : most;
+      }
+    } else {
+#pragma unroll 1
+      for (int g = 0; g < a.group; ++g) {
+        double s = 0.0;
+        for (int d = 4 * lane; d < D; d += 128) {
+          const float4 x = load4<T>(q + (size_t)g * D + d), l = load4<T>(lo + d), u = load4<T>(lo + D + d);
+          s += larger(x.x, l.x, u.x);
+          s += larger(x.y, l.y, u.y);
+          s += larger(x.z, l.z, u.z);
+          s += larger(x.w, l.w, u.w);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        best = s == s ? fmax(best, s) : INFINITY;
+      }
     }
   }
-  return best;
+  // as bits whose order is that of the scores
+  if (page < 0) return 0;
+  return scale > 0.0f ? (uint64_t)most ^ (1ull << 63) : ordered_bits64(best);
 }
 
 // W warps a list, R scores a thread in registers (the rest is read from memory
@@ -553,17 +523,27 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
     in = team.least(in);
     out_key = split ? team.most(out_key) : in;
     const float kth = from_ordered_bits(in), next = from_ordered_bits(out_key);
-    float reach_k = 0.0f;
-    const float* of = a.reach_k + ((size_t)b * a.c.kv_heads + h) * a.chunks;
-    for (int i = lane; i * kScoreChunk < q.F; i += 32) reach_k = max_nan(reach_k, of[i]);
+    float reach_k = 0.0f, reach_q = 0.0f;
+    const float* of = a.reach_k + ((size_t)b * a.c.kv_heads + h) * a.reaches;
+    for (int i = lane; i * kReachPages < q.F; i += 32) reach_k = max_nan(reach_k, of[i]);
+    const int first_token = a.lists > 1 ? t : 0, tokens = a.lists > 1 ? 1 : q.tokens;
+    for (int i = lane; i < tokens; i += 32)
+      reach_q = max_nan(reach_q, a.reach_q[((size_t)b * a.T + first_token + i) * a.c.kv_heads + h]);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) reach_k = max_nan(reach_k, __shfl_xor_sync(0xffffffffu, reach_k, x));
-    const float eps = (float)a.c.head_dim * 0x1p-22f * a.reach_q[row] * reach_k;
+    for (int x = 16; x > 0; x >>= 1) {
+      reach_k = max_nan(reach_k, __shfl_xor_sync(0xffffffffu, reach_k, x));
+      reach_q = max_nan(reach_q, __shfl_xor_sync(0xffffffffu, reach_q, x));
+    }
+    const float size = reach_q * reach_k;  // no sum of a score's terms is larger
+    const float eps = (float)a.c.head_dim * 0x1p-22f * size;
     edge = kth;
     open = false;
     if (!(kth - next > 2.0f * eps)) {
       // scores within 2 eps of the last one that is taken could change places
-      const bool known = eps <= 1e37f && fabsf(kth) <= 1e38f;
+      const bool known = size <= 0x1p100f && fabsf(kth) <= 0x1p101f;
+      // sums below 2^62; a product that float32 cannot hold whole is far below 1
+      const float scale = size == 0.0f ? 1.0f
+                          : known && size >= 0x1p-60f ? __int_as_float((127 + 60 - ilogbf(size)) << 23) : 0.0f;
       const float sure = known ? kth + 2.0f * eps : INFINITY;
       near = known ? kth - 2.0f * eps : -INFINITY;
       uint32_t n = 0, m = 0;
@@ -574,9 +554,8 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
       const int need = want - (int)team.sum(n);
       listed = (int)team.sum(m);
       many = listed > kNear;
-      const int first_token = a.lists > 1 ? t : 0, tokens = a.lists > 1 ? 1 : q.tokens;
       auto exact = [&](int j) {
-        return exact_score<T>(a, b, first_token, tokens, h, cache_page(a.c, q.s, j, a.c.max_pages), lane);
+        return exact_score<T>(a, b, first_token, tokens, h, cache_page(a.c, q.s, j, a.c.max_pages), scale, lane);
       };
       edge = sure;
       open = true;
@@ -593,18 +572,18 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
         team.sync();
 #pragma unroll 1
         for (int e = tid >> 5; e < listed; e += W) {
-          const double x = exact(team.sh.near[e]);
+          const uint64_t x = exact(team.sh.near[e]);
           if (lane == 0) team.sh.exact[e] = x;
         }
         team.sync();
         // rank by score, then by place; those that stay out are marked
         bool stays = true;
         if (tid < listed) {
-          const double x = team.sh.exact[tid];
+          const uint64_t x = team.sh.exact[tid];
           const int j = team.sh.near[tid];
           int rank = 0;
           for (int e = 0; e < listed; ++e) {
-            const double y = team.sh.exact[e];
+            const uint64_t y = team.sh.exact[e];
             rank += y > x || (y == x && team.sh.near[e] < j);
           }
           stays = rank < need;
@@ -613,14 +592,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
         if (tid < listed && !stays) team.sh.near[tid] = -1;
         team.sync();
       } else {
-        double* border = a.border + (size_t)row * a.stride;
+        uint64_t* border = a.border + (size_t)row * a.stride;
         all([&](int j, float s) {
           uint32_t here = __ballot_sync(0xffffffffu, j >= 0 && s >= near && s <= sure);
           while (here) {
             const int l = __ffs(here) - 1;
             here &= here - 1;
             const int page = __shfl_sync(0xffffffffu, j, l);
-            const double x = exact(page);
+            const uint64_t x = exact(page);
             if (lane == l) border[page] = x;
           }
         });
@@ -631,7 +610,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
           const uint64_t mid = low + (high - low) / 2;
           uint32_t n2 = 0;
           all([&](int j, float s) {
-            n2 += j >= 0 && s >= near && s <= sure && ordered_bits64(border[j]) >= mid;
+            n2 += j >= 0 && s >= near && s <= sure && border[j] >= mid;
           });
           n2 = team.sum(n2);
           if (n2 >= (uint32_t)need) low = mid;
@@ -640,14 +619,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
         cut = low;
         uint32_t n2 = 0;
         all([&](int j, float s) {
-          n2 += j >= 0 && s >= near && s <= sure && ordered_bits64(border[j]) > cut;
+          n2 += j >= 0 && s >= near && s <= sure && border[j] > cut;
         });
         ties = need - (int)team.sum(n2);
       }
     }
   }
   // the taken pages in order
-  const double* border = a.border + (size_t)row * a.stride;
+  const uint64_t* border = a.border + (size_t)row * a.stride;
   int done = 0, tied = 0;
   auto write = [&](int j, float s) {
     bool take = j < lo || (j >= hi && j < q.F), tie = false;
@@ -655,7 +634,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_pages_kernel(const __grid_c
       take = open ? s > edge : s >= edge;
       if (!take && listed > 0 && s >= near) {
         if (many) {
-          const uint64_t k = ordered_bits64(border[j]);
+          const uint64_t k = border[j];
           take = k > cut;
           tie = k == cut;
         } else {
@@ -710,21 +689,33 @@ cudaError_t launch_pick(const SelectArgs& a, cudaStream_t stream) {
   return launch_behind(pick_pages_kernel<T, 8, 8>, rows, kPickThreads, 0, stream, a);
 }
 
+// Blocks for the stretches of a table: as many as it can have, unless the batch alone
+// fills the GPU many times over; the blocks of short sequences end at once.
+template <typename... P>
+cudaError_t launch_score(void (*kernel)(P...), const SelectArgs& a, int pages, int sms, cudaStream_t stream) {
+  const int stretches = (a.c.max_pages + pages * kScoreWarps - 1) / (pages * kScoreWarps);
+  const int heads = a.B * a.c.kv_heads, most = (32 * sms + heads - 1) / heads;
+  return launch_behind(kernel, dim3(stretches < most ? stretches : most, a.c.kv_heads, a.B), kScoreThreads, 0,
+                       stream, a);
+}
+
+template <int KD>
+cudaError_t launch_mma(const SelectArgs& a, int sms, cudaStream_t stream) {
+  const int rows = a.T * a.group;
+  return launch_score(rows <= 8 ? score_mma_kernel<1, KD> : rows <= 16 ? score_mma_kernel<2, KD> : score_mma_kernel<4, KD>,
+                      a, 16, sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_select_pages(const SelectArgs& a, int sms, cudaStream_t stream) {
-  const int blocks = 4 * sms;
   cudaError_t e;
-  if (a.c.dtype == DSPARK_BF16 && a.c.head_dim % 32 == 0) {
-    const int rows = a.T * a.group;
-    const auto kernel = rows <= 8 ? score_mma_kernel<1>
-                        : rows <= 16 ? score_mma_kernel<2>
-                                     : score_mma_kernel<4>;
-    e = launch_behind(kernel, blocks, kScoreThreads, 0, stream, a);
-  } else {
-    const auto kernel = a.c.dtype == DSPARK_F32 ? score_ffma_kernel<float> : score_ffma_kernel<__nv_bfloat16>;
-    e = launch_behind(kernel, blocks, kScoreThreads, 0, stream, a);
-  }
+  if (a.c.dtype == DSPARK_BF16 && a.c.head_dim % 32 == 0)
+    e = a.c.head_dim == 128 ? launch_mma<4>(a, sms, stream)
+        : a.c.head_dim == 64 ? launch_mma<2>(a, sms, stream) : launch_mma<0>(a, sms, stream);
+  else
+    e = launch_score(a.c.dtype == DSPARK_F32 ? score_ffma_kernel<float> : score_ffma_kernel<__nv_bfloat16>, a,
+                     kReachPages, sms, stream);
   if (e != cudaSuccess) return e;
   return a.c.dtype == DSPARK_F32 ? launch_pick<float>(a, stream) : launch_pick<__nv_bfloat16>(a, stream);
 }

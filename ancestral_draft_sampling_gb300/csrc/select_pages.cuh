@@ -5,7 +5,7 @@
 
 namespace dspark {
 
-constexpr int kScoreChunk = 64;  // pages that a warp scores for a key head
+constexpr int kReachPages = 8;  // pages that SelectArgs::reach_k goes by
 
 struct SelectArgs {
   dspark_cache c;
@@ -19,10 +19,10 @@ struct SelectArgs {
   // workspace: [B][lists][kv_heads] rows
   int stride;      // pages of a row
   float* scores;   // [rows][stride]
-  double* border;  // [rows][stride], the exact scores of many pages near the border
-  float* reach_q;  // [rows] the largest sum of |q|
-  float* reach_k;  // [B][kv_heads][chunks] the largest |bound| of a chunk
-  int chunks;
+  uint64_t* border;  // [rows][stride], the exact scores of many pages near the border
+  float* reach_q;  // [B][T][kv_heads] the largest sum of |q| of a token's heads
+  float* reach_k;  // [B][kv_heads][reaches] the largest |bound| of kReachPages pages
+  int reaches;
 };
 
 cudaError_t launch_select_pages(const SelectArgs& a, int sms, cudaStream_t stream);

@@ -674,8 +674,9 @@ DSPARK_API size_t dspark_select_workspace_bytes(const dspark_cache* cache, int B
  * the tokens with `shared`), of sum_d max(q_d min_d, q_d max_d): no product of
  * q with a key of the page exceeds it.  (For attention with scale > 0.)  The
  * choice is that of exact scores: where float32 leaves it open, pages are
- * scored in 64 bits, whose sums are off by 2^-53 of their terms.  Equal scores
- * go to the lower page; a score that is not a number counts as infinite.
+ * scored in 64 bits (off by 2^-51 of the largest that sums of their terms can
+ * be).  Equal scores go to the lower page; a score that is not a number counts as
+ * infinite.
  * 1 <= T <= 64, group <= 32.  A sequence whose length is out of range is left out
  * (error 6 or 7); a table entry that names no page has the lowest score (error
  * 7).  Two launches, graph capturable; the same result on every run.  The
