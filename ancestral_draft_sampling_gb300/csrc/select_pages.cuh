@@ -23,6 +23,7 @@ struct SelectArgs {
   float* reach_q;  // [B][T][kv_heads] the largest sum of |q| of a token's heads
   float* reach_k;  // [B][kv_heads][reaches] the largest |bound| of kReachPages pages
   int reaches;
+  float error;     // of a score, relative to those two
 };
 
 cudaError_t launch_select_pages(const SelectArgs& a, int sms, cudaStream_t stream);

@@ -100,6 +100,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
+// `bytes` that lie together, global -> shared: both addresses and the size are
+// multiples of 16.
+__device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Tile store shared -> global (rows/columns outside the tensor are not
 // written), tracked as a bulk group of the issuing thread.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map,

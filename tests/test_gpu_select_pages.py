@@ -253,3 +253,21 @@ def test_replays_and_streams(cuda):
         again = dspark.select_pages(s.c, 1, bounds, s.q, length, 11, stream=side)
         side.synchronize()
         assert torch.equal(again, pages)
+
+
+@pytest.mark.parametrize("D,group,T", [(128, 4, 8), (64, 8, 1), (128, 8, 20)])
+def test_a_wait_that_runs_out_is_reported(cuda, monkeypatch, D, group, T):
+    """DSPARK_TEST_STALL_WAIT=1 makes the warp that issues the products wait for a
+    barrier phase that nothing completes, with a short limit: error 2, a clean
+    return, and a cache that the next call can use."""
+    s = Case(BF, D, 2, group, T, [3000, 0, 700], 16, seed=T)
+    bounds, ws = s.bounds(), dspark.SelectWorkspace(s.c, 3, T)
+    want = dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws)
+    s.check(bounds, want, 9)
+    monkeypatch.setenv("DSPARK_TEST_STALL_WAIT", "1")
+    dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws)
+    torch.cuda.synchronize()
+    assert dspark.read_device_error(s.c) == 2 and dspark.read_device_error(s.c) == 0
+    monkeypatch.delenv("DSPARK_TEST_STALL_WAIT")
+    assert torch.equal(dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws), want)
+    assert dspark.read_device_error(s.c) == 0
