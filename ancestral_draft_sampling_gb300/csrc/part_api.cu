@@ -32,9 +32,12 @@ SelectLayout select_layout(const dspark_cache& c, int B, int T, int lists) {
   return L;
 }
 
-dspark_status select_sizes(int B, int T) {
+dspark_status select_sizes(const dspark_cache* c, int B, int T) {
   if (B <= 0 || T <= 0) return DSPARK_ERR_INVALID_ARG;
-  if (B > DSPARK_CACHE_MAX_B || T > DSPARK_TREE_MAX_TOKENS) return DSPARK_ERR_UNSUPPORTED;
+  // stretches of tables are counted in 32 bits
+  if (B > DSPARK_CACHE_MAX_B || T > DSPARK_TREE_MAX_TOKENS ||
+      (long long)B * c->kv_heads * ((c->max_pages + 63) / 64) >= (1LL << 31))
+    return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
 }
 
@@ -83,15 +86,17 @@ SparseLayout sparse_layout(const dspark_cache& c, int B, int T, int heads, int c
 }
 
 struct PrefixLayout {
-  ItemLayout items;
+  ItemLayout shared, own;
   size_t base, group_of, whole, total;
 };
 
 PrefixLayout prefix_layout(int B, int T, int heads, int kv_heads, int D) {
   PrefixLayout L;
-  L.items = item_layout((long long)B * T, (size_t)2 * B, heads / kv_heads, D);
-  L.base = L.items.end;
-  L.group_of = align_up(L.base + ((size_t)2 * B + 1) * sizeof(long long), 256);
+  const int group = heads / kv_heads;
+  L.shared = item_layout((long long)B * T, (size_t)2 * B, group, D);
+  L.own = item_layout(T, B, group, D);  // behind it
+  L.base = L.shared.end + L.own.end;
+  L.group_of = align_up(L.base + ((size_t)2 * B + 2) * sizeof(long long), 256);
   L.whole = align_up(L.group_of + (size_t)B * sizeof(int32_t), 256);
   L.total = align_up(L.whole + (size_t)2 * B * T * heads * (D + 2) * sizeof(float), 256);
   return L;
@@ -178,7 +183,7 @@ dspark_status dspark_cache_bounds(const dspark_cache* cache, const int32_t* seq,
 }
 
 size_t dspark_select_workspace_bytes(const dspark_cache* cache, int B, int T, int shared) {
-  if (check_cache(cache) != DSPARK_OK || select_sizes(B, T) != DSPARK_OK) return 0;
+  if (check_cache(cache) != DSPARK_OK || select_sizes(cache, B, T) != DSPARK_OK) return 0;
   return select_layout(*cache, B, T, shared ? 1 : T).total;
 }
 
@@ -198,7 +203,7 @@ dspark_status dspark_select_pages(const dspark_cache* cache, int layer, const in
   const void* p4[] = {seq, length, token_count, pages};
   for (const void* p : p4)
     if (!is4(p)) return DSPARK_ERR_INVALID_ARG;
-  st = select_sizes(B, T);
+  st = select_sizes(cache, B, T);
   if (st == DSPARK_OK && heads / cache->kv_heads > DSPARK_TREE_MAX_GROUP) st = DSPARK_ERR_UNSUPPORTED;
   if (st != DSPARK_OK) return st;
   const int lists = shared ? 1 : T;
@@ -282,7 +287,8 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
                                       int T, int heads, void* out, float* lse, void* workspace,
                                       size_t workspace_bytes, cudaStream_t stream) {
   PrefixArgs p{};
-  const dspark_status st = fill_attention(p.a, cache, layer, seq, length, token_count, q, mask,
+  TreeArgs& a = p.shared;
+  const dspark_status st = fill_attention(a, cache, layer, seq, length, token_count, q, mask,
                                           mask_stride, scale, B, T, heads, out, lse);
   if (st != DSPARK_OK) return st;
   if (!group_start || !prefix || !is4(group_start) || !is4(prefix) || groups <= 0 || groups > B)
@@ -292,18 +298,31 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
   if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
     return DSPARK_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  fill_items(p.a, L.items, ws);
-  p.a.item_count = groups + B;
-  p.a.item_base = reinterpret_cast<long long*>(ws + L.base);
-  p.a.page_list = cache->block_table;
-  p.a.whole = reinterpret_cast<float*>(ws + L.whole);
+  fill_items(a, L.shared, ws);
+  a.item_base = reinterpret_cast<long long*>(ws + L.base);
+  a.page_list = cache->block_table;
+  a.whole = reinterpret_cast<float*>(ws + L.whole);
   p.group_start = group_start;
   p.prefix = prefix;
   p.groups = groups;
   p.group_of = reinterpret_cast<int32_t*>(ws + L.group_of);
-  plan(p.a, B * T);
+  // A sequence's rows are few, a group's many: where that makes different forms of the
+  // tensor-core kernel, each kind is launched in its own.  One launch of the wide form
+  // for both: 88 single tokens of 8 heads behind a prefix of 4000 keys 119 us, two
+  // launches %%.
+  p.two = tree_tc_supported(a) && tree_tc_narrow(a, T) && !tree_tc_narrow(a, B * T);
+  p.own = a;
+  plan(a, B * T);
+  a.item_count = p.two ? groups : groups + B;
+  if (p.two) {
+    fill_items(p.own, L.own, ws + L.shared.end);
+    p.own.item_base = a.item_base + groups + 1;
+    p.own.item_count = B;
+    plan(p.own, T);
+  }
   cudaError_t e = launch_prefix_items(p, stream);
-  if (e == cudaSuccess) e = launch_items(p.a, stream);
+  if (e == cudaSuccess) e = launch_items(a, stream);
+  if (e == cudaSuccess && p.two) e = launch_items(p.own, stream);
   if (e == cudaSuccess) e = launch_prefix_join(p, stream);
   return from_cuda(e);
 }

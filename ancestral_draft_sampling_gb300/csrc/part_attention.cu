@@ -130,62 +130,60 @@ __global__ void __launch_bounds__(kListThreads) sparse_items_kernel(const __grid
 constexpr int kItemThreads = 1024;
 
 __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid_constant__ PrefixArgs p) {
-  __shared__ int len[kMaxB];     // committed tokens; -1: nothing to do
-  __shared__ int shared[kMaxB];  // of these, those of the group's prefix
-  __shared__ int group[kMaxB];
-  const TreeArgs& a = p.a;
+  __shared__ int start[kMaxB + 1];  // of the groups
+  __shared__ int prefix[kMaxB];     // their shared tokens; 0: each sequence by itself
+  __shared__ int used[kMaxB];       // by a sequence
+  const TreeArgs &a = p.shared, &own = p.two ? p.own : p.shared;
   follow();
   const int tid = threadIdx.x;  // kMaxB sequences at most
   Held q{-1, 0, -1, 0};
-  if (tid < a.B) {
-    q = find_held(a, tid, true);
-    len[tid] = q.cnt > 0 ? q.len : -1;
-    shared[tid] = 0;
-    group[tid] = -1;
-  }
-  int from = 0, to = 0, n = 0;
+  if (tid < a.B) q = find_held(a, tid, true);
   bool fine = true;
   if (tid < p.groups) {
-    from = p.group_start[tid];
-    to = p.group_start[tid + 1];
-    n = p.prefix[tid];
+    const int from = p.group_start[tid], to = p.group_start[tid + 1], n = p.prefix[tid];
     fine = 0 <= from && from <= to && to <= a.B && n >= 0;
+    start[tid] = from;
+    if (tid + 1 == p.groups) start[p.groups] = to;
+    prefix[tid] = to - from > 1 ? n : 0;
+    used[tid] = 0;
   }
   fine = __syncthreads_and(fine);
   if (!fine && tid == 0) cache_error(a.c, kCacheErrGroup);
+  long long list = 0;
+  if (fine && tid < p.groups && prefix[tid] > 0) {
+    const int s = cache_seq(a.c, a.seq, start[tid]), n = prefix[tid];
+    list = (long long)s * a.c.max_pages;
+    if (s < 0 || n > (1 << 30) || n > cache_held(a.c, s) * a.c.page_size) {
+      cache_error(a.c, kCacheErrGroup);
+      prefix[tid] = 0;
+    }
+  }
+  __syncthreads();
+  int g = -1, hide = 0;
+  if (fine && q.cnt > 0 && tid >= start[0] && tid < start[p.groups]) {
+    g = row_of(start, p.groups, tid);
+    hide = prefix[g];
+    if (q.len < hide) {
+      cache_error(a.c, kCacheErrGroup);
+      hide = 0;
+    }
+    if (hide > 0) used[g] = 1;
+  }
+  __syncthreads();
   if (tid < p.groups) {
     TreeItem x{};
-    x.b = from;
+    x.b = start[tid];
     x.h = -1;
     x.kind = kTreeShared;
-    if (fine && to - from > 1 && n > 0) {
-      const int s = cache_seq(a.c, a.seq, from);
-      if (s < 0 || n > (1 << 30) || n > cache_held(a.c, s) * a.c.page_size) {
-        cache_error(a.c, kCacheErrGroup);
-      } else {
-        int users = 0;
-        for (int b = from; b < to; ++b) {
-          if (len[b] < 0) continue;
-          if (len[b] < n) {
-            cache_error(a.c, kCacheErrGroup);
-            continue;
-          }
-          shared[b] = n;
-          group[b] = tid;
-          ++users;
-        }
-        if (users > 0) {
-          x.list = (long long)s * a.c.max_pages;
-          x.len = n;
-          x.tokens = (to - from) * a.T;
-          x.tiles = ((n - 1) >> a.tile_shift) + 1;
-          x.row_tiles = (x.tokens + a.row_tokens - 1) / a.row_tokens;
-        }
-      }
+    if (used[tid]) {
+      x.list = list;
+      x.len = prefix[tid];
+      x.tokens = (start[tid + 1] - start[tid]) * a.T;
+      x.tiles = ((x.len - 1) >> a.tile_shift) + 1;
+      x.row_tiles = (x.tokens + a.row_tokens - 1) / a.row_tokens;
     }
     put_item(a, tid, x);
   }
-  __syncthreads();
   if (tid < a.B) {
     TreeItem x{};
     x.b = tid;
@@ -193,16 +191,16 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
     x.kind = kTreeOwn;
     if (q.cnt > 0) {
       x.list = (long long)q.s * a.c.max_pages;
-      x.hide = shared[tid];
-      x.lo = x.hide >> a.tile_shift;
+      x.hide = hide;
+      x.lo = x.hide >> own.tile_shift;
       x.len = q.len;
       x.cnt = q.cnt;
       x.tokens = q.cnt;
-      x.tiles = ((q.len + q.cnt - 1) >> a.tile_shift) + 1 - x.lo;
-      x.row_tiles = (q.cnt + a.row_tokens - 1) / a.row_tokens;
+      x.tiles = ((q.len + q.cnt - 1) >> own.tile_shift) + 1 - x.lo;
+      x.row_tiles = (q.cnt + own.row_tokens - 1) / own.row_tokens;
     }
-    put_item(a, p.groups + tid, x);
-    p.group_of[tid] = group[tid];
+    put_item(own, p.two ? tid : p.groups + tid, x);
+    p.group_of[tid] = hide > 0 ? g : -1;
   }
 }
 
@@ -220,101 +218,144 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
                                             *reinterpret_cast<const uint32_t*>(&b));
 }
 
-constexpr int kJoinWarps = 4, kBatch = 4;
+// A row's parts: some of what its sequence has of its own, then some of the prefix.
+// A warp takes four rows, with a lane for each row of eight parts' statistics and the
+// loads of two parts of all four in flight (a row a warp, which finds its parts
+// itself, took 24 us for 16384 rows of 128 dims in four parts, this %%).
+constexpr int kJoinWarps = 4, kBatch = 2;
 
 template <typename T, int ND>
 __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs p) {
-  const TreeArgs& a = p.a;
+  const TreeArgs &a = p.shared, &line = p.two ? p.own : p.shared;
   follow();
-  const size_t row = (size_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= tree_rows(a)) return;
-  const int lane = threadIdx.x & 31, D = a.c.head_dim;
-  const uint32_t bt = (uint32_t)(row / (uint32_t)a.heads), head = (uint32_t)(row - (size_t)bt * a.heads);
-  const int b = (int)(bt / (uint32_t)a.T), t = (int)(bt - (uint32_t)b * a.T);
-  const int h = (int)(head / (uint32_t)a.group), gh = (int)head - h * a.group;
+  const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane >> 2;
+  const int h = blockIdx.y, b = blockIdx.z, r0 = (blockIdx.x * kJoinWarps + (threadIdx.x >> 5)) * 4;
   using Source = TreeSource<true>;
-  const TreeItem own = Source::load(a, p.groups + b);
-  const long long all = a.item_base[a.item_count];
-  if (own.tiles == 0 || t >= own.tokens || all > 0x7fffffffLL) return;
-  const int W = (int)all, G = W < a.blocks ? W : a.blocks;
-  auto block_of = [&](int at) { return (int)((((long long)at + 1) * G - 1) / W); };
-  auto parts_of = [&](const TreeItem& x, int item, int token) {
+  const int own_item = p.two ? b : p.groups + b, g = p.group_of[b];
+  const TreeItem own = Source::load(line, own_item);
+  const long long own_all = line.item_base[line.item_count], all = a.item_base[a.item_count];
+  const int own_base = (int)line.item_base[own_item], rows = own.tokens * a.group;
+  if (own.tiles == 0 || r0 >= rows || own_all > 0x7fffffffLL || all > 0x7fffffffLL) return;
+  // this lane's row of the four (the last one again behind it)
+  const int mine = r0 + (lane & 3) < rows ? r0 + (lane & 3) : rows - 1;
+  const int t = (int)((uint32_t)mine / (uint32_t)a.group), gh = mine - t * a.group;
+  const size_t row = ((size_t)b * a.T + t) * a.heads + h * a.group + gh;
+  auto parts_of = [&](const TreeArgs& l, long long tiles, const TreeItem& x, int base, int token) {
     Parts r;
-    const int rt = token / a.row_tokens;
-    const int us = (int)a.item_base[item] + (h * x.row_tiles + rt) * x.tiles;
+    const int W = (int)tiles, G = W < l.blocks ? W : l.blocks;
+    auto block_of = [&](int at) { return (int)((((long long)at + 1) * G - 1) / W); };
+    const int rt = token / l.row_tokens;
+    const int us = base + (h * x.row_tiles + rt) * x.tiles;
     r.first = block_of(us);
     r.n = block_of(us + x.tiles - 1) - r.first + 1;
     r.slot = 2 * r.first + (tree_first(W, G, r.first) == us ? 0 : 1);
-    r.r = (token - rt * a.row_tokens) * a.group + gh;
+    r.r = (token - rt * l.row_tokens) * l.group + gh;
     return r;
   };
-  const Parts mine = parts_of(own, p.groups + b, t);
-  Parts theirs{0, 0, 0, 0};
-  const int g = p.group_of[b];
+  Parts x = parts_of(line, own_all, own, own_base, t), y{0, 0, 0, 0};
   if (g >= 0) {
-    const TreeItem x = Source::load(a, g);
-    theirs = parts_of(x, g, (b - x.b) * a.T + t);
+    const TreeItem shared = Source::load(a, g);
+    y = parts_of(a, all, shared, (int)a.item_base[g], (b - shared.b) * a.T + t);
   }
-  const int parts = mine.n + theirs.n;
-  auto sums = [&](int i) -> const float* {
-    const Parts& k = i < mine.n ? mine : theirs;
-    if (k.n == 1) return tree_whole(a, i < mine.n ? kTreeOwn : kTreeShared, row);
-    const int j = i < mine.n ? i : i - mine.n;
-    return tree_part(a, j == 0 ? k.slot : 2 * (k.first + j)) + (size_t)k.r * D;
+  const int parts = x.n + y.n;  // of this lane's row
+  auto find = [&](int i, float*& stats) {
+    const bool second = i >= x.n;
+    const Parts& k = second ? y : x;
+    const TreeArgs& l = second ? a : line;
+    const int j = second ? i - x.n : i;
+    if (k.n == 1) {
+      const int kind = second ? kTreeShared : kTreeOwn;
+      stats = tree_whole_stats(a, kind, row);
+      return tree_whole(a, kind, row);
+    }
+    const int slot = j == 0 ? k.slot : 2 * (k.first + j);
+    stats = tree_part_stats(l, slot) + 2 * k.r;
+    return tree_part(l, slot) + (size_t)k.r * D;
   };
   auto stats = [&](int i) {
     if (i >= parts) return make_float2(-INFINITY, 0.0f);
-    const Parts& k = i < mine.n ? mine : theirs;
-    const int j = i < mine.n ? i : i - mine.n;
-    const float* at = k.n == 1 ? tree_whole_stats(a, i < mine.n ? kTreeOwn : kTreeShared, row)
-                               : tree_part_stats(a, j == 0 ? k.slot : 2 * (k.first + j)) + 2 * k.r;
+    float* at;
+    find(i, at);
     return *reinterpret_cast<const float2*>(at);
   };
-  float M = -INFINITY, L = 0.0f;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, stats(i).x);
+  int most = parts;  // of the four rows
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  float4 v[kBatch][4][ND];
+  auto load_parts = [&](int i) {
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float4 o[ND];
+    for (int q = 0; q < kBatch; ++q) {
+      float* unused;
+      const unsigned long long at =
+          i + q < parts ? reinterpret_cast<unsigned long long>(find(i + q, unused)) : 0ull;
 #pragma unroll
-  for (int k = 0; k < ND; ++k) o[k] = make_float4(0, 0, 0, 0);
+      for (int n = 0; n < 4; ++n) {
+        const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, at, n));
+#pragma unroll
+        for (int k = 0; k < ND; ++k) {
+          v[q][n][k] = make_float4(0, 0, 0, 0);
+          if (from && k * 128 + lane * 4 < D) v[q][n][k] = load4(from + k * 128 + lane * 4);
+        }
+      }
+    }
+  };
+  float2 st = stats(sub);
+  load_parts(0);  // under way while the weights are made
+  float M = st.x;
 #pragma unroll 1
-  for (int p0 = 0; p0 < parts; p0 += kBatch) {
-    float4 x[kBatch][ND];
-    float2 st[kBatch];
+  for (int i = sub + 8; i < most; i += 8) M = fmaxf(M, stats(i).x);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      st[i] = stats(p0 + i);
-      const float* at = p0 + i < parts ? sums(p0 + i) : nullptr;
+  for (int k = 4; k < 32; k <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+  float L = 0.0f;
+  float4 o[4][ND];
 #pragma unroll
-      for (int k = 0; k < ND; ++k) {
-        const int d = k * 128 + lane * 4;
-        x[i][k] = make_float4(0, 0, 0, 0);
-        if (at && d < D) x[i][k] = load4(at + d);
-      }
-    }
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      // a part that saw nothing weighs nothing
-      const float w = M == -INFINITY ? 0.0f : st[i].x == M ? 1.0f : exp2f(st[i].x - M);
-      L += w * st[i].y;
+    for (int k = 0; k < ND; ++k) o[n][k] = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int p0 = 0; p0 < most; p0 += 8) {
+    const int n_here = most - p0 < 8 ? most - p0 : 8;
+    if (p0 > 0) st = stats(p0 + sub);
+    // a part that saw nothing weighs nothing
+    const float w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f(st.x - M);
+    L += w * st.y;
+#pragma unroll 1
+    for (int i = 0; i < n_here; i += kBatch) {
+      if (p0 + i > 0) load_parts(p0 + i);
 #pragma unroll
-      for (int k = 0; k < ND; ++k) {
-        o[k].x = fmaf(w, x[i][k].x, o[k].x);
-        o[k].y = fmaf(w, x[i][k].y, o[k].y);
-        o[k].z = fmaf(w, x[i][k].z, o[k].z);
-        o[k].w = fmaf(w, x[i][k].w, o[k].w);
+      for (int q = 0; q < kBatch; ++q) {
+        if (i + q >= n_here) break;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float f = __shfl_sync(0xffffffffu, w, (i + q) * 4 + n);
+#pragma unroll
+          for (int k = 0; k < ND; ++k) {
+            o[n][k].x = fmaf(f, v[q][n][k].x, o[n][k].x);
+            o[n][k].y = fmaf(f, v[q][n][k].y, o[n][k].y);
+            o[n][k].z = fmaf(f, v[q][n][k].z, o[n][k].z);
+            o[n][k].w = fmaf(f, v[q][n][k].w, o[n][k].w);
+          }
+        }
       }
     }
   }
+#pragma unroll
+  for (int k = 4; k < 32; k <<= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  if (lane < 4 && r0 + lane < rows && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
 #pragma unroll
-  for (int k = 0; k < ND; ++k) {
-    const int d = k * 128 + lane * 4;
-    if (d < D)
-      put4(static_cast<T*>(a.out) + row * D + d,
-           make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+  for (int n = 0; n < 4; ++n) {
+    const float f = __shfl_sync(0xffffffffu, inv, n);
+    const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)row, n);
+    if (r0 + n >= rows) break;
+#pragma unroll
+    for (int k = 0; k < ND; ++k) {
+      const int d = k * 128 + lane * 4;
+      if (d < D)
+        put4(static_cast<T*>(a.out) + to * D + d,
+             make_float4(o[n][k].x * f, o[n][k].y * f, o[n][k].z * f, o[n][k].w * f));
+    }
   }
-  if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
 }
 
 }  // namespace
@@ -328,10 +369,10 @@ cudaError_t launch_prefix_items(const PrefixArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_prefix_join(const PrefixArgs& a, cudaStream_t stream) {
-  const size_t rows = (size_t)a.a.B * a.a.T * a.a.heads;
-  const unsigned blocks = (unsigned)((rows + kJoinWarps - 1) / kJoinWarps);
-  const bool wide = a.a.c.head_dim > 128;
-  const auto kernel = a.a.c.dtype == DSPARK_F32
+  const TreeArgs& l = a.shared;
+  const dim3 blocks((l.T * l.group + 4 * kJoinWarps - 1) / (4 * kJoinWarps), l.c.kv_heads, l.B);
+  const bool wide = l.c.head_dim > 128;
+  const auto kernel = l.c.dtype == DSPARK_F32
                           ? (wide ? prefix_join_kernel<float, 2> : prefix_join_kernel<float, 1>)
                           : (wide ? prefix_join_kernel<__nv_bfloat16, 2> : prefix_join_kernel<__nv_bfloat16, 1>);
   return launch_behind(kernel, blocks, 32 * kJoinWarps, 0, stream, a);

@@ -16,13 +16,15 @@ struct SparseArgs {
 };
 cudaError_t launch_sparse_items(const SparseArgs& a, cudaStream_t stream);
 
-// Groups of sequences with a shared prefix: an item for each group's prefix,
-// then one for what each sequence has behind it.
+// Groups of sequences with a shared prefix: an item for each group's prefix, and
+// one for what each sequence has behind it.  Both kinds are one line of tiles (two =
+// 0), or two, in launches of their own, where one sequence's rows and a group's want
+// different forms of the kernel.
 struct PrefixArgs {
-  TreeArgs a;                  // a.items, a.item_work and a.item_base are made here
+  TreeArgs shared, own;        // items, item_work and item_base are made here; own: if two
   const int32_t* group_start;  // [groups + 1]
   const int32_t* prefix;       // [groups]
-  int groups;
+  int groups, two;
   int32_t* group_of;           // [B] the item of a sequence's prefix, or -1
 };
 cudaError_t launch_prefix_items(const PrefixArgs& a, cudaStream_t stream);

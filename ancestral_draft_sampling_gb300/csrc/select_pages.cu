@@ -1142,10 +1142,8 @@ cudaError_t launch_score_ffma(const SelectArgs& a, int sms, cudaStream_t stream)
 cudaError_t launch_select_pages(const SelectArgs& args, int sms, cudaStream_t stream) {
   SelectArgs a = args;
   const int D = a.c.head_dim;
-  // the items are counted in 32 bits
-  const long long items = (long long)a.B * a.c.kv_heads * ((a.c.max_pages + kScorePages - 1) / kScorePages);
   const bool bf16 = a.c.dtype == DSPARK_BF16;
-  const bool tc = bf16 && (D == 64 || D == 128) && items < INT_MAX;
+  const bool tc = bf16 && (D == 64 || D == 128);
   a.error = (tc ? 2 * (17 * (D / 8 / kSums) + kSums) : D / 4 + 4) * 0x1p-24f;
   const cudaError_t e = tc      ? (D == 64 ? launch_score_tc<64>(a, sms, stream) : launch_score_tc<128>(a, sms, stream))
                         : bf16 ? launch_score_ffma<__nv_bfloat16>(a, sms, stream)

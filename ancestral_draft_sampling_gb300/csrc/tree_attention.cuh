@@ -379,6 +379,8 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Whether the tensor-core kernel takes a cache.
 bool tree_tc_supported(const TreeArgs& a);
+// Whether its units of up to `tokens` tokens are narrow (tree_attention_tc.cuh).
+bool tree_tc_narrow(const TreeArgs& a, int tokens);
 // How the work is cut up, for units of up to `tokens` tokens.
 void tree_tc_plan(TreeArgs& a, int tokens, int sms);
 void tree_ffma_plan(TreeArgs& a, int tokens, int sms);

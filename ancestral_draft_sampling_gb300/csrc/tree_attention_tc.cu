@@ -10,6 +10,8 @@ bool tree_tc_supported(const TreeArgs& a) {
          (page & (page - 1)) == 0;
 }
 
+bool tree_tc_narrow(const TreeArgs& a, int tokens) { return tokens * a.group <= kNarrowRows; }
+
 void tree_tc_plan(TreeArgs& a, int tokens, int sms) {
   a.most = tokens;
   a.tile_shift = 7;

@@ -87,7 +87,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
+// Narrow units of items have a warp apart for what comes of their sums.
+template <bool kNarrow, bool kItems>
+constexpr int kThreads = kNarrow && kItems ? 416 : 384;
 constexpr int kTile = 128;             // keys of a tile
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 bfloat16
 constexpr int kNarrowRows = 32;        // rows that each warp of a stream has
@@ -126,7 +128,7 @@ template <bool kItems>
 using Unit = typename std::conditional<kItems, ItemUnit, SeqUnit>::type;
 __device__ __forceinline__ int unit_tokens(const SeqUnit& u) { return u.cnt; }
 __device__ __forceinline__ int unit_tokens(const ItemUnit& u) { return u.tokens; }
-constexpr int kUnits = 4, kUnitReaders = 11;  // warps 0, 1, 3 and the softmax
+constexpr int kUnits = 4, kUnitReaders = 11;  // warps 0, 1, 3 and the softmax (and 12)
 
 template <bool kItems>
 struct Control {  // shared memory behind the tiles
@@ -144,6 +146,7 @@ struct Control {  // shared memory behind the tiles
   // sums by hand: a unit's first scores are there before the last unit's sums
   // have been read.
   uint64_t o_free[2];
+  uint64_t e_full[2];  // of each stream, for warp 12: the unit's maxima and sums are there
   uint64_t u_full[kUnits], u_empty[kUnits];
   Unit<kItems> units[kUnits];
   TreeShare<kItems> share;
@@ -170,7 +173,9 @@ struct Narrow {
   float top[2][4][kNarrowRows];              // of each warp: a maximum that raises m,
   float sum[2][4][kNarrowRows];              // and at the end its part of l
   uint32_t raise[2][4];                      // the warp has such maxima
-  uint8_t rest[32768 - 16384 - 2048 - 32];
+  // for warp 12, of two units in turn: m, and the warps' parts of l
+  float end_top[2][2][kNarrowRows], end_sum[2][2][4][kNarrowRows];
+  uint8_t rest[32768 - 16384 - 2048 - 32 - 512 - 2048];
 };
 static_assert(sizeof(Narrow) == 32768, "a multiple of every tile");
 
@@ -650,7 +655,7 @@ __device__ __noinline__ bool fill_ring(const TcArgs& P, Control<kItems>& sh, boo
 }
 
 template <int D, bool kNarrow, bool kItems>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
     tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v) {
@@ -667,14 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the next scores need not wait for the product of the weights
   constexpr bool apart = S::apart || kNarrow;
+  constexpr bool kAside = kNarrow && kItems;
   static_assert(offsetof(Ctl, v_all) == 31 * 8 && offsetof(Ctl, o_free) == 37 * 8, "barriers");
   if (warp == 0) {
     uint64_t* bar = sh.k_full;
     mbar_init(bar + lane, lane < 31 ? 1 : 8);
-    if (lane < 7) mbar_init(bar + 32 + lane, 4);
+    if (lane < 7 + (kAside ? 2 : 0)) mbar_init(bar + 32 + lane, kAside && (lane == 5 || lane == 6) ? 1 : 4);
     if (lane < kUnits) {
       mbar_init(&sh.u_full[lane], 1);
-      mbar_init(&sh.u_empty[lane], kUnitReaders);
+      mbar_init(&sh.u_empty[lane], kUnitReaders + (kAside ? 1 : 0));
     }
     if (lane < 2) sh.add_first[lane] = 0;
     if (lane == 0) sh.failed = 0;
@@ -922,6 +928,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         some = w.next(a);
       }
     }
+  } else if (kAside && warp == 12) {
+    // ------------------------------------------------------------ ends
+    // Joins the two streams' sums of a unit and writes what comes of them, while the
+    // streams are at work on the next one: done by a stream's own warps this kept them
+    // from it for 3000 to 4500 cycles a unit, of 8000 that a unit's end took.
+    int unit = 0;
+    uint32_t used[2] = {0, 0}, stats[2] = {0, 0};  // tiles that a stream has weighed; phases
+    UnitReader units;
+    Unit<kItems> w;
+    const int r_token = (int)((uint32_t)lane / (uint32_t)a.group), r_head = lane - r_token * a.group;
+#pragma unroll 1
+    for (; ok && units.next(sh, w, ok, lane); ++unit) {
+      const int tokens = unit_tokens(w) - w.t0 < P.fit ? unit_tokens(w) - w.t0 : P.fit;
+      const int rows = tokens * a.group, buffer = unit & 1, t = w.t0 + r_token;
+      const bool valid = lane < rows, join = w.n > 1;
+      const size_t out_row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
+      const int slot = 2 * blockIdx.x + (unit == 0 ? 0 : 1);
+      const bool part = !w.whole || a.whole;
+      float *part_sums = nullptr, *part_stats = nullptr;
+      if constexpr (kItems) {
+        if (part) {
+          part_sums = w.whole ? tree_whole(a, w.kind, out_row) : tree_part(a, slot) + (size_t)lane * D;
+          part_stats = w.whole ? tree_whole_stats(a, w.kind, out_row) : tree_part_stats(a, slot) + 2 * lane;
+        }
+      }
+      float m[2], l[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        m[st] = -INFINITY;
+        if (st < w.n) {
+          used[st] += (uint32_t)(w.n + 1 - st) >> 1;
+          ok = ok && wait_warp(&sh.e_full[st], stats[st]++ & 1);
+          if (!ok) break;
+          m[st] = *(volatile float*)&nar.end_top[buffer][st][lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[st] += *(volatile float*)&nar.end_sum[buffer][st][i][lane];
+          ok = wait_warp(&sh.pv_done[st], (used[st] - 1) & 1);
+        }
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const float now = fmaxf(m[0], m[1]);
+      const float fa = m[0] == now ? 1.0f : ex2(m[0] - now), fb = !join ? 0.0f : m[1] == now ? 1.0f : ex2(m[1] - now);
+      const float sum = l[0] * fa + l[1] * fb;
+      const float inv = !part ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(tmem + S::o_col(0) + 32 * i, o);
+        if (join) {
+          uint32_t o2[32];
+          tmem_ld32(tmem + S::o_col(1) + 32 * i, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) * fa + __uint_as_float(o2[k]) * fb);
+        } else {
+          tmem_ld_wait();
+        }
+        if (i + 1 == D / 32) {  // the sums have been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_free[0]);
+        }
+        if (valid && !part) {
+          char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + 32 * i);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t p[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+              p[d] = pack_bf16(__uint_as_float(o[16 * k + 2 * d]) * inv, __uint_as_float(o[16 * k + 2 * d + 1]) * inv);
+            if (P.out32) {
+              store32(to + 32 * k, p);
+            } else {
+              reinterpret_cast<uint4*>(to)[2 * k] = make_uint4(p[0], p[1], p[2], p[3]);
+              reinterpret_cast<uint4*>(to)[2 * k + 1] = make_uint4(p[4], p[5], p[6], p[7]);
+            }
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t p[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) p[d] = o[8 * k + d];
+            store32(part_sums + 32 * i + 8 * k, p);
+          }
+        }
+      }
+      if (valid) {
+        if (part) {
+          part_stats[0] = now;
+          part_stats[1] = sum;
+        } else if (a.lse) {
+          a.lse[out_row] = sum == 0.0f ? -INFINITY : now * kLn2 + logf(sum);
+        }
+      }
+    }
   } else {
     // --------------------------------------------------------- softmax
     const int st = warp >= 8, quarter = warp & 3, r = quarter * 32 + lane;
@@ -1118,8 +1223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             found |= rows_bad[i];
           }
           if (found) {
-            if (st == 1 && tile == first && unit > 0) {
-              // the first stream may still be reading the last unit's sums, its
+            if ((kAside || st == 1) && tile == first && unit > 0) {
+              // the first stream (warp 12) may still be reading the last unit's sums, its
               // join with these; it cannot end this unit before this stream has
               // gone on, so the phase is the last one or this one
               ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
@@ -1197,6 +1302,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       some = units.next(sh, next.w, ok, lane);
       if (!ok) break;
       if (some) look_at(next);
+      if constexpr (kAside) {
+        if (worked) {
+          if (quarter == 0) nar.end_top[unit & 1][st][lane] = m;
+          nar.end_sum[unit & 1][st][quarter][lane] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.e_full[st]);
+        }
+        is_first = false;
+        continue;
+      }
       if (worked) {
         ok = wait_warp(&sh.pv_done[st], (used - 1) & 1);
         if (!ok) break;
@@ -1365,7 +1480,8 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return launch_behind(tree_tc_kernel<D, kNarrow, kItems>, a.blocks, kThreads, smem_bytes<D, kItems>(), stream, P,
+  return launch_behind(tree_tc_kernel<D, kNarrow, kItems>, a.blocks, kThreads<kNarrow, kItems>,
+                       smem_bytes<D, kItems>(), stream, P,
                        mq, mk, mv);
 }
 

@@ -674,7 +674,7 @@ DSPARK_API size_t dspark_select_workspace_bytes(const dspark_cache* cache, int B
  * the tokens with `shared`), of sum_d max(q_d min_d, q_d max_d): no product of
  * q with a key of the page exceeds it.  (For attention with scale > 0.)  The
  * choice is that of exact scores: where float32 leaves it open, pages are
- * scored in 64 bits (off by 2^-51 of the largest that sums of their terms can
+ * scored more exactly (off by 2^-46 of the largest that sums of their terms can
  * be).  Equal scores go to the lower page; a score that is not a number counts as
  * infinite.
  * 1 <= T <= 64, group <= 32.  A sequence whose length is out of range is left out
@@ -742,7 +742,7 @@ DSPARK_API size_t dspark_prefix_workspace_bytes(int B, int T, int heads,
  * group's where its first row does not hold the prefix (error 12).  Results do
  * not depend on it where the pages hold the same tokens, but for the order of the
  * sums.  All else is as for dspark_tree_attention; partial results of both kinds
- * are float32.  B * T * heads < 2^31.  Three launches, graph capturable, no
+ * are float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no
  * synchronisation.
  */
 DSPARK_API dspark_status dspark_prefix_attention(
