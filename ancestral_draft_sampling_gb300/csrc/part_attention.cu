@@ -42,14 +42,16 @@ __device__ __forceinline__ Held find_held(const TreeArgs& a, int b, bool report)
   return r;
 }
 
-__device__ __forceinline__ void put_item(const TreeArgs& a, int i, const TreeItem& x) {
+__device__ __forceinline__ long long put_item(const TreeArgs& a, int i, const TreeItem& x) {
   const int4* from = reinterpret_cast<const int4*>(&x);
   int4* to = reinterpret_cast<int4*>(const_cast<TreeItem*>(a.items) + i);
   to[0] = from[0];
   to[1] = from[1];
   to[2] = from[2];
-  const_cast<long long*>(a.item_work)[i] =
-      (long long)x.tiles * x.row_tiles * (x.h < 0 ? a.c.kv_heads : 1);
+  const long long work =
+      x.tiles == 0 ? 0 : (long long)(x.tiles + a.extra) * x.row_tiles * (x.h < 0 ? a.c.kv_heads : 1);
+  const_cast<long long*>(a.item_work)[i] = work;
+  return work;
 }
 
 // ---------------------------------------------------------- selected pages
@@ -133,9 +135,11 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
   __shared__ int start[kMaxB + 1];  // of the groups
   __shared__ int prefix[kMaxB];     // their shared tokens; 0: each sequence by itself
   __shared__ int used[kMaxB];       // by a sequence
+  __shared__ unsigned long long totals[2];  // places of the lines
   const TreeArgs &a = p.shared, &own = p.two ? p.own : p.shared;
   follow();
   const int tid = threadIdx.x;  // kMaxB sequences at most
+  if (tid < 2) totals[tid] = 0;
   Held q{-1, 0, -1, 0};
   if (tid < a.B) q = find_held(a, tid, true);
   bool fine = true;
@@ -182,7 +186,8 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
       x.tiles = ((x.len - 1) >> a.tile_shift) + 1;
       x.row_tiles = (x.tokens + a.row_tokens - 1) / a.row_tokens;
     }
-    put_item(a, tid, x);
+    const long long work = put_item(a, tid, x);
+    if (work) atomicAdd(&totals[0], (unsigned long long)work);
   }
   if (tid < a.B) {
     TreeItem x{};
@@ -199,8 +204,13 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
       x.tiles = ((q.len + q.cnt - 1) >> own.tile_shift) + 1 - x.lo;
       x.row_tiles = (q.cnt + own.row_tokens - 1) / own.row_tokens;
     }
-    put_item(own, p.two ? tid : p.groups + tid, x);
+    const long long work = put_item(own, p.two ? tid : p.groups + tid, x);
+    if (work) atomicAdd(&totals[1], (unsigned long long)work);
     p.group_of[tid] = hide > 0 ? g : -1;
+  }
+  if (p.two) {
+    __syncthreads();
+    if (tid < 2) const_cast<long long*>(a.totals)[tid] = (long long)totals[tid];
   }
 }
 
@@ -233,30 +243,40 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
   using Source = TreeSource<true>;
   const int own_item = p.two ? b : p.groups + b, g = p.group_of[b];
   const TreeItem own = Source::load(line, own_item);
-  const long long own_all = line.item_base[line.item_count], all = a.item_base[a.item_count];
+  // (a line of no work has no block that would write where its items start)
+  const long long all = p.two ? a.totals[0] : a.item_base[a.item_count], own_all = p.two ? a.totals[1] : all;
+  const long long both[2] = {all, own_all};
   const int own_base = (int)line.item_base[own_item], rows = own.tokens * a.group;
+  const TreeItem shared = Source::load(a, g < 0 ? 0 : g);
+  const int base = (int)a.item_base[g < 0 ? 0 : g];
   if (own.tiles == 0 || r0 >= rows || own_all > 0x7fffffffLL || all > 0x7fffffffLL) return;
   // this lane's row of the four (the last one again behind it)
   const int mine = r0 + (lane & 3) < rows ? r0 + (lane & 3) : rows - 1;
   const int t = (int)((uint32_t)mine / (uint32_t)a.group), gh = mine - t * a.group;
   const size_t row = ((size_t)b * a.T + t) * a.heads + h * a.group + gh;
-  auto parts_of = [&](const TreeArgs& l, long long tiles, const TreeItem& x, int base, int token) {
+  const int split = p.two ? tree_split(both, a.blocks) : a.blocks;
+  auto parts_of = [&](const TreeArgs& l, int blocks, int W, const TreeItem& x, int from, int token) {
     Parts r;
-    const int W = (int)tiles, G = W < l.blocks ? W : l.blocks;
-    auto block_of = [&](int at) { return (int)((((long long)at + 1) * G - 1) / W); };
+    const int G = W < blocks ? W : blocks;
+    // the block of a place: floor(((at + 1) G - 1) / W), found from below
+    const float each = (float)G / (float)W;
+    auto block_of = [&](int at) {
+      int c = (int)((float)at * each);
+      c = c >= G ? G - 1 : c;
+      while (c > 0 && tree_first(W, G, c) > at) --c;
+      while (c + 1 < G && tree_first(W, G, c + 1) <= at) ++c;
+      return c;
+    };
     const int rt = token / l.row_tokens;
-    const int us = base + (h * x.row_tiles + rt) * x.tiles;
-    r.first = block_of(us);
-    r.n = block_of(us + x.tiles - 1) - r.first + 1;
-    r.slot = 2 * r.first + (tree_first(W, G, r.first) == us ? 0 : 1);
+    const int us = from + (h * x.row_tiles + rt) * (x.tiles + l.extra);
+    r.first = block_of(us + l.extra);
+    r.n = block_of(us + l.extra + x.tiles - 1) - r.first + 1;
+    r.slot = 2 * r.first + (tree_first(W, G, r.first) >= us ? 0 : 1);
     r.r = (token - rt * l.row_tokens) * l.group + gh;
     return r;
   };
-  Parts x = parts_of(line, own_all, own, own_base, t), y{0, 0, 0, 0};
-  if (g >= 0) {
-    const TreeItem shared = Source::load(a, g);
-    y = parts_of(a, all, shared, (int)a.item_base[g], (b - shared.b) * a.T + t);
-  }
+  Parts x = parts_of(line, p.two ? a.blocks - split : a.blocks, (int)own_all, own, own_base, t), y{0, 0, 0, 0};
+  if (g >= 0) y = parts_of(a, split, (int)all, shared, base, (b - shared.b) * a.T + t);
   const int parts = x.n + y.n;  // of this lane's row
   auto find = [&](int i, float*& stats) {
     const bool second = i >= x.n;

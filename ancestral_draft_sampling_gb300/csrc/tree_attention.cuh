@@ -83,6 +83,16 @@ struct TreeArgs {
   // kinds kTreeShared and kTreeOwn: results of units that one block has whole,
   // by row [B][T][heads] and kind: sums [2][rows][D], maxima and sums [2][rows][2]
   float* whole;
+  // The end of a unit and the start of the next cost as much as some tiles: each
+  // unit of an item has so many places on the line before its own.
+  int extra;
+  // null, or the places of two lines that a launch's blocks share out (tree_split)
+  const long long* totals;
+};
+
+// A block's place among those of its line.
+struct TreeGrid {
+  int block, blocks;
 };
 
 constexpr int kTreeMaxBlocks = 160;   // blocks of a call (the GPU has 152 SMs)
@@ -173,6 +183,7 @@ struct TreeSource {
   static __device__ __forceinline__ int work(const TreeArgs& a, const Seq& q) {
     return q.row_tiles * a.c.kv_heads * q.tiles;
   }
+  static __device__ __forceinline__ int extra(const TreeArgs&) { return 0; }
   static __device__ __forceinline__ int head(const Seq&) { return 0; }
   static __device__ __forceinline__ int tokens(const Seq& q) { return q.cnt; }
   static __device__ __forceinline__ int row(const Seq&, int b) { return b; }
@@ -193,8 +204,9 @@ struct TreeSource<true> {
   static __device__ __forceinline__ Seq make(const TreeArgs&, const Raw& r) { return r; }
   static __device__ __forceinline__ long long work(const TreeArgs& a, int b) { return a.item_work[b]; }
   static __device__ __forceinline__ int work(const TreeArgs& a, const Seq& q) {
-    return q.row_tiles * q.tiles * (q.h < 0 ? a.c.kv_heads : 1);
+    return q.tiles == 0 ? 0 : q.row_tiles * (q.tiles + a.extra) * (q.h < 0 ? a.c.kv_heads : 1);
   }
+  static __device__ __forceinline__ int extra(const TreeArgs& a) { return a.extra; }
   static __device__ __forceinline__ int head(const Seq& q) { return q.h < 0 ? 0 : q.h; }
   static __device__ __forceinline__ int tokens(const Seq& q) { return q.tokens; }
   static __device__ __forceinline__ int row(const Seq& q, int) { return q.b; }
@@ -208,6 +220,16 @@ struct TreeSource<true> {
 __device__ __forceinline__ int tree_first(int W, int G, int c) {
   const uint32_t q = (uint32_t)W / (uint32_t)G, r = (uint32_t)W - q * G;
   return (int)(q * c + r * c / (uint32_t)G);
+}
+
+// Blocks of the first of two lines, of `blocks` for both.  A place of the first costs
+// about one and a half of the second: a pair of tiles of 256 rows 3470 cycles, a tile
+// of few rows of 128 dims 2850, of 64 dims 1425.
+__device__ __forceinline__ int tree_split(const long long* totals, int blocks) {
+  const double first = 1.5 * (double)totals[0], both = first + (double)totals[1];
+  if (totals[0] <= 0 || totals[1] <= 0) return totals[0] > 0 ? blocks : 0;
+  const int n = (int)(blocks * first / both + 0.5);
+  return n < 1 ? 1 : n >= blocks ? blocks - 1 : n;
 }
 
 // A block's walk over its share, one unit at a time.
@@ -227,6 +249,19 @@ struct TreeWalk {
   bool whole;          // all of the unit's tiles are here
 
   __device__ __forceinline__ bool next(const TreeArgs& a) {
+    if constexpr (kItems) {  // a share may end in the places before a unit's tiles
+      do {
+        if (!step(a)) {
+          n = 0;
+          return false;
+        }
+      } while (n == 0);
+      return true;
+    } else {
+      return step(a);
+    }
+  }
+  __device__ __forceinline__ bool step(const TreeArgs& a) {
     if (pos >= end) return false;
     int work = Source::work(a, q);
     while (pos >= base + work) {
@@ -237,8 +272,9 @@ struct TreeWalk {
       work = Source::work(a, q);
     }
     const uint32_t at = (uint32_t)(pos - base);
-    const int unit = (int)(at / (uint32_t)q.tiles);
-    first = (int)at - unit * q.tiles;
+    const int extra = Source::extra(a), places = q.tiles + extra;
+    const int unit = (int)(at / (uint32_t)places);
+    first = (int)at - unit * places;
     h = unit;
     rt = 0;
     if (q.row_tiles > 1) {
@@ -247,10 +283,15 @@ struct TreeWalk {
     }
     h += Source::head(q);
     const int left = end - pos;
-    n = q.tiles - first;
+    n = places - first;
     if (n > left) n = left;
-    whole = n == q.tiles;
     pos += n;
+    if constexpr (kItems) {
+      const int last = first + n - extra;  // tiles before the share's end
+      first = first > extra ? first - extra : 0;
+      n = last > first ? last - first : 0;
+    }
+    whole = n == q.tiles;
     return true;
   }
 };
@@ -262,12 +303,12 @@ struct TreeShare {
   TreeWalk<kItems> walk;
 };
 
-// Every thread of the block calls this (blockDim.x a multiple of 32): sums the
+// Every thread of the block calls this (blockDim.x a multiple of 32, `grid` its place): sums the
 // work of the sequences and finds where this block's share starts.  Leaves the
 // walk in sh, on its first unit (n = 0: there is none), which one thread finds
 // for all.  The block is synchronised twice.
 template <bool kItems>
-__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>& sh) {
+__device__ __forceinline__ void tree_start(const TreeArgs& a, const TreeGrid& grid, TreeShare<kItems>& sh) {
   using Source = TreeSource<kItems>;
   const int n = blockDim.x, t = threadIdx.x, B = Source::count(a);
   const int per = B <= n ? 1 : (int)((uint32_t)(B + n - 1) / (uint32_t)n);
@@ -292,7 +333,7 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>&
     if (i < warp) before += v;
     all += v;
   }
-  if (kItems && a.item_base && blockIdx.x == 0) {
+  if (kItems && a.item_base && grid.block == 0) {
     long long at = before;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -303,15 +344,15 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>&
   }
   TreeWalk<kItems> w{};
   if (all > 0x7fffffffLL) {
-    if (blockIdx.x == 0 && t == 0) cache_error(a.c, kCacheErrPage);
+    if (grid.block == 0 && t == 0) cache_error(a.c, kCacheErrPage);
     all = 0;
   }
   w.W = (int)all;
-  const int G = w.W < a.blocks ? w.W : a.blocks;
-  const bool some = (int)blockIdx.x < G;
+  const int G = w.W < grid.blocks ? w.W : grid.blocks;
+  const bool some = grid.block < G;
   if (some) {
-    w.pos = tree_first(w.W, G, blockIdx.x);
-    w.end = tree_first(w.W, G, blockIdx.x + 1);
+    w.pos = tree_first(w.W, G, grid.block);
+    w.end = tree_first(w.W, G, grid.block + 1);
     if (w.pos >= before && w.pos < before + work) {  // one thread
       w.base = (int)before;
       w.b = b0;
@@ -331,14 +372,14 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>&
 // does not begin there; the unit is this block's to join when the share before
 // it holds the unit's beginning.
 template <bool kItems>
-__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk<kItems>& w) {
+__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeGrid& grid, const TreeWalk<kItems>& w) {
   using Source = TreeSource<kItems>;
   TreeJoin j{};
-  const int c = blockIdx.x;
+  const int c = grid.block;
   if (w.n > 0 && w.first > 0) {
-    const int G = w.W < a.blocks ? w.W : a.blocks;
-    const int us = w.pos - w.n - w.first, before = tree_first(w.W, G, c - 1);
-    if (before <= us) {
+    const int G = w.W < grid.blocks ? w.W : grid.blocks, extra = Source::extra(a);
+    const int us = w.pos - w.n - w.first - extra, before = tree_first(w.W, G, c - 1);
+    if (before <= us + extra) {
       j.b = Source::row(w.q, w.b);
       j.h = w.h;
       j.t0 = w.rt * a.row_tokens;
@@ -346,10 +387,10 @@ __device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk<
       const int tokens = left < a.row_tokens ? left : a.row_tokens;
       j.rows = tokens * a.group;
       j.first = c - 1;
-      j.slot = 2 * (c - 1) + (before == us ? 0 : 1);
+      j.slot = 2 * (c - 1) + (before >= us ? 0 : 1);
       j.last = c;
 #pragma unroll 1
-      while (j.last + 1 < G && tree_first(w.W, G, j.last + 1) < us + w.q.tiles) ++j.last;
+      while (j.last + 1 < G && tree_first(w.W, G, j.last + 1) < us + extra + w.q.tiles) ++j.last;
     }
   }
   a.join[c] = j;
@@ -388,6 +429,8 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_ffma(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_items_tc(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_items_ffma(const TreeArgs& a, cudaStream_t stream);
+// Two lines of items in one launch: units of many rows, and narrow ones.
+cudaError_t launch_two_lines_tc(const TreeArgs& many, const TreeArgs& narrow, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream);
 
 }  // namespace dspark

@@ -87,9 +87,7 @@ namespace {
 
 using namespace sm100;
 
-// Narrow units of items have a warp apart for what comes of their sums.
-template <bool kNarrow, bool kItems>
-constexpr int kThreads = kNarrow && kItems ? 416 : 384;
+constexpr int kThreads = 384;
 constexpr int kTile = 128;             // keys of a tile
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 bfloat16
 constexpr int kNarrowRows = 32;        // rows that each warp of a stream has
@@ -128,7 +126,7 @@ template <bool kItems>
 using Unit = typename std::conditional<kItems, ItemUnit, SeqUnit>::type;
 __device__ __forceinline__ int unit_tokens(const SeqUnit& u) { return u.cnt; }
 __device__ __forceinline__ int unit_tokens(const ItemUnit& u) { return u.tokens; }
-constexpr int kUnits = 4, kUnitReaders = 11;  // warps 0, 1, 3 and the softmax (and 12)
+constexpr int kUnits = 4, kUnitReaders = 11;  // warps 0 (2), 1, 3 and the softmax
 
 template <bool kItems>
 struct Control {  // shared memory behind the tiles
@@ -146,7 +144,7 @@ struct Control {  // shared memory behind the tiles
   // sums by hand: a unit's first scores are there before the last unit's sums
   // have been read.
   uint64_t o_free[2];
-  uint64_t e_full[2];  // of each stream, for warp 12: the unit's maxima and sums are there
+  uint64_t e_full[2];  // of each stream, for warp 0: a narrow unit's maxima and sums are there
   uint64_t u_full[kUnits], u_empty[kUnits];
   Unit<kItems> units[kUnits];
   TreeShare<kItems> share;
@@ -173,7 +171,7 @@ struct Narrow {
   float top[2][4][kNarrowRows];              // of each warp: a maximum that raises m,
   float sum[2][4][kNarrowRows];              // and at the end its part of l
   uint32_t raise[2][4];                      // the warp has such maxima
-  // for warp 12, of two units in turn: m, and the warps' parts of l
+  // for warp 0, of two units in turn: m, and the warps' parts of l
   float end_top[2][2][kNarrowRows], end_sum[2][2][4][kNarrowRows];
   uint8_t rest[32768 - 16384 - 2048 - 32 - 512 - 2048];
 };
@@ -654,11 +652,10 @@ __device__ __noinline__ bool fill_ring(const TcArgs& P, Control<kItems>& sh, boo
   return ok;
 }
 
+// What a block does, of those of `grid`'s line.
 template <int D, bool kNarrow, bool kItems>
-__global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
-    tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v) {
+__device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                        const CUtensorMap& map_v, const TreeGrid& grid) {
   using S = Shape<D>;
   using Ctl = Control<kItems>;
   extern __shared__ uint8_t raw[];
@@ -680,7 +677,7 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
     if (lane < 7 + (kAside ? 2 : 0)) mbar_init(bar + 32 + lane, kAside && (lane == 5 || lane == 6) ? 1 : 4);
     if (lane < kUnits) {
       mbar_init(&sh.u_full[lane], 1);
-      mbar_init(&sh.u_empty[lane], kUnitReaders + (kAside ? 1 : 0));
+      mbar_init(&sh.u_empty[lane], kUnitReaders);
     }
     if (lane < 2) sh.add_first[lane] = 0;
     if (lane == 0) sh.failed = 0;
@@ -693,12 +690,12 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
   }
   follow();
   tc_fence_before();
-  tree_start(a, sh.share);  // synchronises the block
+  tree_start(a, grid, sh.share);  // synchronises the block
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   bool ok = true;
 
-  if (warp == 0) {
+  if (warp == (kAside ? 2 : 0)) {
     ok = fill_ring<D, kItems>(P, sh, false, &map_k, &map_q, q_tile, k_ring, lane);
   } else if (warp == 3) {
     ok = fill_ring<D, kItems>(P, sh, true, &map_v, &map_q, q_tile, v_ring, lane);
@@ -889,142 +886,157 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
       if (elect_one()) mma_commit(&sh.drain);
       mbar_wait(&sh.drain, 0, kSpin >> 4);
     }
-  } else if (warp == 2) {
+  } else if (warp == (kAside ? 0 : 2)) {
     // ----------------------------------------------------------- units
-    if (lane == 0) {
-      TreeWalk<kItems> w = sh.share.walk;
-      Place at{0, 1};
-      bool some = w.n > 0, first = true;
-#pragma unroll 1
-      while (true) {
-        ok = wait(&sh.u_empty[at.slot], at.parity);
-        if (!ok) break;
-        Unit<kItems> u{};
-        if (some) {
-          u.n = w.n;
-          u.key = (w.q.lo + w.first) * kTile;
-          if constexpr (kItems) {
-            u.tokens = w.q.tokens;
-            u.hide = w.q.hide;
-            u.kind = w.q.kind;
-            u.list = w.q.list;
-          } else {
-            u.s = w.q.s;
-          }
-          u.len = w.q.len;
-          u.cnt = w.q.cnt;
-          u.b = TreeSource<kItems>::row(w.q, w.b);
-          u.h = w.h;
-          u.t0 = w.rt * a.row_tokens;
-          u.both = TreeSource<kItems>::tokens(w.q) - u.t0 > P.fit;
-          u.whole = w.whole;
-        }
-        sh.units[at.slot] = u;
-        mbar_arrive(&sh.u_full[at.slot]);
-        at.step(kUnits);
-        if (first) tree_describe(a, w);
-        first = false;
-        if (!some) break;
-        some = w.next(a);
-      }
-    }
-  } else if (kAside && warp == 12) {
-    // ------------------------------------------------------------ ends
-    // Joins the two streams' sums of a unit and writes what comes of them, while the
-    // streams are at work on the next one: done by a stream's own warps this kept them
-    // from it for 3000 to 4500 cycles a unit, of 8000 that a unit's end took.
-    int unit = 0;
-    uint32_t used[2] = {0, 0}, stats[2] = {0, 0};  // tiles that a stream has weighed; phases
-    UnitReader units;
-    Unit<kItems> w;
-    const int r_token = (int)((uint32_t)lane / (uint32_t)a.group), r_head = lane - r_token * a.group;
-#pragma unroll 1
-    for (; ok && units.next(sh, w, ok, lane); ++unit) {
-      const int tokens = unit_tokens(w) - w.t0 < P.fit ? unit_tokens(w) - w.t0 : P.fit;
-      const int rows = tokens * a.group, buffer = unit & 1, t = w.t0 + r_token;
-      const bool valid = lane < rows, join = w.n > 1;
-      const size_t out_row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
-      const int slot = 2 * blockIdx.x + (unit == 0 ? 0 : 1);
-      const bool part = !w.whole || a.whole;
-      float *part_sums = nullptr, *part_stats = nullptr;
-      if constexpr (kItems) {
-        if (part) {
-          part_sums = w.whole ? tree_whole(a, w.kind, out_row) : tree_part(a, slot) + (size_t)lane * D;
-          part_stats = w.whole ? tree_whole_stats(a, w.kind, out_row) : tree_part_stats(a, slot) + 2 * lane;
-        }
-      }
-      float m[2], l[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        m[st] = -INFINITY;
-        if (st < w.n) {
-          used[st] += (uint32_t)(w.n + 1 - st) >> 1;
-          ok = ok && wait_warp(&sh.e_full[st], stats[st]++ & 1);
-          if (!ok) break;
-          m[st] = *(volatile float*)&nar.end_top[buffer][st][lane];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l[st] += *(volatile float*)&nar.end_sum[buffer][st][i][lane];
-          ok = wait_warp(&sh.pv_done[st], (used[st] - 1) & 1);
-        }
-      }
-      if (!ok) break;
-      tc_fence_after();
-      const float now = fmaxf(m[0], m[1]);
-      const float fa = m[0] == now ? 1.0f : ex2(m[0] - now), fb = !join ? 0.0f : m[1] == now ? 1.0f : ex2(m[1] - now);
-      const float sum = l[0] * fa + l[1] * fb;
-      const float inv = !part ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-#pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        __syncwarp();
-        tmem_ld32(tmem + S::o_col(0) + 32 * i, o);
-        if (join) {
-          uint32_t o2[32];
-          tmem_ld32(tmem + S::o_col(1) + 32 * i, o2);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            o[k] = __float_as_uint(__uint_as_float(o[k]) * fa + __uint_as_float(o2[k]) * fb);
+    TreeWalk<kItems> walk = sh.share.walk;
+    Place at{0, 1};
+    bool some = walk.n > 0, first = true;
+    // describes the next unit, or that there are no more; one thread
+    auto describe = [&]() {
+      ok = wait(&sh.u_empty[at.slot], at.parity);
+      if (!ok) return false;
+      Unit<kItems> u{};
+      if (some) {
+        u.n = walk.n;
+        u.key = (walk.q.lo + walk.first) * kTile;
+        if constexpr (kItems) {
+          u.tokens = walk.q.tokens;
+          u.hide = walk.q.hide;
+          u.kind = walk.q.kind;
+          u.list = walk.q.list;
         } else {
-          tmem_ld_wait();
+          u.s = walk.q.s;
         }
-        if (i + 1 == D / 32) {  // the sums have been read
-          tc_fence_before();
+        u.len = walk.q.len;
+        u.cnt = walk.q.cnt;
+        u.b = TreeSource<kItems>::row(walk.q, walk.b);
+        u.h = walk.h;
+        u.t0 = walk.rt * a.row_tokens;
+        u.both = TreeSource<kItems>::tokens(walk.q) - u.t0 > P.fit;
+        u.whole = walk.whole;
+      }
+      sh.units[at.slot] = u;
+      mbar_arrive(&sh.u_full[at.slot]);
+      at.step(kUnits);
+      if (first) tree_describe(a, grid, walk);
+      first = false;
+      if (!some) return false;
+      some = walk.next(a);
+      return true;
+    };
+    if constexpr (!kAside) {
+      if (lane == 0) {
+#pragma unroll 1
+        while (describe()) {
+        }
+      }
+    } else {
+      // Between descriptions, four units behind them: joins the two streams' sums of a
+      // unit and writes what comes of them, while the streams are at work on the next
+      // one (done by a stream's own warps this kept them from it for 3000 to 4500
+      // cycles a unit, of 8000 that a unit's end took).
+      bool more = true;
+      auto ahead = [&]() {
+        if (lane == 0 && more) more = describe();
+        more = __shfl_sync(0xffffffffu, more, 0);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      };
+#pragma unroll 1
+      for (int i = 0; i < kUnits && more; ++i) ahead();
+      uint32_t used[2] = {0, 0}, stats[2] = {0, 0};  // tiles that a stream has weighed; phases
+      const int r_token = (int)((uint32_t)lane / (uint32_t)a.group), r_head = lane - r_token * a.group;
+#pragma unroll 1
+      for (int unit = 0; ok; ++unit) {
+        __syncwarp();
+        const Unit<kItems> w = sh.units[unit & (kUnits - 1)];
+        if (w.n == 0) break;
+        const int tokens = unit_tokens(w) - w.t0 < P.fit ? unit_tokens(w) - w.t0 : P.fit;
+        const int rows = tokens * a.group, buffer = unit & 1, t = w.t0 + r_token;
+        const bool valid = lane < rows, join = w.n > 1;
+        const size_t out_row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
+        const int slot = 2 * grid.block + (unit == 0 ? 0 : 1);
+        const bool part = !w.whole || a.whole;
+        float *part_sums = nullptr, *part_stats = nullptr;
+        if constexpr (kItems) {
+          if (part) {
+            part_sums = w.whole ? tree_whole(a, w.kind, out_row) : tree_part(a, slot) + (size_t)lane * D;
+            part_stats = w.whole ? tree_whole_stats(a, w.kind, out_row) : tree_part_stats(a, slot) + 2 * lane;
+          }
+        }
+        float m[2], l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          m[st] = -INFINITY;
+          if (st < w.n) {
+            used[st] += (uint32_t)(w.n + 1 - st) >> 1;
+            ok = ok && wait_warp(&sh.e_full[st], stats[st]++ & 1);
+            if (!ok) break;
+            m[st] = *(volatile float*)&nar.end_top[buffer][st][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[st] += *(volatile float*)&nar.end_sum[buffer][st][i][lane];
+            ok = wait_warp(&sh.pv_done[st], (used[st] - 1) & 1);
+          }
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const float now = fmaxf(m[0], m[1]);
+        const float fa = m[0] == now ? 1.0f : ex2(m[0] - now), fb = !join ? 0.0f : m[1] == now ? 1.0f : ex2(m[1] - now);
+        const float sum = l[0] * fa + l[1] * fb;
+        const float inv = !part ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.o_free[0]);
-        }
-        if (valid && !part) {
-          char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + 32 * i);
+          tmem_ld32(tmem + S::o_col(0) + 32 * i, o);
+          if (join) {
+            uint32_t o2[32];
+            tmem_ld32(tmem + S::o_col(1) + 32 * i, o2);
+            tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t p[8];
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) * fa + __uint_as_float(o2[k]) * fb);
+          } else {
+            tmem_ld_wait();
+          }
+          if (i + 1 == D / 32) {  // the sums have been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_free[0]);
+          }
+          if (valid && !part) {
+            char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + 32 * i);
 #pragma unroll
-            for (int d = 0; d < 8; ++d)
-              p[d] = pack_bf16(__uint_as_float(o[16 * k + 2 * d]) * inv, __uint_as_float(o[16 * k + 2 * d + 1]) * inv);
-            if (P.out32) {
-              store32(to + 32 * k, p);
-            } else {
-              reinterpret_cast<uint4*>(to)[2 * k] = make_uint4(p[0], p[1], p[2], p[3]);
-              reinterpret_cast<uint4*>(to)[2 * k + 1] = make_uint4(p[4], p[5], p[6], p[7]);
+            for (int k = 0; k < 2; ++k) {
+              uint32_t p[8];
+#pragma unroll
+              for (int d = 0; d < 8; ++d)
+                p[d] = pack_bf16(__uint_as_float(o[16 * k + 2 * d]) * inv, __uint_as_float(o[16 * k + 2 * d + 1]) * inv);
+              if (P.out32) {
+                store32(to + 32 * k, p);
+              } else {
+                reinterpret_cast<uint4*>(to)[2 * k] = make_uint4(p[0], p[1], p[2], p[3]);
+                reinterpret_cast<uint4*>(to)[2 * k + 1] = make_uint4(p[4], p[5], p[6], p[7]);
+              }
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t p[8];
+#pragma unroll
+              for (int d = 0; d < 8; ++d) p[d] = o[8 * k + d];
+              store32(part_sums + 32 * i + 8 * k, p);
             }
           }
-        } else if (valid) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t p[8];
-#pragma unroll
-            for (int d = 0; d < 8; ++d) p[d] = o[8 * k + d];
-            store32(part_sums + 32 * i + 8 * k, p);
+        }
+        if (valid) {
+          if (part) {
+            part_stats[0] = now;
+            part_stats[1] = sum;
+          } else if (a.lse) {
+            a.lse[out_row] = sum == 0.0f ? -INFINITY : now * kLn2 + logf(sum);
           }
         }
-      }
-      if (valid) {
-        if (part) {
-          part_stats[0] = now;
-          part_stats[1] = sum;
-        } else if (a.lse) {
-          a.lse[out_row] = sum == 0.0f ? -INFINITY : now * kLn2 + logf(sum);
-        }
+        ahead();
       }
     }
   } else {
@@ -1224,7 +1236,7 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
           }
           if (found) {
             if ((kAside || st == 1) && tile == first && unit > 0) {
-              // the first stream (warp 12) may still be reading the last unit's sums, its
+              // the first stream (warp 0) may still be reading the last unit's sums, its
               // join with these; it cannot end this unit before this stream has
               // gone on, so the phase is the last one or this one
               ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
@@ -1303,6 +1315,10 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
       if (!ok) break;
       if (some) look_at(next);
       if constexpr (kAside) {
+        // warp 0 has begun with the last unit: its barriers are waited for by parity, so
+        // no phase may be run ahead of (this unit's first sums wait for the same)
+        if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
+        if (!ok) break;
         if (worked) {
           if (quarter == 0) nar.end_top[unit & 1][st][lane] = m;
           nar.end_sum[unit & 1][st][quarter][lane] = l;
@@ -1327,7 +1343,7 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) l += *(volatile float*)&nar.sum[st][i][lane];
       }
-      const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
+      const int slot = 2 * grid.block + (is_first ? 0 : 1);
       is_first = false;
       if (!both && st == 1) {
         // the first stream joins the two
@@ -1433,14 +1449,30 @@ __global__ void __launch_bounds__(kThreads<kNarrow, kItems>, 1)
 }
 
 template <int D, bool kNarrow, bool kItems>
-cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow, kItems>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, kItems>());
-  if (e != cudaSuccess) return e;
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  tree_tc<D, kNarrow, kItems>(P, map_q, map_k, map_v, TreeGrid{(int)blockIdx.x, P.a.blocks});
+}
+
+// Two lines of items, each with its form: the blocks are shared out by their work.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    two_lines_tc_kernel(const __grid_constant__ TcArgs many, const __grid_constant__ TcArgs narrow,
+                        const __grid_constant__ CUtensorMap many_q, const __grid_constant__ CUtensorMap narrow_q,
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  follow();
+  const int all = many.a.blocks, first = tree_split(many.a.totals, all), block = blockIdx.x;
+  if (block < first) tree_tc<D, false, true>(many, many_q, map_k, map_v, TreeGrid{block, first});
+  else tree_tc<D, true, true>(narrow, narrow_q, map_k, map_v, TreeGrid{block - first, all - first});
+}
+
+// The arguments of a launch.
+template <int D, bool kNarrow, bool kItems>
+cudaError_t prepare(const TreeArgs& a, TcArgs& P, CUtensorMap& mq, CUtensorMap& mk, CUtensorMap& mv) {
   const auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
-  TcArgs P{};
+  P = TcArgs{};
   P.a = a;
   P.page_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
   P.pages = kTile / P.page_rows;
@@ -1455,7 +1487,6 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   P.k_slots = slots - P.v_slots;
   while ((1 << P.page_shift) < a.c.page_size) ++P.page_shift;
   P.out32 = aligned_to(a.out, 32);
-  CUtensorMap mq, mk, mv;
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   {
     const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.c.kv_heads,
@@ -1480,9 +1511,32 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return launch_behind(tree_tc_kernel<D, kNarrow, kItems>, a.blocks, kThreads<kNarrow, kItems>,
-                       smem_bytes<D, kItems>(), stream, P,
+  return cudaSuccess;
+}
+
+template <int D, bool kNarrow, bool kItems>
+cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+  TcArgs P;
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow, kItems>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, kItems>());
+  if (e == cudaSuccess) e = prepare<D, kNarrow, kItems>(a, P, mq, mk, mv);
+  if (e != cudaSuccess) return e;
+  return launch_behind(tree_tc_kernel<D, kNarrow, kItems>, a.blocks, kThreads, smem_bytes<D, kItems>(), stream, P,
                        mq, mk, mv);
+}
+
+template <int D>
+cudaError_t launch_two(const TreeArgs& many, const TreeArgs& narrow, cudaStream_t stream) {
+  TcArgs P, Q;
+  CUtensorMap pq, qq, mk, mv;
+  cudaError_t e = cudaFuncSetAttribute(two_lines_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem_bytes<D, true>());
+  if (e == cudaSuccess) e = prepare<D, false, true>(many, P, pq, mk, mv);
+  if (e == cudaSuccess) e = prepare<D, true, true>(narrow, Q, qq, mk, mv);
+  if (e != cudaSuccess) return e;
+  return launch_behind(two_lines_tc_kernel<D>, many.blocks, kThreads, smem_bytes<D, true>(), stream, P, Q, pq, qq,
+                       mk, mv);
 }
 
 template <bool kItems>
