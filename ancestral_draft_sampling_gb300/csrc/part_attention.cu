@@ -42,7 +42,7 @@ __device__ __forceinline__ Held find_held(const TreeArgs& a, int b, bool report)
   return r;
 }
 
-__device__ __forceinline__ long long put_item(const TreeArgs& a, int i, const TreeItem& x) {
+__device__ __forceinline__ void put_item(const TreeArgs& a, int i, const TreeItem& x) {
   const int4* from = reinterpret_cast<const int4*>(&x);
   int4* to = reinterpret_cast<int4*>(const_cast<TreeItem*>(a.items) + i);
   to[0] = from[0];
@@ -51,7 +51,6 @@ __device__ __forceinline__ long long put_item(const TreeArgs& a, int i, const Tr
   const long long work =
       x.tiles == 0 ? 0 : (long long)(x.tiles + a.extra) * x.row_tiles * (x.h < 0 ? a.c.kv_heads : 1);
   const_cast<long long*>(a.item_work)[i] = work;
-  return work;
 }
 
 // ---------------------------------------------------------- selected pages
@@ -135,11 +134,9 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
   __shared__ int start[kMaxB + 1];  // of the groups
   __shared__ int prefix[kMaxB];     // their shared tokens; 0: each sequence by itself
   __shared__ int used[kMaxB];       // by a sequence
-  __shared__ unsigned long long totals[2];  // places of the lines
   const TreeArgs &a = p.shared, &own = p.two ? p.own : p.shared;
   follow();
   const int tid = threadIdx.x;  // kMaxB sequences at most
-  if (tid < 2) totals[tid] = 0;
   Held q{-1, 0, -1, 0};
   if (tid < a.B) q = find_held(a, tid, true);
   bool fine = true;
@@ -186,8 +183,7 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
       x.tiles = ((x.len - 1) >> a.tile_shift) + 1;
       x.row_tiles = (x.tokens + a.row_tokens - 1) / a.row_tokens;
     }
-    const long long work = put_item(a, tid, x);
-    if (work) atomicAdd(&totals[0], (unsigned long long)work);
+    put_item(a, tid, x);
   }
   if (tid < a.B) {
     TreeItem x{};
@@ -204,13 +200,8 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
       x.tiles = ((q.len + q.cnt - 1) >> own.tile_shift) + 1 - x.lo;
       x.row_tiles = (q.cnt + own.row_tokens - 1) / own.row_tokens;
     }
-    const long long work = put_item(own, p.two ? tid : p.groups + tid, x);
-    if (work) atomicAdd(&totals[1], (unsigned long long)work);
+    put_item(own, p.two ? tid : p.groups + tid, x);
     p.group_of[tid] = hide > 0 ? g : -1;
-  }
-  if (p.two) {
-    __syncthreads();
-    if (tid < 2) const_cast<long long*>(a.totals)[tid] = (long long)totals[tid];
   }
 }
 
@@ -243,9 +234,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
   using Source = TreeSource<true>;
   const int own_item = p.two ? b : p.groups + b, g = p.group_of[b];
   const TreeItem own = Source::load(line, own_item);
-  // (a line of no work has no block that would write where its items start)
-  const long long all = p.two ? a.totals[0] : a.item_base[a.item_count], own_all = p.two ? a.totals[1] : all;
-  const long long both[2] = {all, own_all};
+  const long long own_all = line.item_base[line.item_count], all = a.item_base[a.item_count];
   const int own_base = (int)line.item_base[own_item], rows = own.tokens * a.group;
   const TreeItem shared = Source::load(a, g < 0 ? 0 : g);
   const int base = (int)a.item_base[g < 0 ? 0 : g];
@@ -254,29 +243,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
   const int mine = r0 + (lane & 3) < rows ? r0 + (lane & 3) : rows - 1;
   const int t = (int)((uint32_t)mine / (uint32_t)a.group), gh = mine - t * a.group;
   const size_t row = ((size_t)b * a.T + t) * a.heads + h * a.group + gh;
-  const int split = p.two ? tree_split(both, a.blocks) : a.blocks;
-  auto parts_of = [&](const TreeArgs& l, int blocks, int W, const TreeItem& x, int from, int token) {
+  auto parts_of = [&](const TreeArgs& l, int W, const TreeItem& x, int from, int token) {
     Parts r;
-    const int G = W < blocks ? W : blocks;
-    // the block of a place: floor(((at + 1) G - 1) / W), found from below
-    const float each = (float)G / (float)W;
+    const int G = W < l.blocks ? W : l.blocks, q = W / G, rest = W - q * G;
+    const float each = (float)G / (float)W, part = 1.0f / (float)G;
+    // tree_first: rest c < 2^15, so half a unit outweighs float's rounding
+    auto first_of = [&](int c) { return q * c + (int)(((float)(rest * c) + 0.5f) * part); };
+    // the block of a place, found from beside it
     auto block_of = [&](int at) {
       int c = (int)((float)at * each);
       c = c >= G ? G - 1 : c;
-      while (c > 0 && tree_first(W, G, c) > at) --c;
-      while (c + 1 < G && tree_first(W, G, c + 1) <= at) ++c;
+      while (c > 0 && first_of(c) > at) --c;
+      while (c + 1 < G && first_of(c + 1) <= at) ++c;
       return c;
     };
-    const int rt = token / l.row_tokens;
+    const int rt = l.row_tiles == 1 ? 0 : token / l.row_tokens;
     const int us = from + (h * x.row_tiles + rt) * (x.tiles + l.extra);
     r.first = block_of(us + l.extra);
     r.n = block_of(us + l.extra + x.tiles - 1) - r.first + 1;
-    r.slot = 2 * r.first + (tree_first(W, G, r.first) >= us ? 0 : 1);
+    r.slot = 2 * r.first + (first_of(r.first) >= us ? 0 : 1);
     r.r = (token - rt * l.row_tokens) * l.group + gh;
     return r;
   };
-  Parts x = parts_of(line, p.two ? a.blocks - split : a.blocks, (int)own_all, own, own_base, t), y{0, 0, 0, 0};
-  if (g >= 0) y = parts_of(a, split, (int)all, shared, base, (b - shared.b) * a.T + t);
+  Parts x = parts_of(line, (int)own_all, own, own_base, t), y{0, 0, 0, 0};
+  if (g >= 0) y = parts_of(a, (int)all, shared, base, (b - shared.b) * a.T + t);
   const int parts = x.n + y.n;  // of this lane's row
   auto find = [&](int i, float*& stats) {
     const bool second = i >= x.n;

@@ -86,13 +86,6 @@ struct TreeArgs {
   // The end of a unit and the start of the next cost as much as some tiles: each
   // unit of an item has so many places on the line before its own.
   int extra;
-  // null, or the places of two lines that a launch's blocks share out (tree_split)
-  const long long* totals;
-};
-
-// A block's place among those of its line.
-struct TreeGrid {
-  int block, blocks;
 };
 
 constexpr int kTreeMaxBlocks = 160;   // blocks of a call (the GPU has 152 SMs)
@@ -222,16 +215,6 @@ __device__ __forceinline__ int tree_first(int W, int G, int c) {
   return (int)(q * c + r * c / (uint32_t)G);
 }
 
-// Blocks of the first of two lines, of `blocks` for both.  A place of the first costs
-// about one and a half of the second: a pair of tiles of 256 rows 3470 cycles, a tile
-// of few rows of 128 dims 2850, of 64 dims 1425.
-__device__ __forceinline__ int tree_split(const long long* totals, int blocks) {
-  const double first = 1.5 * (double)totals[0], both = first + (double)totals[1];
-  if (totals[0] <= 0 || totals[1] <= 0) return totals[0] > 0 ? blocks : 0;
-  const int n = (int)(blocks * first / both + 0.5);
-  return n < 1 ? 1 : n >= blocks ? blocks - 1 : n;
-}
-
 // A block's walk over its share, one unit at a time.
 template <bool kItems>
 struct TreeWalk {
@@ -303,12 +286,12 @@ struct TreeShare {
   TreeWalk<kItems> walk;
 };
 
-// Every thread of the block calls this (blockDim.x a multiple of 32, `grid` its place): sums the
+// Every thread of the block calls this (blockDim.x a multiple of 32): sums the
 // work of the sequences and finds where this block's share starts.  Leaves the
 // walk in sh, on its first unit (n = 0: there is none), which one thread finds
 // for all.  The block is synchronised twice.
 template <bool kItems>
-__device__ __forceinline__ void tree_start(const TreeArgs& a, const TreeGrid& grid, TreeShare<kItems>& sh) {
+__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>& sh) {
   using Source = TreeSource<kItems>;
   const int n = blockDim.x, t = threadIdx.x, B = Source::count(a);
   const int per = B <= n ? 1 : (int)((uint32_t)(B + n - 1) / (uint32_t)n);
@@ -333,7 +316,7 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, const TreeGrid& gr
     if (i < warp) before += v;
     all += v;
   }
-  if (kItems && a.item_base && grid.block == 0) {
+  if (kItems && a.item_base && blockIdx.x == 0) {
     long long at = before;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -344,15 +327,15 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, const TreeGrid& gr
   }
   TreeWalk<kItems> w{};
   if (all > 0x7fffffffLL) {
-    if (grid.block == 0 && t == 0) cache_error(a.c, kCacheErrPage);
+    if (blockIdx.x == 0 && t == 0) cache_error(a.c, kCacheErrPage);
     all = 0;
   }
   w.W = (int)all;
-  const int G = w.W < grid.blocks ? w.W : grid.blocks;
-  const bool some = grid.block < G;
+  const int G = w.W < a.blocks ? w.W : a.blocks;
+  const bool some = (int)blockIdx.x < G;
   if (some) {
-    w.pos = tree_first(w.W, G, grid.block);
-    w.end = tree_first(w.W, G, grid.block + 1);
+    w.pos = tree_first(w.W, G, blockIdx.x);
+    w.end = tree_first(w.W, G, blockIdx.x + 1);
     if (w.pos >= before && w.pos < before + work) {  // one thread
       w.base = (int)before;
       w.b = b0;
@@ -372,12 +355,12 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, const TreeGrid& gr
 // does not begin there; the unit is this block's to join when the share before
 // it holds the unit's beginning.
 template <bool kItems>
-__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeGrid& grid, const TreeWalk<kItems>& w) {
+__device__ __forceinline__ void tree_describe(const TreeArgs& a, const TreeWalk<kItems>& w) {
   using Source = TreeSource<kItems>;
   TreeJoin j{};
-  const int c = grid.block;
+  const int c = blockIdx.x;
   if (w.n > 0 && w.first > 0) {
-    const int G = w.W < grid.blocks ? w.W : grid.blocks, extra = Source::extra(a);
+    const int G = w.W < a.blocks ? w.W : a.blocks, extra = Source::extra(a);
     const int us = w.pos - w.n - w.first - extra, before = tree_first(w.W, G, c - 1);
     if (before <= us + extra) {
       j.b = Source::row(w.q, w.b);
@@ -429,8 +412,6 @@ cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_ffma(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_items_tc(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_items_ffma(const TreeArgs& a, cudaStream_t stream);
-// Two lines of items in one launch: units of many rows, and narrow ones.
-cudaError_t launch_two_lines_tc(const TreeArgs& many, const TreeArgs& narrow, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream);
 
 }  // namespace dspark

@@ -145,8 +145,7 @@ __global__ void __launch_bounds__(Tiles<T, ND, RW>::kThreads)
   }
   const float c = a.scale * 1.4426950408889634f;
   follow();
-  const TreeGrid grid{(int)blockIdx.x, a.blocks};
-  tree_start(a, grid, share);
+  tree_start(a, share);
   NextTile<kItems> ahead{share.walk, 0, share.walk.n > 0};
   TreeWalk<kItems> w = share.walk;
 
@@ -496,7 +495,7 @@ __global__ void __launch_bounds__(Tiles<T, ND, RW>::kThreads)
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   // behind the work, so that the first tile does not wait for it
-  if (threadIdx.x == 0) tree_describe(a, grid, share.walk);
+  if (threadIdx.x == 0) tree_describe(a, share.walk);
 }
 
 template <typename T, int ND, bool halves, int RW, bool kItems>

@@ -652,10 +652,11 @@ __device__ __noinline__ bool fill_ring(const TcArgs& P, Control<kItems>& sh, boo
   return ok;
 }
 
-// What a block does, of those of `grid`'s line.
 template <int D, bool kNarrow, bool kItems>
-__device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_q, const CUtensorMap& map_k,
-                                        const CUtensorMap& map_v, const TreeGrid& grid) {
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v) {
   using S = Shape<D>;
   using Ctl = Control<kItems>;
   extern __shared__ uint8_t raw[];
@@ -690,7 +691,7 @@ __device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_
   }
   follow();
   tc_fence_before();
-  tree_start(a, grid, sh.share);  // synchronises the block
+  tree_start(a, sh.share);  // synchronises the block
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   bool ok = true;
@@ -918,7 +919,7 @@ __device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_
       sh.units[at.slot] = u;
       mbar_arrive(&sh.u_full[at.slot]);
       at.step(kUnits);
-      if (first) tree_describe(a, grid, walk);
+      if (first) tree_describe(a, walk);
       first = false;
       if (!some) return false;
       some = walk.next(a);
@@ -954,7 +955,7 @@ __device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_
         const int rows = tokens * a.group, buffer = unit & 1, t = w.t0 + r_token;
         const bool valid = lane < rows, join = w.n > 1;
         const size_t out_row = ((size_t)w.b * a.T + t) * a.heads + w.h * a.group + r_head;
-        const int slot = 2 * grid.block + (unit == 0 ? 0 : 1);
+        const int slot = 2 * blockIdx.x + (unit == 0 ? 0 : 1);
         const bool part = !w.whole || a.whole;
         float *part_sums = nullptr, *part_stats = nullptr;
         if constexpr (kItems) {
@@ -1343,7 +1344,7 @@ __device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_
 #pragma unroll
         for (int i = 0; i < 4; ++i) l += *(volatile float*)&nar.sum[st][i][lane];
       }
-      const int slot = 2 * grid.block + (is_first ? 0 : 1);
+      const int slot = 2 * blockIdx.x + (is_first ? 0 : 1);
       is_first = false;
       if (!both && st == 1) {
         // the first stream joins the two
@@ -1449,30 +1450,14 @@ __device__ __forceinline__ void tree_tc(const TcArgs& P, const CUtensorMap& map_
 }
 
 template <int D, bool kNarrow, bool kItems>
-__global__ void __launch_bounds__(kThreads, 1)
-    tree_tc_kernel(const __grid_constant__ TcArgs P, const __grid_constant__ CUtensorMap map_q,
-                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  tree_tc<D, kNarrow, kItems>(P, map_q, map_k, map_v, TreeGrid{(int)blockIdx.x, P.a.blocks});
-}
-
-// Two lines of items, each with its form: the blocks are shared out by their work.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    two_lines_tc_kernel(const __grid_constant__ TcArgs many, const __grid_constant__ TcArgs narrow,
-                        const __grid_constant__ CUtensorMap many_q, const __grid_constant__ CUtensorMap narrow_q,
-                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  follow();
-  const int all = many.a.blocks, first = tree_split(many.a.totals, all), block = blockIdx.x;
-  if (block < first) tree_tc<D, false, true>(many, many_q, map_k, map_v, TreeGrid{block, first});
-  else tree_tc<D, true, true>(narrow, narrow_q, map_k, map_v, TreeGrid{block - first, all - first});
-}
-
-// The arguments of a launch.
-template <int D, bool kNarrow, bool kItems>
-cudaError_t prepare(const TreeArgs& a, TcArgs& P, CUtensorMap& mq, CUtensorMap& mk, CUtensorMap& mv) {
+cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow, kItems>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, kItems>());
+  if (e != cudaSuccess) return e;
   const auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
-  P = TcArgs{};
+  TcArgs P{};
   P.a = a;
   P.page_rows = a.c.page_size < kTile ? a.c.page_size : kTile;
   P.pages = kTile / P.page_rows;
@@ -1487,6 +1472,7 @@ cudaError_t prepare(const TreeArgs& a, TcArgs& P, CUtensorMap& mq, CUtensorMap& 
   P.k_slots = slots - P.v_slots;
   while ((1 << P.page_shift) < a.c.page_size) ++P.page_shift;
   P.out32 = aligned_to(a.out, 32);
+  CUtensorMap mq, mk, mv;
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   {
     const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.c.kv_heads,
@@ -1511,32 +1497,8 @@ cudaError_t prepare(const TreeArgs& a, TcArgs& P, CUtensorMap& mq, CUtensorMap& 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  return cudaSuccess;
-}
-
-template <int D, bool kNarrow, bool kItems>
-cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
-  TcArgs P;
-  CUtensorMap mq, mk, mv;
-  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, kNarrow, kItems>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, kItems>());
-  if (e == cudaSuccess) e = prepare<D, kNarrow, kItems>(a, P, mq, mk, mv);
-  if (e != cudaSuccess) return e;
   return launch_behind(tree_tc_kernel<D, kNarrow, kItems>, a.blocks, kThreads, smem_bytes<D, kItems>(), stream, P,
                        mq, mk, mv);
-}
-
-template <int D>
-cudaError_t launch_two(const TreeArgs& many, const TreeArgs& narrow, cudaStream_t stream) {
-  TcArgs P, Q;
-  CUtensorMap pq, qq, mk, mv;
-  cudaError_t e = cudaFuncSetAttribute(two_lines_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem_bytes<D, true>());
-  if (e == cudaSuccess) e = prepare<D, false, true>(many, P, pq, mk, mv);
-  if (e == cudaSuccess) e = prepare<D, true, true>(narrow, Q, qq, mk, mv);
-  if (e != cudaSuccess) return e;
-  return launch_behind(two_lines_tc_kernel<D>, many.blocks, kThreads, smem_bytes<D, true>(), stream, P, Q, pq, qq,
-                       mk, mv);
 }
 
 template <bool kItems>

@@ -742,7 +742,7 @@ DSPARK_API size_t dspark_prefix_workspace_bytes(int B, int T, int heads,
  * group's where its first row does not hold the prefix (error 12).  Results do
  * not depend on it where the pages hold the same tokens, but for the order of the
  * sums.  All else is as for dspark_tree_attention; partial results of both kinds
- * are float32.  B * T * heads < 2^31.  Three launches, graph capturable, no
+ * are float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no
  * synchronisation.
  */
 DSPARK_API dspark_status dspark_prefix_attention(
