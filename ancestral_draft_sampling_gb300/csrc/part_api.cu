@@ -96,7 +96,7 @@ PrefixLayout prefix_layout(int B, int T, int heads, int kv_heads, int D) {
   L.shared = item_layout((long long)B * T, (size_t)2 * B, group, D);
   L.own = item_layout(T, B, group, D);  // behind it
   L.base = L.shared.end + L.own.end;
-  L.group_of = align_up(L.base + ((size_t)2 * B + 2) * sizeof(long long), 256);
+  L.group_of = align_up(L.base + ((size_t)2 * B + 4) * sizeof(long long), 256);
   L.whole = align_up(L.group_of + (size_t)B * sizeof(int32_t), 256);
   L.total = align_up(L.whole + (size_t)2 * B * T * heads * (D + 2) * sizeof(float), 256);
   return L;
@@ -315,8 +315,8 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
   // A sequence's rows are few, a group's many: where that makes different forms of the
   // tensor-core kernel, each kind is launched in its own.  88 single tokens of 8 heads
   // behind a prefix of 4000 keys: one line in the form of many rows 119 us, a launch for
-  // each kind %%; 64 x 8 tokens, 16 behind each of four prefixes of up to 16000 keys: 139
-  // and %%.  (One launch whose blocks are shared out between both kinds: 99 and 159 us,
+  // each kind 92; 64 x 8 tokens, 16 behind each of four prefixes of up to 16000 keys: 139
+  // and 140.  (One launch whose blocks are shared out between both kinds: 99 and 159 us,
   // with blocks that others' loads delay.)
   p.two = tree_tc_supported(a) && tree_tc_narrow(a, T) && !tree_tc_narrow(a, B * T);
   p.own = a;
@@ -324,7 +324,7 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
   a.item_count = p.two ? groups : groups + B;
   if (p.two) {
     fill_items(p.own, L.own, ws + L.shared.end);
-    p.own.item_base = a.item_base + groups + 1;
+    p.own.item_base = a.item_base + groups + 2;
     p.own.item_count = B;
     plan(p.own, T);
   }

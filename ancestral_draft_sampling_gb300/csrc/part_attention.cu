@@ -77,42 +77,60 @@ __global__ void __launch_bounds__(kListThreads) sparse_items_kernel(const __grid
     const size_t step = (size_t)a.c.kv_heads * p.count;  // between the lists of two tokens
     const int32_t* from = p.pages + ((size_t)b * p.lists * a.c.kv_heads + h) * p.count;
     int n = 0;
-    for (int r0 = 0; r0 < F; r0 += kRange) {
-      for (int i = tid; i < 2 * kRange; i += kListThreads) (&seen[0][0])[i] = 0;
-      __syncthreads();
-      bool any = false;
-      for (int e = tid; e < entries; e += kListThreads) {
-        const int t = (int)((uint32_t)e / (uint32_t)p.count);
-        const int page = from[t * step + (e - t * p.count)];
-        if (page >= F && r0 == 0) cache_error(a.c, kCacheErrPage);
-        if (page < r0 || page >= F || page >= r0 + kRange) continue;
-        any = true;
-        if (p.lists == 1) {
-          seen[0][page - r0] = seen[1][page - r0] = ~0u;
-        } else {
-          atomicOr(&seen[t >> 5][page - r0], 1u << (t & 31));
-        }
+    // one list in ascending order, as it is selected, needs no sorting out
+    bool sorted = lists == 1;
+    if (sorted) {
+      for (int i = tid; i < p.count && sorted; i += kListThreads) {
+        const int page = from[i], before = i > 0 ? from[i - 1] : -1;
+        sorted = page < F && (page < 0 || i == 0 || (before >= 0 && before < page));
+        n += page >= 0;
       }
-      if (!__syncthreads_or(any)) continue;
-      constexpr int kEach = kRange / kListThreads;
-      int mine = 0;
-      for (int i = 0; i < kEach; ++i) {
-        const int at = tid * kEach + i;
-        mine += (seen[0][at] | seen[1][at]) != 0;
-      }
+      sorted = __syncthreads_and(sorted);
+    }
+    if (sorted) {
       int total;
-      int at = n + block_exclusive(mine, warps, total);
-      for (int i = 0; i < kEach; ++i) {
-        const int k = tid * kEach + i;
-        const uint64_t m = (uint64_t)seen[1][k] << 32 | seen[0][k];
-        if (m) {
-          list[at] = cache_page(a.c, q.s, r0 + k, q.held);  // -1 is reported where it is read
-          bits[at] = m;
-          ++at;
-        }
+      block_exclusive(n, warps, total);
+      n = total;
+      for (int i = tid; i < n; i += kListThreads) {
+        list[i] = cache_page(a.c, q.s, from[i], q.held);  // -1 is reported where it is read
+        bits[i] = ~0ull;
       }
-      n += total;
-      __syncthreads();
+    } else {
+      n = 0;
+      for (int r0 = 0; r0 < F; r0 += kRange) {
+        const int each = ((F - r0 < kRange ? F - r0 : kRange) + kListThreads - 1) / kListThreads;
+        for (int i = tid; i < each * kListThreads; i += kListThreads) seen[0][i] = seen[1][i] = 0;
+        __syncthreads();
+        bool any = false;
+        for (int e = tid; e < entries; e += kListThreads) {
+          const int t = (int)((uint32_t)e / (uint32_t)p.count);
+          const int page = from[t * step + (e - t * p.count)];
+          if (page >= F && r0 == 0) cache_error(a.c, kCacheErrPage);
+          if (page < r0 || page >= F || page >= r0 + kRange) continue;
+          any = true;
+          if (p.lists == 1) {
+            seen[0][page - r0] = seen[1][page - r0] = ~0u;
+          } else {
+            atomicOr(&seen[t >> 5][page - r0], 1u << (t & 31));
+          }
+        }
+        if (!__syncthreads_or(any)) continue;
+        int mine = 0;
+        for (int i = 0; i < each; ++i) mine += (seen[0][tid * each + i] | seen[1][tid * each + i]) != 0;
+        int total;
+        int at = n + block_exclusive(mine, warps, total);
+        for (int i = 0; i < each; ++i) {
+          const int k = tid * each + i;
+          const uint64_t m = (uint64_t)seen[1][k] << 32 | seen[0][k];
+          if (m) {
+            list[at] = cache_page(a.c, q.s, r0 + k, q.held);
+            bits[at] = m;
+            ++at;
+          }
+        }
+        n += total;
+        __syncthreads();
+      }
     }
     // behind them the partly filled page and the drafted tokens
     const int last = (q.len + q.cnt - 1) / a.c.page_size;
@@ -220,44 +238,49 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
 }
 
 // A row's parts: some of what its sequence has of its own, then some of the prefix.
-// A warp takes four rows, with a lane for each row of eight parts' statistics and the
-// loads of two parts of all four in flight (a row a warp, which finds its parts
-// itself, took 24 us for 16384 rows of 128 dims in four parts, this %%).
-constexpr int kJoinWarps = 4, kBatch = 2;
+// A warp takes two rows, with a lane for each row of 16 parts, which finds that part and
+// its statistics, and the loads of eight parts of both in flight.  Bound by latency:
+// what a line's blocks have of it is found without a division, which the attention's
+// first block has made (88 single tokens of 64 heads in nine parts: 11 us, 13.4 with six
+// divisions a lane and the loads of two parts and four rows in flight, which for 4096
+// rows in two or three parts is the better: 15.8 against 17.8).
+constexpr int kJoinWarps = 4, kJoinRows = 2, kJoinBatch = 8;
 
 template <typename T, int ND>
 __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs p) {
   const TreeArgs &a = p.shared, &line = p.two ? p.own : p.shared;
   follow();
-  const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane >> 2;
-  const int h = blockIdx.y, b = blockIdx.z, r0 = (blockIdx.x * kJoinWarps + (threadIdx.x >> 5)) * 4;
+  const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane >> 1;
+  const int h = blockIdx.y, b = blockIdx.z, r0 = (blockIdx.x * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
   using Source = TreeSource<true>;
   const int own_item = p.two ? b : p.groups + b, g = p.group_of[b];
   const TreeItem own = Source::load(line, own_item);
   const long long own_all = line.item_base[line.item_count], all = a.item_base[a.item_count];
+  const long long own_each = line.item_base[line.item_count + 1], each = a.item_base[a.item_count + 1];
   const int own_base = (int)line.item_base[own_item], rows = own.tokens * a.group;
   const TreeItem shared = Source::load(a, g < 0 ? 0 : g);
   const int base = (int)a.item_base[g < 0 ? 0 : g];
   if (own.tiles == 0 || r0 >= rows || own_all > 0x7fffffffLL || all > 0x7fffffffLL) return;
-  // this lane's row of the four (the last one again behind it)
-  const int mine = r0 + (lane & 3) < rows ? r0 + (lane & 3) : rows - 1;
+  // this lane's row of the two (the last one again behind it)
+  const int mine = r0 + (lane & 1) < rows ? r0 + (lane & 1) : rows - 1;
   const int t = (int)((uint32_t)mine / (uint32_t)a.group), gh = mine - t * a.group;
   const size_t row = ((size_t)b * a.T + t) * a.heads + h * a.group + gh;
-  auto parts_of = [&](const TreeArgs& l, int W, const TreeItem& x, int from, int token) {
+  auto parts_of = [&](const TreeArgs& l, int W, long long shares, const TreeItem& x, int from, int token) {
     Parts r;
-    const int G = W < l.blocks ? W : l.blocks, q = W / G, rest = W - q * G;
-    const float each = (float)G / (float)W, part = 1.0f / (float)G;
+    const int G = W < l.blocks ? W : l.blocks, q = (int)shares, rest = (int)(shares >> 32);
+    const float part = __fdividef(1.0f, (float)G), per = __fdividef((float)G, (float)W);
     // tree_first: rest c < 2^15, so half a unit outweighs float's rounding
     auto first_of = [&](int c) { return q * c + (int)(((float)(rest * c) + 0.5f) * part); };
     // the block of a place, found from beside it
     auto block_of = [&](int at) {
-      int c = (int)((float)at * each);
+      int c = (int)((float)at * per);
       c = c >= G ? G - 1 : c;
       while (c > 0 && first_of(c) > at) --c;
       while (c + 1 < G && first_of(c + 1) <= at) ++c;
       return c;
     };
-    const int rt = l.row_tiles == 1 ? 0 : token / l.row_tokens;
+    // tokens of a group are fewer than 2^17
+    const int rt = (int)(((float)token + 0.5f) * __fdividef(1.0f, (float)l.row_tokens));
     const int us = from + (h * x.row_tiles + rt) * (x.tiles + l.extra);
     r.first = block_of(us + l.extra);
     r.n = block_of(us + l.extra + x.tiles - 1) - r.first + 1;
@@ -265,79 +288,76 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     r.r = (token - rt * l.row_tokens) * l.group + gh;
     return r;
   };
-  Parts x = parts_of(line, (int)own_all, own, own_base, t), y{0, 0, 0, 0};
-  if (g >= 0) y = parts_of(a, (int)all, shared, base, (b - shared.b) * a.T + t);
-  const int parts = x.n + y.n;  // of this lane's row
-  auto find = [&](int i, float*& stats) {
-    const bool second = i >= x.n;
-    const Parts& k = second ? y : x;
-    const TreeArgs& l = second ? a : line;
-    const int j = second ? i - x.n : i;
-    if (k.n == 1) {
-      const int kind = second ? kTreeShared : kTreeOwn;
-      stats = tree_whole_stats(a, kind, row);
-      return tree_whole(a, kind, row);
-    }
-    const int slot = j == 0 ? k.slot : 2 * (k.first + j);
-    stats = tree_part_stats(l, slot) + 2 * k.r;
-    return tree_part(l, slot) + (size_t)k.r * D;
-  };
-  auto stats = [&](int i) {
-    if (i >= parts) return make_float2(-INFINITY, 0.0f);
-    float* at;
-    find(i, at);
-    return *reinterpret_cast<const float2*>(at);
-  };
-  int most = parts;  // of the four rows
-  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-  most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-  float4 v[kBatch][4][ND];
-  auto load_parts = [&](int i) {
+  const Parts x = parts_of(line, (int)own_all, own_each, own, own_base, t);
+  Parts y{0, 0, 0, 0};
+  if (g >= 0) y = parts_of(a, (int)all, each, shared, base, (b - shared.b) * a.T + t);
+  const int parts = x.n + y.n;
+  const int most = max(parts, __shfl_xor_sync(0xffffffffu, parts, 1));  // of both rows
+  float M = -INFINITY, L = 0.0f;
+  float4 o[kJoinRows][ND];
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      float* unused;
-      const unsigned long long at =
-          i + q < parts ? reinterpret_cast<unsigned long long>(find(i + q, unused)) : 0ull;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, at, n));
-#pragma unroll
-        for (int k = 0; k < ND; ++k) {
-          v[q][n][k] = make_float4(0, 0, 0, 0);
-          if (from && k * 128 + lane * 4 < D) v[q][n][k] = load4(from + k * 128 + lane * 4);
-        }
-      }
-    }
-  };
-  float2 st = stats(sub);
-  load_parts(0);  // under way while the weights are made
-  float M = st.x;
-#pragma unroll 1
-  for (int i = sub + 8; i < most; i += 8) M = fmaxf(M, stats(i).x);
-#pragma unroll
-  for (int k = 4; k < 32; k <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-  float L = 0.0f;
-  float4 o[4][ND];
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < kJoinRows; ++n)
 #pragma unroll
     for (int k = 0; k < ND; ++k) o[n][k] = make_float4(0, 0, 0, 0);
 #pragma unroll 1
-  for (int p0 = 0; p0 < most; p0 += 8) {
-    const int n_here = most - p0 < 8 ? most - p0 : 8;
-    if (p0 > 0) st = stats(p0 + sub);
-    // a part that saw nothing weighs nothing
-    const float w = M == -INFINITY ? 0.0f : st.x == M ? 1.0f : exp2f(st.x - M);
-    L += w * st.y;
+  for (int p0 = 0; p0 < most; p0 += 16) {
+    // part p0 + sub of the lane's row
+    unsigned long long sums = 0;
+    float2 st = make_float2(-INFINITY, 0.0f);
+    const int i = p0 + sub;
+    if (i < parts) {
+      const bool second = i >= x.n;
+      const int n = second ? y.n : x.n, first = second ? y.first : x.first, r = second ? y.r : x.r;
+      const int j = second ? i - x.n : i, kind = second ? kTreeShared : kTreeOwn;
+      const TreeArgs& l = second ? a : line;
+      const int slot = j == 0 ? (second ? y.slot : x.slot) : 2 * (first + j);
+      const float* stats = n == 1 ? tree_whole_stats(a, kind, row) : tree_part_stats(l, slot) + 2 * r;
+      sums = reinterpret_cast<unsigned long long>(n == 1 ? tree_whole(a, kind, row) : tree_part(l, slot) + (size_t)r * D);
+      st = *reinterpret_cast<const float2*>(stats);
+    }
+    const int here = most - p0 < 16 ? most - p0 : 16;
+    float w = 0.0f;
 #pragma unroll 1
-    for (int i = 0; i < n_here; i += kBatch) {
-      if (p0 + i > 0) load_parts(p0 + i);
+    for (int q0 = 0; q0 < here; q0 += kJoinBatch) {
+      float4 v[kJoinBatch][kJoinRows][ND];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        if (i + q >= n_here) break;
+      for (int q = 0; q < kJoinBatch; ++q)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float f = __shfl_sync(0xffffffffu, w, (i + q) * 4 + n);
+        for (int n = 0; n < kJoinRows; ++n) {
+          const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, sums, (q0 + q) * 2 + n));
+#pragma unroll
+          for (int k = 0; k < ND; ++k) {
+            v[q][n][k] = make_float4(0, 0, 0, 0);
+            if (from && k * 128 + lane * 4 < D) v[q][n][k] = load4(from + k * 128 + lane * 4);
+          }
+        }
+      if (q0 == 0) {  // while they are under way: the weights of these sixteen parts
+        float now = st.x;
+#pragma unroll
+        for (int k = 2; k < 32; k <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, k));
+        now = fmaxf(now, M);
+        // a part that saw nothing weighs nothing
+        w = now == -INFINITY ? 0.0f : st.x == now ? 1.0f : exp2f(st.x - now);
+        const float keep = M == now ? 1.0f : exp2f(M - now);
+        float sum = w * st.y;
+#pragma unroll
+        for (int k = 2; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        L = L * keep + sum;
+        M = now;
+        if (p0 > 0) {
+#pragma unroll
+          for (int n = 0; n < kJoinRows; ++n) {
+            const float f = __shfl_sync(0xffffffffu, keep, n);
+#pragma unroll
+            for (int k = 0; k < ND; ++k) o[n][k] = make_float4(o[n][k].x * f, o[n][k].y * f, o[n][k].z * f, o[n][k].w * f);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kJoinBatch; ++q)
+#pragma unroll
+        for (int n = 0; n < kJoinRows; ++n) {
+          const float f = __shfl_sync(0xffffffffu, w, (q0 + q) * 2 + n);
 #pragma unroll
           for (int k = 0; k < ND; ++k) {
             o[n][k].x = fmaf(f, v[q][n][k].x, o[n][k].x);
@@ -346,15 +366,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
             o[n][k].w = fmaf(f, v[q][n][k].w, o[n][k].w);
           }
         }
-      }
     }
   }
-#pragma unroll
-  for (int k = 4; k < 32; k <<= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  if (lane < 4 && r0 + lane < rows && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
+  if (lane < kJoinRows && r0 + lane < rows && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : M * kLn2 + logf(L);
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
+  for (int n = 0; n < kJoinRows; ++n) {
     const float f = __shfl_sync(0xffffffffu, inv, n);
     const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)row, n);
     if (r0 + n >= rows) break;
@@ -380,7 +397,8 @@ cudaError_t launch_prefix_items(const PrefixArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_prefix_join(const PrefixArgs& a, cudaStream_t stream) {
   const TreeArgs& l = a.shared;
-  const dim3 blocks((l.T * l.group + 4 * kJoinWarps - 1) / (4 * kJoinWarps), l.c.kv_heads, l.B);
+  constexpr int rows = kJoinRows * kJoinWarps;
+  const dim3 blocks((l.T * l.group + rows - 1) / rows, l.c.kv_heads, l.B);
   const bool wide = l.c.head_dim > 128;
   const auto kernel = l.c.dtype == DSPARK_F32
                           ? (wide ? prefix_join_kernel<float, 2> : prefix_join_kernel<float, 1>)

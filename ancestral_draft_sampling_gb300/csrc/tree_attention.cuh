@@ -79,7 +79,9 @@ struct TreeArgs {
   int item_count;
   const int32_t* page_list;
   const uint64_t* page_bits;   // beside page_list: bit t: token t sees the page
-  long long* item_base;        // out, or null: [item_count + 1] the line's tile where an item starts
+  // out, or null: [item_count + 2] the line's place where an item starts, all places,
+  // and floor(places / blocks) with the rest of that division above it
+  long long* item_base;
   // kinds kTreeShared and kTreeOwn: results of units that one block has whole,
   // by row [B][T][heads] and kind: sums [2][rows][D], maxima and sums [2][rows][2]
   float* whole;
@@ -323,7 +325,11 @@ __device__ __forceinline__ void tree_start(const TreeArgs& a, TreeShare<kItems>&
       a.item_base[b] = at;
       at += Source::work(a, b);
     }
-    if (t == 0) a.item_base[B] = all;
+    if (t == 0) {
+      a.item_base[B] = all;
+      const uint32_t W = (uint32_t)all, G = W < (uint32_t)a.blocks ? (W ? W : 1u) : (uint32_t)a.blocks;
+      a.item_base[B + 1] = (long long)(W / G) | (long long)(W - W / G * G) << 32;
+    }
   }
   TreeWalk<kItems> w{};
   if (all > 0x7fffffffLL) {
