@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
   if (fine && tid < p.groups && prefix[tid] > 0) {
     const int s = cache_seq(a.c, a.seq, start[tid]), n = prefix[tid];
     list = (long long)s * a.c.max_pages;
-    if (s < 0 || n > (1 << 30) || n > cache_held(a.c, s) * a.c.page_size) {
+    if (s < 0 || n > a.length[start[tid]] || n > (1 << 30) || n > cache_held(a.c, s) * a.c.page_size) {
       cache_error(a.c, kCacheErrGroup);
       prefix[tid] = 0;
     }

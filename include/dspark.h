@@ -739,7 +739,7 @@ DSPARK_API size_t dspark_prefix_workspace_bytes(int B, int T, int heads,
  *                table entries there are not looked at.
  * A row whose sequence has fewer committed tokens than its group's prefix is
  * attended by itself, as all rows are where group_start is no such list, and a
- * group's where its first row does not hold the prefix (error 12).  Results do
+ * group's where its first row has fewer or does not hold them (error 12).  Results do
  * not depend on it where the pages hold the same tokens, but for the order of the
  * sums.  All else is as for dspark_tree_attention; partial results of both kinds
  * are float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no

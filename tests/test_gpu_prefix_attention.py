@@ -217,6 +217,13 @@ def test_groups_that_are_none(cuda, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_first_row_that_has_less_than_the_prefix(cuda, dtype):
+    """What its pages hold behind its own tokens is not read by the others."""
+    s = Prefix(dtype, 64, 1, 2, 4, [(100, [5, 40, 9]), (48, [2, 2])], 16, alone=(7,))
+    s.check(*s.run(prefix=[108, 48]), error=12)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_sequences_out_of_range_are_left(cuda, dtype):
     s = Prefix(dtype, 64, 1, 2, 4, [(48, [5, 40, 9])], 16, alone=(7,))
     good = s.run()
