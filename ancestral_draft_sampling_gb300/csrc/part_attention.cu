@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kListThreads) sparse_items_kernel(const __grid
       }
     } else {
       n = 0;
-      for (int r0 = 0; r0 < F; r0 += kRange) {
+      for (int r0 = 0; r0 < F || r0 == 0; r0 += kRange) {  // without full pages too: entries are looked at
         const int each = ((F - r0 < kRange ? F - r0 : kRange) + kListThreads - 1) / kListThreads;
         for (int i = tid; i < each * kListThreads; i += kListThreads) seen[0][i] = seen[1][i] = 0;
         __syncthreads();

@@ -259,6 +259,22 @@ def test_bad_entries(cuda, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lists", [1, 3])
+def test_entries_of_a_sequence_without_full_pages(cuda, dtype, lists):
+    c = dspark.PagedCache(1, 4, 16, 2, 64, 1, 4, dtype=dtype)
+    c.pool.normal_()
+    n = torch.tensor([9], dtype=torch.int32, device="cuda")
+    dspark.cache_reserve(c, n, 3)
+    q = torch.randn(1, 3, 4, 64, device="cuda").to(dtype)
+    none = torch.full((1, lists, 2, 5), -1, dtype=torch.int32, device="cuda")
+    want = dspark.sparse_attention(c, 0, q, n, none)[0]
+    assert dspark.read_device_error(c) == 0
+    none[0, lists - 1, 1, 2] = 0
+    assert torch.equal(dspark.sparse_attention(c, 0, q, n, none)[0], want)
+    assert dspark.read_device_error(c) == 7
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_graph_replay_and_streams(cuda, dtype):
     """A captured call reads lengths, lists and masks anew, and two graphs with
     workspaces of their own replay in any order; another stream; a workspace that a
