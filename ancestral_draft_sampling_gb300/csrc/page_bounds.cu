@@ -89,8 +89,16 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31;
   for (int b = threadIdx.x; b < a.B; b += kThreads) sh.offset[b] = filled(a, b, sh, blockIdx.x == 0);
   __syncthreads();
+  if ((long long)a.B * a.c.max_pages > INT_MAX) {  // the line is counted in 32 bits
+    long long all = 0;
+    for (int b = 0; b < a.B; ++b) all += sh.offset[b];
+    if (all > INT_MAX) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) cache_error(a.c, kCacheErrPage);
+      return;
+    }
+  }
   row_offsets(sh.offset, sh.offset, a.B, sh.warps);
-  const uint32_t pages = sh.offset[a.B] > 0 ? sh.offset[a.B] : 0;
+  const uint32_t pages = sh.offset[a.B];
   const int words = a.c.head_dim * (int)sizeof(T) / 16;  // of a row
   const int rows = words < 32 ? 32 / words : 1;          // that a warp reads at a time
   const int row0 = words < 32 ? lane / words : 0, word0 = words < 32 ? lane - row0 * words : lane;

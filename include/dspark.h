@@ -641,8 +641,8 @@ DSPARK_API dspark_status dspark_tree_attention(
  * dspark_cache_accept or prompt, with the lengths before and after it, keeps
  * them; a length below its start fills nothing.  Other bounds are left as they
  * are.  A NaN among a page's keys makes the bounds of its dimension NaN.  A
- * sequence that holds fewer than `length` tokens is left out (error 7).  One
- * launch.
+ * sequence that holds fewer than `length` tokens is left out (error 7), and so are
+ * all where they have filled 2^31 pages or more.  One launch.
  */
 DSPARK_API dspark_status dspark_cache_bounds(const dspark_cache* cache,
                                              const int32_t* seq,

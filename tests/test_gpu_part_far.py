@@ -96,3 +96,21 @@ def test_equal_rows_are_equal(cuda):
         assert (x.abs() <= 2 * (2.0 ** -19 + 2048 * 2.0 ** -24)).all()
     assert dspark.read_device_error(c) == 0
     assert math.isfinite(float(lse.sum()))
+
+
+def test_more_pages_than_are_counted(cuda):
+    """One sequence in 1024 rows of a call: 2^31 pages together; and in one."""
+    wide = (1 << 21) + 1
+    c = dspark.PagedCache(1, 2, 1, 1, 8, 1, wide, dtype=F32)
+    c.pool.copy_(torch.arange(32.0, device="cuda").reshape(c.pool.shape))
+    c.block_table.fill_(1)
+    c.page_count.fill_(wide)
+    start, length = ints([0]).repeat(1024), ints([1 << 21]).repeat(1024)
+    seq = torch.zeros_like(start)
+    bounds = torch.zeros(1, 2, 1, 2, 8, device="cuda")
+    dspark.cache_bounds(c, start, length, bounds=bounds, seq=seq)
+    assert dspark.read_device_error(c) == 7 and not bounds.any()
+    start[1:] = 1 << 21  # the first alone
+    dspark.cache_bounds(c, start, length, bounds=bounds, seq=seq)
+    assert dspark.read_device_error(c) == 0
+    assert torch.equal(bounds[0, 1, 0], c.pool[0, 0, 1, 0].expand(2, -1)) and not bounds[0, 0].any()
