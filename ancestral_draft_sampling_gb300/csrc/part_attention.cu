@@ -238,19 +238,19 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
 }
 
 // A row's parts: some of what its sequence has of its own, then some of the prefix.
-// A warp takes two rows, with a lane for each row of 16 parts, which finds that part and
-// its statistics, and the loads of eight parts of both in flight.  Bound by latency:
+// A warp takes four rows, with a lane for each row of 8 parts, which finds that part and
+// its statistics, and the loads of four parts of all in flight.  Bound by latency:
 // what a line's blocks have of it is found without a division, which the attention's
 // first block has made (88 single tokens of 64 heads in nine parts: 11 us, 13.4 with six
-// divisions a lane and the loads of two parts and four rows in flight, which for 4096
-// rows in two or three parts is the better: 15.8 against 17.8).
-constexpr int kJoinWarps = 4, kJoinRows = 2, kJoinBatch = 8;
+// divisions a lane and half as many loads in flight; 16384 rows in two or three parts:
+// 15, and 18 with two rows a warp and eight parts).
+constexpr int kJoinWarps = 4, kJoinRows = 4, kJoinParts = 32 / kJoinRows, kJoinBatch = 4;
 
 template <typename T, int ND>
 __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs p) {
   const TreeArgs &a = p.shared, &line = p.two ? p.own : p.shared;
   follow();
-  const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane >> 1;
+  const int lane = threadIdx.x & 31, D = a.c.head_dim, sub = lane / kJoinRows;
   const int h = blockIdx.y, b = blockIdx.z, r0 = (blockIdx.x * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
   using Source = TreeSource<true>;
   const int own_item = p.two ? b : p.groups + b, g = p.group_of[b];
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
   const TreeItem shared = Source::load(a, g < 0 ? 0 : g);
   const int base = (int)a.item_base[g < 0 ? 0 : g];
   if (own.tiles == 0 || r0 >= rows || own_all > 0x7fffffffLL || all > 0x7fffffffLL) return;
-  // this lane's row of the two (the last one again behind it)
-  const int mine = r0 + (lane & 1) < rows ? r0 + (lane & 1) : rows - 1;
+  // this lane's row of the warp's (the last one again behind it)
+  const int mine = r0 + lane % kJoinRows < rows ? r0 + lane % kJoinRows : rows - 1;
   const int t = (int)((uint32_t)mine / (uint32_t)a.group), gh = mine - t * a.group;
   const size_t row = ((size_t)b * a.T + t) * a.heads + h * a.group + gh;
   auto parts_of = [&](const TreeArgs& l, int W, long long shares, const TreeItem& x, int from, int token) {
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
   Parts y{0, 0, 0, 0};
   if (g >= 0) y = parts_of(a, (int)all, each, shared, base, (b - shared.b) * a.T + t);
   const int parts = x.n + y.n;
-  const int most = max(parts, __shfl_xor_sync(0xffffffffu, parts, 1));  // of both rows
+  const int most = __reduce_max_sync(0xffffffffu, parts);
   float M = -INFINITY, L = 0.0f;
   float4 o[kJoinRows][ND];
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
 #pragma unroll
     for (int k = 0; k < ND; ++k) o[n][k] = make_float4(0, 0, 0, 0);
 #pragma unroll 1
-  for (int p0 = 0; p0 < most; p0 += 16) {
+  for (int p0 = 0; p0 < most; p0 += kJoinParts) {
     // part p0 + sub of the lane's row
     unsigned long long sums = 0;
     float2 st = make_float2(-INFINITY, 0.0f);
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
       sums = reinterpret_cast<unsigned long long>(n == 1 ? tree_whole(a, kind, row) : tree_part(l, slot) + (size_t)r * D);
       st = *reinterpret_cast<const float2*>(stats);
     }
-    const int here = most - p0 < 16 ? most - p0 : 16;
+    const int here = most - p0 < kJoinParts ? most - p0 : kJoinParts;
     float w = 0.0f;
 #pragma unroll 1
     for (int q0 = 0; q0 < here; q0 += kJoinBatch) {
@@ -324,24 +324,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
       for (int q = 0; q < kJoinBatch; ++q)
 #pragma unroll
         for (int n = 0; n < kJoinRows; ++n) {
-          const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, sums, (q0 + q) * 2 + n));
+          const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, sums, (q0 + q) * kJoinRows + n));
 #pragma unroll
           for (int k = 0; k < ND; ++k) {
             v[q][n][k] = make_float4(0, 0, 0, 0);
             if (from && k * 128 + lane * 4 < D) v[q][n][k] = load4(from + k * 128 + lane * 4);
           }
         }
-      if (q0 == 0) {  // while they are under way: the weights of these sixteen parts
+      if (q0 == 0) {  // while they are under way: the weights of these parts
         float now = st.x;
 #pragma unroll
-        for (int k = 2; k < 32; k <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, k));
+        for (int k = kJoinRows; k < 32; k <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, k));
         now = fmaxf(now, M);
         // a part that saw nothing weighs nothing
         w = now == -INFINITY ? 0.0f : st.x == now ? 1.0f : exp2f(st.x - now);
         const float keep = M == now ? 1.0f : exp2f(M - now);
         float sum = w * st.y;
 #pragma unroll
-        for (int k = 2; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        for (int k = kJoinRows; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
         L = L * keep + sum;
         M = now;
         if (p0 > 0) {
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
       for (int q = 0; q < kJoinBatch; ++q)
 #pragma unroll
         for (int n = 0; n < kJoinRows; ++n) {
-          const float f = __shfl_sync(0xffffffffu, w, (q0 + q) * 2 + n);
+          const float f = __shfl_sync(0xffffffffu, w, (q0 + q) * kJoinRows + n);
 #pragma unroll
           for (int k = 0; k < ND; ++k) {
             o[n][k].x = fmaf(f, v[q][n][k].x, o[n][k].x);
