@@ -316,7 +316,7 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
   // tensor-core kernel, each kind is launched in its own.  88 single tokens of 8 heads
   // behind a prefix of 4000 keys: one line in the form of many rows 119 us, a launch for
   // each kind 92; 64 x 8 tokens, 16 behind each of four prefixes of up to 16000 keys: 139
-  // and 137.  (One launch whose blocks are shared out between both kinds: 99 and 159 us,
+  // and 136.  (One launch whose blocks are shared out between both kinds: 99 and 159 us,
   // with blocks that others' loads delay.)
   p.two = tree_tc_supported(a) && tree_tc_narrow(a, T) && !tree_tc_narrow(a, B * T);
   p.own = a;
