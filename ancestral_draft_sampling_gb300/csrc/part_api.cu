@@ -151,18 +151,18 @@ void fill_items(TreeArgs& a, const ItemLayout& L, char* ws) {
 }
 
 void plan(TreeArgs& a, int tokens) {
-  if (tree_tc_supported(a)) {
+  if (items_tc_supported(a)) {
     tree_tc_plan(a, tokens, sm_count());
     // in tiles: 4000 cycles of a narrow unit's end, of 1425 a tile of 64 dims and 2850
     // of 128; 8000 of 3470 for a pair of tiles of 256 rows
-    a.extra = !tree_tc_narrow(a, tokens) ? 2 : a.c.head_dim == 64 ? 3 : 1;
+    a.extra = !tree_tc_narrow(a, tokens) ? 2 : a.c.head_dim <= 64 ? 3 : 1;
   } else {
     tree_ffma_plan(a, tokens, sm_count());
   }
 }
 
 cudaError_t launch_items(const TreeArgs& a, cudaStream_t stream) {
-  return tree_tc_supported(a) ? launch_items_tc(a, stream) : launch_items_ffma(a, stream);
+  return items_tc_supported(a) ? launch_items_tc(a, stream) : launch_items_ffma(a, stream);
 }
 
 }  // namespace
@@ -318,7 +318,7 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
   // each kind 92; 64 x 8 tokens, 16 behind each of four prefixes of up to 16000 keys: 139
   // and 136.  (One launch whose blocks are shared out between both kinds: 99 and 159 us,
   // with blocks that others' loads delay.)
-  p.two = tree_tc_supported(a) && tree_tc_narrow(a, T) && !tree_tc_narrow(a, B * T);
+  p.two = items_tc_supported(a) && tree_tc_narrow(a, T) && !tree_tc_narrow(a, B * T);
   p.own = a;
   plan(a, B * T);
   a.item_count = p.two ? groups : groups + B;

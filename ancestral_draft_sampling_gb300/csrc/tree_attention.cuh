@@ -416,6 +416,8 @@ void tree_tc_plan(TreeArgs& a, int tokens, int sms);
 void tree_ffma_plan(TreeArgs& a, int tokens, int sms);
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_ffma(const TreeArgs& a, cudaStream_t stream);
+// The same over items, which may have heads of other sizes too.
+bool items_tc_supported(const TreeArgs& a);
 cudaError_t launch_items_tc(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_items_ffma(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeArgs& a, cudaStream_t stream);

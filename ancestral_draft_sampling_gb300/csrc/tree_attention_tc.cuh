@@ -1,5 +1,6 @@
 // tree_attention_tc.cuh -- attention of drafted tokens over the paged cache on
-// the 5th-generation tensor cores (tcgen05), bfloat16, head_dim 64 or 128.
+// the 5th-generation tensor cores (tcgen05), bfloat16, head_dim 64 or 128 (over
+// items: a multiple of 16 up to 128, in the form of the next larger one).
 //
 // For 128 rows (drafted tokens times query heads) and each tile of 128 keys:
 // S = Q K^T into tensor memory, weights P = 2^(c S - m) (c = scale log2 e)
@@ -671,6 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the next scores need not wait for the product of the weights
   constexpr bool apart = S::apart || kNarrow;
   constexpr bool kAside = kNarrow && kItems;
+  // of a head: items may have fewer than D, and what the copies fill in is 0
+  const int dim = kItems ? a.c.head_dim : D;
   static_assert(offsetof(Ctl, v_all) == 31 * 8 && offsetof(Ctl, o_free) == 37 * 8, "barriers");
   if (warp == 0) {
     uint64_t* bar = sh.k_full;
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *part_sums = nullptr, *part_stats = nullptr;
         if constexpr (kItems) {
           if (part) {
-            part_sums = w.whole ? tree_whole(a, w.kind, out_row) : tree_part(a, slot) + (size_t)lane * D;
+            part_sums = w.whole ? tree_whole(a, w.kind, out_row) : tree_part(a, slot) + (size_t)lane * dim;
             part_stats = w.whole ? tree_whole_stats(a, w.kind, out_row) : tree_part_stats(a, slot) + 2 * lane;
           }
         }
@@ -1005,9 +1008,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&sh.o_free[0]);
           }
           if (valid && !part) {
-            char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + 32 * i);
+            char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * dim + 32 * i);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+              if (32 * i + 16 * k >= dim) break;
               uint32_t p[8];
 #pragma unroll
               for (int d = 0; d < 8; ++d)
@@ -1022,6 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (valid) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+              if (32 * i + 8 * k >= dim) break;
               uint32_t p[8];
 #pragma unroll
               for (int d = 0; d < 8; ++d) p[d] = o[8 * k + d];
@@ -1373,7 +1378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // partial results: of a unit that other blocks have part of, and of kinds
           // that are joined row by row
           const bool part = !w.whole || (kItems && a.whole);
-          float* part_sums = part ? tree_part(a, slot) + (size_t)part_row * D : nullptr;
+          float* part_sums = part ? tree_part(a, slot) + (size_t)part_row * dim : nullptr;
           float* part_stats = part ? tree_part_stats(a, slot) + 2 * part_row : nullptr;
           if constexpr (kItems) {
             if (part && w.whole) {
@@ -1398,9 +1403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
             }
             if (valid && !part) {
-              char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + 32 * i);
+              char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.out) + out_row * dim + 32 * i);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
+                if (32 * i + 16 * k >= dim) break;
                 uint32_t p[8];
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
@@ -1417,6 +1423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float* to = part_sums + 32 * i;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
+                if (32 * i + 8 * k >= dim) break;
                 uint32_t p[8];
 #pragma unroll
                 for (int d = 0; d < 8; ++d) p[d] = o[8 * k + d];
@@ -1475,9 +1482,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   {
-    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)a.group, (cuuint64_t)a.c.kv_heads,
+    const cuuint64_t dims[5] = {(cuuint64_t)a.c.head_dim, (cuuint64_t)a.group, (cuuint64_t)a.c.kv_heads,
                                 (cuuint64_t)a.T * (kItems ? a.B : 1), (cuuint64_t)(kItems ? 1 : a.B)};
-    const cuuint64_t row = (cuuint64_t)D * 2;
+    const cuuint64_t row = (cuuint64_t)a.c.head_dim * 2;
     const cuuint64_t strides[4] = {row, row * a.group, row * a.heads, row * a.heads * dims[3]};
     const cuuint32_t box[5] = {64, (cuuint32_t)a.group, 1, (cuuint32_t)P.q_tokens, 1};
     if (encode(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(a.q), dims, strides,
@@ -1487,9 +1494,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   }
   for (int i = 0; i < 2; ++i) {
     char* base = static_cast<char*>(a.c.pool) + cache_row(a.c, 2 * a.layer + i, 0, 0, 0);
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.c.page_size,
+    const cuuint64_t dims[4] = {(cuuint64_t)a.c.head_dim, (cuuint64_t)a.c.page_size,
                                 (cuuint64_t)a.c.kv_heads, (cuuint64_t)a.c.num_pages};
-    const cuuint64_t row = (cuuint64_t)D * 2;
+    const cuuint64_t row = (cuuint64_t)a.c.head_dim * 2;
     const cuuint64_t strides[3] = {row, row * a.c.page_size, row * a.c.page_size * a.c.kv_heads};
     const cuuint32_t box[4] = {64, (cuuint32_t)P.page_rows, 1, 1};
     if (encode(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, ones,
@@ -1504,7 +1511,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
 template <bool kItems>
 cudaError_t launch_all(const TreeArgs& a, cudaStream_t stream) {
   const bool narrow = a.slot_rows <= kNarrowRows;
-  if (a.c.head_dim == 64)
+  if (a.c.head_dim <= 64)
     return narrow ? launch<64, true, kItems>(a, stream) : launch<64, false, kItems>(a, stream);
   return narrow ? launch<128, true, kItems>(a, stream) : launch<128, false, kItems>(a, stream);
 }

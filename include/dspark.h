@@ -709,7 +709,8 @@ DSPARK_API size_t dspark_sparse_workspace_bytes(const dspark_cache* cache, int B
  *                7).  Lists of tokens behind the last one are not read.
  * All else is as for dspark_tree_attention: q, mask, token_count, scale, out, lse,
  * what a token sees that sees nothing, the workspace, the roundings, the shapes
- * that run on the tensor cores, and the errors.  Keys and values that a token
+ * that run on the tensor cores (here with every head_dim up to 128 that is a
+ * multiple of 16), and the errors.  Keys and values that a token
  * does not see never reach its result, those of pages that only other tokens'
  * lists name among them.  count * T <= 2^24.  Three launches, graph capturable, no
  * synchronisation.
@@ -741,8 +742,9 @@ DSPARK_API size_t dspark_prefix_workspace_bytes(int B, int T, int heads,
  * attended by itself, as all rows are where group_start is no such list, and a
  * group's where its first row has fewer or does not hold them (error 12).  Results do
  * not depend on it where the pages hold the same tokens, but for the order of the
- * sums.  All else is as for dspark_tree_attention; partial results of both kinds
- * are float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no
+ * sums.  All else is as for dspark_tree_attention, and the shapes that run on the
+ * tensor cores are dspark_sparse_attention's; partial results of both kinds are
+ * float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no
  * synchronisation.
  */
 DSPARK_API dspark_status dspark_prefix_attention(

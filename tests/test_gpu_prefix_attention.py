@@ -102,7 +102,14 @@ SHAPES = [  # dtype, D, kv, group, T, groups, page, mask
     (BF, 128, 2, 7, 19, [(129, [511, 0, 90]), (127, [1, 2])], 256, "holes"),
     (BF, 128, 1, 1, 2, [(3000, [1, 2, 3, 4])], 16, "causal"),
     (BF, 128, 1, 2, 1, [(7, [0, 0])], 8, "causal"),
-    (BF, 96, 2, 3, 6, [(77, [0, 20]), (16, [1, 1])], 16, "tree"),   # FFMA: dim
+    (BF, 96, 2, 3, 6, [(77, [0, 20]), (16, [1, 1])], 16, "tree"),   # dims of the next larger form
+    (BF, 96, 1, 8, 61, [(320, [5, 0, 7]), (0, [9, 3]), (1000, [10, 300])], 32, "tree"),
+    (BF, 80, 2, 4, 1, [(960, [0, 40])], 64, "causal"),
+    (BF, 112, 2, 4, 8, [(256, [0, 1, 100]), (64, [500])], 64, "causal"),
+    (BF, 48, 4, 8, 1, [(512, list(range(0, 88)))], 16, "causal"),
+    (BF, 32, 2, 5, 7, [(112, [30, 0]), (16, [3] * 9)], 16, "full"),
+    (BF, 16, 1, 32, 9, [(200, [0, 70, 3])], 64, "holes"),
+    (BF, 72, 2, 3, 6, [(77, [0, 20]), (16, [1, 1])], 16, "tree"),   # FFMA: dim
     (BF, 128, 1, 4, 5, [(48, [50, 1, 0])], 12, "tree"),             # FFMA: page
     (BF, 256, 1, 2, 4, [(65, [0, 64])], 32, "causal"),
     (BF, 8, 1, 2, 3, [(10, [1, 2]), (33, [200])], 16, "tree"),
@@ -182,7 +189,8 @@ def test_special_values(cuda, dtype):
 
 # heads of each key head, tokens, members: units of few, 128 and 256 rows
 @pytest.mark.parametrize("D,kv,group,T,members", [(128, 8, 1, 8, 4), (64, 8, 1, 8, 4), (128, 8, 8, 6, 11), (64, 8, 8, 6, 11),
-                                                  (128, 2, 4, 32, 8), (64, 2, 4, 33, 8), (64, 8, 4, 1, 44)])
+                                                  (128, 2, 4, 32, 8), (64, 2, 4, 33, 8), (64, 8, 4, 1, 44),
+                                                  (96, 8, 1, 8, 4), (48, 8, 8, 6, 11), (80, 2, 4, 32, 8)])
 def test_units_that_follow_one_another(cuda, D, kv, group, T, members):
     """Prefixes and suffixes of one to several tiles behind one another in each
     block, with NaN in every place that holds no token."""

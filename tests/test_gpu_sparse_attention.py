@@ -88,7 +88,15 @@ SHAPES = [  # dtype, D, kv, group, T, lengths, page, mask, lists, width
     (BF, 128, 2, 3, 64, [500, 100], 8, "tree", None, 11),
     (BF, 64, 1, 1, 64, [1200], 512, "holes", 1, 2),
     (BF, 128, 1, 1, 2, [3000], 16, "causal", None, 40),
-    (BF, 96, 2, 3, 6, [177, 0], 16, "tree", None, 4),        # FFMA: dim
+    (BF, 96, 2, 3, 6, [177, 0], 16, "tree", None, 4),        # dims of the next larger form
+    (BF, 96, 1, 8, 61, [300, 0, 640], 32, "tree", 1, 7),
+    (BF, 96, 2, 5, 7, [30, 0, 1000], 16, "full", None, 20),
+    (BF, 80, 3, 1, 1, [0, 1, 127, 128, 129, 255], 8, "causal", None, 9),
+    (BF, 112, 2, 7, 19, [1111, 0, 90], 256, "holes", None, 3),
+    (BF, 48, 1, 32, 9, [200, 129], 64, "holes", None, 2),
+    (BF, 32, 4, 8, 1, [700, 3], 128, "causal", None, 2),
+    (BF, 16, 2, 3, 64, [500, 100], 8, "tree", None, 11),
+    (BF, 72, 2, 3, 6, [177, 0], 16, "tree", None, 4),        # FFMA: dim
     (BF, 128, 1, 4, 5, [50, 130], 12, "tree", None, 4),      # FFMA: page
     (BF, 256, 1, 2, 4, [165], 32, "causal", 1, 3),
     (BF, 8, 1, 2, 3, [10, 200], 16, "tree", None, 5),
@@ -124,7 +132,7 @@ def test_pages_that_no_list_names_are_not_read(cuda, dtype):
     s.check(*again)
 
 
-@pytest.mark.parametrize("dtype,D,group,T,page", [(BF, 128, 2, 6, 32), (BF, 128, 8, 9, 16), (BF, 64, 4, 50, 64),
+@pytest.mark.parametrize("dtype,D,group,T,page", [(BF, 96, 2, 6, 32), (BF, 48, 8, 40, 16), (BF, 128, 2, 6, 32), (BF, 128, 8, 9, 16), (BF, 64, 4, 50, 64),
                                                   (F32, 64, 2, 6, 16), (BF, 96, 2, 6, 16)])
 def test_special_values_reach_who_lists_them(cuda, dtype, D, group, T, page):
     """NaN and infinities in pages that some tokens list reach those and no
@@ -210,7 +218,8 @@ def test_long_lists_of_a_long_context(cuda, dtype, page):
 
 
 # head_dim, key heads, heads of each, tokens: 8, 48 and 192 rows
-FORMS = [(128, 8, 1, 8), (64, 8, 1, 8), (128, 8, 8, 6), (64, 8, 8, 6), (128, 8, 3, 64), (64, 8, 3, 64)]
+FORMS = [(128, 8, 1, 8), (64, 8, 1, 8), (128, 8, 8, 6), (64, 8, 8, 6), (128, 8, 3, 64), (64, 8, 3, 64),
+         (96, 8, 1, 8), (48, 8, 8, 6), (112, 8, 3, 64)]
 
 
 @pytest.mark.parametrize("D,kv,group,T", FORMS)
