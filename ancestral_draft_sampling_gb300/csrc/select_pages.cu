@@ -123,7 +123,8 @@ __device__ __forceinline__ void copy16(void* to, uint64_t from, bool there) {
                : "memory");
 }
 
-// On the tensor cores: bfloat16, head_dim D = 64 or 128.  An item is 128 pages of a
+// On the tensor cores: bfloat16, head_dim up to D = 64 or 128, filled up with zeros
+// (heads of 96, 88 x 8 lists of 8 heads and up to 250 pages: 35 us, 88 with the FFMA form's scores).  An item is 128 pages of a
 // sequence's key head, one row of 2 D bounds each; of the query rows up to N go with
 // them at a time, q- and q+ behind one another: S [page][row] = (lo | hi) (q- | q+)^T into tensor memory, as kSums sums of
 // D / 2 terms each.  A thread then has a page, takes the largest score of each token's
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   uint8_t* const A = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* const B = A + 2 * kBytes;
   Control& sh = *reinterpret_cast<Control*>(B + 2 * N * 4 * D);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = a.c.head_dim;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.a_full[i], 4);
@@ -242,6 +243,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     // ---------------------------------------------------------------- bounds
     constexpr int kTogether = 32 / kWords;  // rows at a time
     const int part = lane / kWords, w = lane - part * kWords, row0 = (warp - 8) * 32;
+    // the word of a row in memory, where dims may be fewer than D, or zeros
+    const int side = w / (D / 8), word = side * (dim / 8) + w - side * (D / 8);
+    const bool filled = w - side * (D / 8) < dim / 8;
     // where the rows of an item lie, one a lane (0: nowhere)
     auto rows_of = [&](int i) -> uint64_t {
       if (i >= items) return 0;
@@ -276,8 +280,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll 4
       for (int r = 0; r < 32; r += kTogether) {
         const uint64_t row = __shfl_sync(0xffffffffu, from, r + part);
-        copy16(to + r * 128 + (((w & 7) ^ ((r + part) & 7)) << 4), (row ? row : reinterpret_cast<uint64_t>(a.bounds)) + 16 * w,
-               row != 0);
+        const bool some = row != 0 && filled;
+        copy16(to + r * 128 + (((w & 7) ^ ((r + part) & 7)) << 4),
+               some ? row + 16 * word : reinterpret_cast<uint64_t>(a.bounds), some);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       at.step();
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       for (int t0 = 0; t0 < x.tokens; t0 += fit) {
         const int tokens = x.tokens - t0 < fit ? x.tokens - t0 : fit, rows = tokens * a.group;
         const char* const from =
-            a.q + (((size_t)x.b * a.T + t0) * a.heads + (size_t)x.h * a.group) * D * 2 + 16 * w;
+            a.q + (((size_t)x.b * a.T + t0) * a.heads + (size_t)x.h * a.group) * dim * 2 + 16 * w;
         uint8_t* const to = B + at.i * (N * 4 * D) + (w >> 3) * (N * 128);
         uint4 q[4];
         auto load = [&](int r0) {
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           for (int k = 0; k < 4; ++k) {
             const int r = r0 + k * kStep + row0, t = r / a.group;
             q[k] = make_uint4(0, 0, 0, 0);
-            if (r < rows)
-              q[k] = *reinterpret_cast<const uint4*>(from + ((size_t)t * a.heads + (r - t * a.group)) * D * 2);
+            if (r < rows && w < dim / 8)
+              q[k] = *reinterpret_cast<const uint4*>(from + ((size_t)t * a.heads + (r - t * a.group)) * dim * 2);
           }
         };
         load(0);
@@ -1145,9 +1150,10 @@ cudaError_t launch_select_pages(const SelectArgs& args, int sms, cudaStream_t st
   SelectArgs a = args;
   const int D = a.c.head_dim;
   const bool bf16 = a.c.dtype == DSPARK_BF16;
-  const bool tc = bf16 && (D == 64 || D == 128);
-  a.error = (tc ? 2 * (17 * (D / 8 / kSums) + kSums) : D / 4 + 4) * 0x1p-24f;
-  const cudaError_t e = tc      ? (D == 64 ? launch_score_tc<64>(a, sms, stream) : launch_score_tc<128>(a, sms, stream))
+  const bool tc = bf16 && D <= 128;
+  const int terms = D <= 64 ? 64 : 128;
+  a.error = (tc ? 2 * (17 * (terms / 8 / kSums) + kSums) : D / 4 + 4) * 0x1p-24f;
+  const cudaError_t e = tc      ? (D <= 64 ? launch_score_tc<64>(a, sms, stream) : launch_score_tc<128>(a, sms, stream))
                         : bf16 ? launch_score_ffma<__nv_bfloat16>(a, sms, stream)
                                : launch_score_ffma<float>(a, sms, stream);
   if (e != cudaSuccess) return e;

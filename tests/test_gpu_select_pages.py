@@ -132,7 +132,12 @@ SHAPES = [  # dtype, D, kv, group, T, lengths, page, count, first, last, shared
     (BF, 128, 1, 8, 61, [1000, 0, 300], 32, 7, 0, 0, True),
     (BF, 128, 2, 8, 64, [650], 32, 5, 1, 0, False),
     (BF, 256, 1, 2, 2, [400], 16, 6, 0, 0, False),
-    (BF, 72, 2, 5, 3, [300, 170], 16, 4, 1, 1, False),   # FFMA: dim
+    (BF, 72, 2, 5, 3, [300, 170], 16, 4, 1, 1, False),   # dims of the next larger form
+    (BF, 96, 3, 4, 8, [2000, 63, 1111], 16, 20, 1, 1, False),
+    (BF, 120, 1, 8, 61, [1000, 0, 300], 32, 7, 0, 0, True),
+    (BF, 40, 2, 3, 5, [900, 100], 8, 33, 0, 0, False),
+    (BF, 8, 2, 8, 64, [650], 32, 5, 1, 0, False),
+    (BF, 136, 2, 5, 3, [300, 170], 16, 4, 1, 1, False),  # FFMA: dim
     (F32, 64, 2, 3, 7, [500, 777], 16, 12, 0, 0, False),
     (F32, 128, 1, 8, 9, [300], 4, 31, 3, 3, True),
     (F32, 40, 1, 32, 3, [70], 1, 10, 0, 0, False),
