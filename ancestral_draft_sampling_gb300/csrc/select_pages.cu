@@ -143,7 +143,10 @@ constexpr int kSums = 4, kScorePages = 128, kScoreThreads = 544;
 constexpr int kMaxB = DSPARK_CACHE_MAX_B;
 
 struct Control {
-  uint64_t a_full[2], a_empty[2], b_full[2], b_empty[2], t_full[2], t_empty[2];
+  uint64_t a_full[2], a_empty[2], b_full[2], b_empty[2], t_empty[2];
+  // scores are there, of each team: a wait is for a phase's parity, so nobody may wait
+  // on a barrier some of whose phases it has passed over
+  uint64_t t_full[2][2];
   uint32_t tmem;
   int failed;
   float sum_q[64];
@@ -195,7 +198,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       mbar_init(&sh.a_empty[i], 5);
       mbar_init(&sh.b_full[i], 4);
       mbar_init(&sh.b_empty[i], 1);
-      mbar_init(&sh.t_full[i], 1);
+      mbar_init(&sh.t_full[0][i], 1);
+      mbar_init(&sh.t_full[1][i], 1);
       mbar_init(&sh.t_empty[i], 4);
     }
     sh.failed = 0;
@@ -367,12 +371,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const uint32_t idesc = idesc_bf16_f32(kScorePages, N, 0, 0);
     const uint64_t da0 = smem_desc_sw128(smem_u32(A), 16, 1024), db0 = smem_desc_sw128(smem_u32(B), 16, 1024);
     Slot as{0, 0}, bs{0, 0}, ts{0, 1};
+    int turn = 0;  // the team that takes the item
 #pragma unroll 1
-    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+    for (int i = blockIdx.x; i < items && ok; i += gridDim.x, turn ^= 1) {
       const Item x = item(i);
       ok = wait_warp(&sh.a_full[as.i], as.parity);
       // failure-path test: bounds are there, and nothing completes this phase
-      if (stall) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.t_full[0], 0, kStallPolls));
+      if (stall) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.t_full[0][0], 0, kStallPolls));
 #pragma unroll 1
       for (int t0 = 0; t0 < x.tokens && ok; t0 += fit) {
         ok = wait_warp(&sh.b_full[bs.i], bs.parity) && wait_warp(&sh.t_empty[ts.i], ts.parity);
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             mma_bf16(to + (k / kEach) * N, da + (((k >> 2) * (kScorePages * 128) + (k & 3) * 32) >> 4),
                      db + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc, k % kEach != 0);
           }
-          mma_commit(&sh.t_full[ts.i]);
+          mma_commit(&sh.t_full[turn][ts.i]);
           mma_commit(&sh.b_empty[bs.i]);
           if (t0 + fit >= x.tokens) mma_commit(&sh.a_empty[as.i]);
         }
@@ -399,7 +404,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- scores
-    Slot as{0, 0}, ts{0, 0};
+    Slot as{0, 0};
+    int slot = 0;         // of the next tile's scores
+    uint32_t phases = 0;  // bit i: the parity of this team's next phase in slot i
     const int team = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const bool together = a.lists == 1;
     const size_t list_step = (size_t)a.c.kv_heads * a.stride;
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const Item x = item(i);
       if (turn != team) {  // the other four warps'
         as.step();
-        for (int t0 = 0; t0 < x.tokens; t0 += fit) ts.step();
+        for (int t0 = 0; t0 < x.tokens; t0 += fit) slot ^= 1;
         continue;
       }
       const int page = x.page0 + row;
@@ -441,10 +448,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll 1
       for (int t0 = 0; t0 < x.tokens; t0 += fit) {
         const int tokens = x.tokens - t0 < fit ? x.tokens - t0 : fit, rows = tokens * a.group;
-        ok = wait_warp(&sh.t_full[ts.i], ts.parity);
+        ok = wait_warp(&sh.t_full[team][slot], (phases >> slot) & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t from = tmem + ts.i * kSums * N + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t from = tmem + slot * kSums * N + ((uint32_t)(quarter * 32) << 16);
         float best = -INFINITY;
         int left = a.group;  // rows of the token
 #pragma unroll 1
@@ -476,8 +483,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.t_empty[ts.i]);
-        ts.step();
+        if (lane == 0) mbar_arrive(&sh.t_empty[slot]);
+        phases ^= 1u << slot;
+        slot ^= 1;
       }
       if (together && there) *at = run;
     }

@@ -276,3 +276,22 @@ def test_a_wait_that_runs_out_is_reported(cuda, monkeypatch, D, group, T):
     monkeypatch.delenv("DSPARK_TEST_STALL_WAIT")
     assert torch.equal(dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws), want)
     assert dspark.read_device_error(s.c) == 0
+
+
+# rows of more than one tile of products (64), and more items (128 pages of a key
+# head) than the GPU has multiprocessors, so that a block goes through several
+@pytest.mark.parametrize("D,kv,group,T,B,shared", [(64, 4, 8, 20, 44, False), (128, 4, 5, 17, 30, True), (96, 2, 32, 5, 70, False),
+                                                   (128, 8, 8, 61, 15, True), (64, 3, 7, 64, 40, True)])
+def test_items_that_follow_one_another(cuda, D, kv, group, T, B, shared):
+    rng = np.random.default_rng(D + T)
+    length = [int(x) for x in rng.integers(100, 900, B)]
+    length[B // 2], length[0] = 0, 1300
+    count = [T] + [int(x) for x in rng.integers(0, T + 1, B - 1)]
+    s = Case(BF, D, kv, group, T, length, 2, count=count, seed=T)
+    assert sum(-(-(n // 2) // 128) for n, t in zip(length, count) if t and n // 2 > 9) * kv > 160 and T * group > 64
+    bounds = s.bounds()
+    got = dspark.select_pages(s.c, 1, bounds, s.q, ints(length), 9, first=1, shared=shared, token_count=ints(count))
+    s.check(bounds, got, 9, 1, 0, shared)
+    for _ in range(5):
+        again = dspark.select_pages(s.c, 1, bounds, s.q, ints(length), 9, first=1, shared=shared, token_count=ints(count))
+        assert torch.equal(got, again)
