@@ -41,10 +41,15 @@ inline int sm_count() {
 // block's: the second phase of the barrier of u, once u is ready), so that the
 // wait runs out, the kernel records kDevErrTimeout and takes its abort path.
 constexpr uint32_t kStallPolls = 1u << 12;
-inline bool stall_first_wait_requested() {
+// =2: the second stream's warps of the attention over items with few rows come late to
+// every unit's end, by kLateNs.  No wait runs out.
+constexpr int kStallWait = 1, kStallLate = 2;
+constexpr unsigned kLateNs = 50000;
+inline int stall_requested() {
   const char* env = std::getenv("DSPARK_TEST_STALL_WAIT");
-  return env != nullptr && env[0] == '1';
+  return env != nullptr && env[0] >= '1' && env[0] <= '9' ? env[0] - '0' : 0;
 }
+inline bool stall_first_wait_requested() { return stall_requested() == kStallWait; }
 
 inline dspark_status from_cuda(cudaError_t e) {
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;

@@ -138,11 +138,12 @@ struct Control {  // shared memory behind the tiles
   uint64_t s_full[2], pv_done[2];  // of each stream
   uint64_t v_all, b_done;
   uint64_t p_ready[2], v_sync[2];  // of each stream
-  // sums have been read: by the first stream at the end of every unit (both
-  // streams' where it joins them), by the second where it has rows of its own.
-  // Nobody arrives without work in the unit, so no phase is run ahead of.  The
-  // products wait for them, and so does the second stream before it adds to its
-  // sums by hand: a unit's first scores are there before the last unit's sums
+  // sums have been read: by the first stream (narrow units of items: by warp 0) at
+  // the end of every unit, both streams' where it joins them, and by the second where
+  // it has rows of its own.  Nobody arrives or waits at a unit's end without work in
+  // the unit, so no phase is run ahead of and none is passed over.  The products wait
+  // for them, and so does a stream before it adds to its sums by hand where another
+  // warp reads them: a unit's first scores are there before the last unit's sums
   // have been read.
   uint64_t o_free[2];
   uint64_t e_full[2];  // of each stream, for warp 0: a narrow unit's maxima and sums are there
@@ -312,7 +313,7 @@ struct TcArgs {
   int page_shift;        // log2 of the page size
   int out32;             // out is aligned to 32 bytes
   int narrow;            // at most 32 rows a unit: the kernel's other form
-  int stall;             // failure-path test: the product warp's wait runs out
+  int stall;             // tests: a wait that runs out, a stream that is late
 };
 
 // A role's place in a ring: the slot, and the parity of its phase.
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       halved += both;
       // failure-path test: scores are on their way, and nothing completes this
       // phase but the abort path itself
-      if (P.stall) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.drain, 0, kStallPolls));
+      if (P.stall == kStallWait) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.drain, 0, kStallPolls));
       if (both && !apart) {  // bound by the products: as little as can be between them
 #pragma unroll 1
         for (int i = 0; i < w.n && ok; ++i) {
@@ -1321,11 +1322,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (some) look_at(next);
       if constexpr (kAside) {
-        // warp 0 has begun with the last unit: its barriers are waited for by parity, so
-        // no phase may be run ahead of (this unit's first sums wait for the same)
-        if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
-        if (!ok) break;
+        if (P.stall == kStallLate && st == 1) __nanosleep(kLateNs);
         if (worked) {
+          // Not before warp 0 has read what the last unit left.  The wait goes by parity:
+          // the phase before that one is over, since the last unit's products waited for
+          // it, and this unit's is not, since warp 0 waits for this stream first.  A
+          // stream without work in the unit must not wait: warp 0 does not wait for it
+          // and could be a phase further on.
+          if (unit > 0) ok = wait_warp(&sh.o_free[0], (unit - 1) & 1);
+          if (!ok) break;
           if (quarter == 0) nar.end_top[unit & 1][st][lane] = m;
           nar.end_sum[unit & 1][st][quarter][lane] = l;
           __syncwarp();
@@ -1472,7 +1477,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   P.q_tokens = a.most < P.fit ? a.most : P.fit;
   P.q_tiles = a.most > P.fit ? 2 : 1;
   P.narrow = kNarrow;
-  P.stall = stall_first_wait_requested();
+  P.stall = stall_requested();
   const int slots = Shape<D>::tiles - P.q_tiles -
                     (kNarrow ? (int)sizeof(Narrow) / Shape<D>::tile_bytes : 0);
   P.v_slots = slots / 2;

@@ -360,3 +360,27 @@ def test_a_wait_that_runs_out_is_reported(cuda, monkeypatch, D, group, T):
     s.run(**a)
     assert torch.equal(a["out"], want[0]) and torch.equal(a["lse"], want[1])
     assert dspark.read_device_error(s.c) == 0
+
+
+@pytest.mark.parametrize("D,kv,group,T", [(64, 8, 4, 1), (128, 8, 2, 3), (96, 4, 8, 4)])
+def test_a_stream_that_is_late(cuda, monkeypatch, D, kv, group, T):
+    """Units of one tile leave the second stream without work.  With
+    DSPARK_TEST_STALL_WAIT=2 its warps come to each unit's end long after the
+    others: the same results, and no wait runs out."""
+    rng = np.random.default_rng(D)
+    length = [int(n) for n in rng.integers(0, 120, 240)]
+    for b in range(0, 240, 9):  # and some units of two to four tiles
+        length[b] = int(rng.integers(130, 400))
+    s = Sparse(BF, D, kv, group, T, length, 16, "causal", width=24, seed=D)
+    a = dict(out=torch.zeros_like(s.q), lse=torch.zeros(240, T, kv * group, device="cuda"),
+             workspace=dspark.SparseWorkspace(s.c, 240, T, kv * group, 24))
+    s.run(**a)
+    s.check(a["out"], a["lse"])
+    want = [a["out"].clone(), a["lse"].clone()]
+    monkeypatch.setenv("DSPARK_TEST_STALL_WAIT", "2")
+    for _ in range(3):
+        a["out"].zero_()
+        s.run(**a)
+        torch.cuda.synchronize()
+        assert dspark.read_device_error(s.c) == 0
+        assert torch.equal(a["out"], want[0]) and torch.equal(a["lse"], want[1])
