@@ -43,7 +43,9 @@ inline int sm_count() {
 constexpr uint32_t kStallPolls = 1u << 12;
 // =2: the second stream's warps of the attention over items with few rows come late to
 // every unit's end, by kLateNs.  No wait runs out.
-constexpr int kStallWait = 1, kStallLate = 2;
+// =3: one of the selection's warps that load queries has given up; the others' waits
+// run out.
+constexpr int kStallWait = 1, kStallLate = 2, kStallAlone = 3;
 constexpr unsigned kLateNs = 50000;
 inline int stall_requested() {
   const char* env = std::getenv("DSPARK_TEST_STALL_WAIT");

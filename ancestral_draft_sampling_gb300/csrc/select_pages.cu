@@ -147,9 +147,10 @@ struct Control {
   // scores are there, of each team: a wait is for a phase's parity, so nobody may wait
   // on a barrier some of whose phases it has passed over
   uint64_t t_full[2][2];
+  uint64_t drain;   // all products are done
   uint32_t tmem;
   int failed;
-  float sum_q[64];
+  float sum_q[2][64];  // of a row tile's rows, and of the one with sums before it
   uint32_t named[2][4];  // the rows of both slots that are pages
   int warps[33];
   int offset[kMaxB + 1];  // items of the sequences before
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       mbar_init(&sh.t_full[1][i], 1);
       mbar_init(&sh.t_empty[i], 4);
     }
+    mbar_init(&sh.drain, 1);
     sh.failed = 0;
     fence_mbar_init();
   }
@@ -304,6 +306,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     constexpr int kStep = 4 * kTogether;                          // rows of four warps
     const int part = lane / kLanes, w = lane - part * kLanes, row0 = (warp - 12) * kTogether + part;
     Slot at{0, 1};
+    int turn = 0;
+    // failure-path test: one of them has given up
+    if (stall == kStallAlone && warp == 13) ok = false;
 #pragma unroll 1
     for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
       const Item x = item(i);
@@ -313,6 +318,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         const char* const from =
             a.q + (((size_t)x.b * a.T + t0) * a.heads + (size_t)x.h * a.group) * dim * 2 + 16 * w;
         uint8_t* const to = B + at.i * (N * 4 * D) + (w >> 3) * (N * 128);
+        float* const sums = sh.sum_q[turn];
         uint4 q[4];
         auto load = [&](int r0) {
 #pragma unroll
@@ -347,23 +353,27 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                 s += fabsf(__uint_as_float(u[n] << 16)) + fabsf(__uint_as_float(u[n] & 0xffff0000u));
 #pragma unroll
               for (int n = kLanes / 2; n > 0; n >>= 1) s += __shfl_xor_sync(0xffffffffu, s, n);
-              if (w == 0 && r < rows) sh.sum_q[r] = s;
+              if (w == 0 && r < rows) sums[r] = s;
             }
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.b_full[at.i]);
-        at.step();
         if (x.page0 == 0) {  // the largest sum of each token's heads
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          // the four warps' sums are there (and the other ones used up); a warp that has
+          // given up does not come, and the wait for it runs out
+          ok = wait_warp(&sh.b_full[at.i], at.parity ^ 1);
+          turn ^= 1;
+          if (!ok) break;
           for (int t = threadIdx.x - 12 * 32; t < tokens; t += 128) {
             float best = 0.0f;
-            for (int g = 0; g < a.group; ++g) best = max_nan(best, sh.sum_q[t * a.group + g]);
+            for (int g = 0; g < a.group; ++g) best = max_nan(best, sums[t * a.group + g]);
             a.reach_q[((size_t)x.b * a.T + t0 + t) * a.c.kv_heads + x.h] = best;
           }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          __syncwarp();
         }
+        at.step();
       }
     }
   } else if (warp == 16) {
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const Item x = item(i);
       ok = wait_warp(&sh.a_full[as.i], as.parity);
       // failure-path test: bounds are there, and nothing completes this phase
-      if (stall) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.t_full[0][0], 0, kStallPolls));
+      if (stall == kStallWait) ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.t_full[0][0], 0, kStallPolls));
 #pragma unroll 1
       for (int t0 = 0; t0 < x.tokens && ok; t0 += fit) {
         ok = wait_warp(&sh.b_full[bs.i], bs.parity) && wait_warp(&sh.t_empty[ts.i], ts.parity);
@@ -402,6 +412,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       as.step();
     }
+    // tensor memory is given back behind the last of them
+    if (elect_one()) mma_commit(&sh.drain);
+    wait_warp(&sh.drain, 0);
   } else {
     // ---------------------------------------------------------------- scores
     Slot as{0, 0};
@@ -1139,7 +1152,7 @@ cudaError_t launch_score_tc(const SelectArgs& a, int sms, cudaStream_t stream) {
       cudaFuncSetAttribute(score_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   return launch_behind(score_tc_kernel<D>, sms, kScoreThreads, bytes, stream, a, N,
-                       (int)stall_first_wait_requested());
+                       stall_requested());
 }
 
 template <typename T>

@@ -295,3 +295,20 @@ def test_items_that_follow_one_another(cuda, D, kv, group, T, B, shared):
     for _ in range(5):
         again = dspark.select_pages(s.c, 1, bounds, s.q, ints(length), 9, first=1, shared=shared, token_count=ints(count))
         assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("D,group,T", [(128, 4, 8), (64, 8, 20)])
+def test_a_warp_that_gives_up_alone(cuda, monkeypatch, D, group, T):
+    """DSPARK_TEST_STALL_WAIT=3: one of the four warps that load queries has given
+    up, the other three have not.  Their waits for it run out: error 2, a clean
+    return, and a cache that the next call can use."""
+    s = Case(BF, D, 2, group, T, [3000, 0, 700], 16, seed=T)
+    bounds, ws = s.bounds(), dspark.SelectWorkspace(s.c, 3, T)
+    want = dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws)
+    monkeypatch.setenv("DSPARK_TEST_STALL_WAIT", "3")
+    dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws)
+    torch.cuda.synchronize()
+    assert dspark.read_device_error(s.c) == 2 and dspark.read_device_error(s.c) == 0
+    monkeypatch.delenv("DSPARK_TEST_STALL_WAIT")
+    assert torch.equal(dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws), want)
+    assert dspark.read_device_error(s.c) == 0
