@@ -864,7 +864,7 @@ __device__ __noinline__ uint64_t exact_scores(const SelectArgs& a, const List& l
 }
 
 // Writes one list: `scores` of the sequence's F > count pages, sums of terms whose
-// sizes add up to size_of() at most; border: room for F numbers.  A
+// sizes add up to size_of() at most (0 only where all scores are); border: room for F numbers.  A
 // thread holds the first R of its scores as bits whose order is theirs (read anew from
 // memory and made each time they took a third of the time).
 template <typename T, int W, int R, typename Size>
@@ -873,8 +873,8 @@ __device__ __forceinline__ void pick_list(const SelectArgs& a, const List& l, co
   constexpr int kSize = 32 * W;
   const int tid = team.thread, lane = tid & 31, F = l.seq.F;
   const int lo = a.first, hi = F - a.last, want = a.count - a.first - a.last;
-  // 0 (below every score's) where there is no candidate
-  auto key_of = [&](int j) { return j >= lo && j < hi ? ordered_bits(scores[j]) : 0u; };
+  // 0 (below every score's) where there is no candidate; -0 is 0
+  auto key_of = [&](int j) { return j >= lo && j < hi ? ordered_bits(scores[j] + 0.0f) : 0u; };
   uint32_t held[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) held[i] = key_of(i * kSize + tid);
@@ -922,9 +922,12 @@ __device__ __forceinline__ void pick_list(const SelectArgs& a, const List& l, co
     below = split ? team.most(below) : edge;
     const float last = from_ordered_bits(edge);
     const float eps = a.error * size;
-    if (!(last - from_ordered_bits(below) > 2.0f * eps)) {
+    // eps grows with the terms, and below 2^-126 float32 rounds by a fixed step, or
+    // drops a term whole: of sums that small nothing is known
+    const bool small = size > 0.0f && size < 0x1p-90f;
+    if (small || !(last - from_ordered_bits(below) > 2.0f * eps)) {
       // scores within 2 eps of the last one that is taken could change places
-      const bool known = size <= 0x1p100f && fabsf(last) <= 0x1p101f;
+      const bool known = !small && size <= 0x1p100f && fabsf(last) <= 0x1p101f;
       // sums below 2^22; a product that float32 cannot hold whole is far below 2^-32
       const float scale = size == 0.0f ? 1.0f
                           : known && size >= 0x1p-60f ? __int_as_float((127 + 21 - ilogbf(size)) << 23) : 0.0f;
@@ -1070,8 +1073,8 @@ __device__ __forceinline__ void pick_list(const SelectArgs& a, const List& l, co
   }
 }
 
-// The largest of n numbers times the largest of m, by a warp; NaN if one is.  All
-// loads are under way before the first is used.
+// The largest of n numbers times the largest of m, by a warp; NaN if one is, and 0 only
+// if all n or all m are.  All loads are under way before the first is used.
 __device__ __forceinline__ float largest_product(const float* x, int n, size_t step_x, const float* y, int m,
                                                  int lane) {
   float u = 0.0f, v[8];
@@ -1087,7 +1090,8 @@ __device__ __forceinline__ float largest_product(const float* x, int n, size_t s
     u = max_nan(u, __shfl_xor_sync(0xffffffffu, u, i));
     v[0] = max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], i));
   }
-  return u * v[0];
+  const float size = u * v[0];
+  return size < 0x1p-126f && u > 0.0f && v[0] > 0.0f ? 0x1p-126f : size;
 }
 
 // ----------------------------------------------------------------- kernels

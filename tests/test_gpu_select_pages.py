@@ -312,3 +312,39 @@ def test_a_warp_that_gives_up_alone(cuda, monkeypatch, D, group, T):
     monkeypatch.delenv("DSPARK_TEST_STALL_WAIT")
     assert torch.equal(dspark.select_pages(s.c, 1, bounds, s.q, ints(s.length), 9, workspace=ws), want)
     assert dspark.read_device_error(s.c) == 0
+
+
+# powers of two that queries and bounds are multiplied by: scores that float32 rounds by
+# a fixed step, cannot hold at all, or can though one of the two is below its normal numbers
+@pytest.mark.parametrize("forms", ["few lists", "many lists"])
+@pytest.mark.parametrize("powers", [(-70, -75), (-65, -66), (-60, -64), (-45, -50), (-40, -40), (-30, -32), (-140, 0), (0, -140),
+                                    (-140, 55), (60, -140), (-140, -20)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_scores(cuda, dtype, powers, forms):
+    """The choice is that of exact scores whatever their size."""
+    few = forms == "few lists"
+    s = Case(dtype, 64, 2 if few else 4, 2, 2 if few else 4, [1600, 900] if few else [900] * 40, 16, seed=8)
+    length = ints(s.length)
+    bounds = s.bounds()
+    bounds = torch.where(torch.isnan(bounds), 0.0, bounds)
+    for_q, for_bounds = (max(p, -131) if dtype is BF else p for p in powers)  # its least number is 2^-133
+    s.q = (s.q.double() * 2.0 ** for_q).to(dtype)
+    bounds = (bounds.double() * 2.0 ** for_bounds).to(dtype)
+    assert (s.q != 0).any() and (bounds != 0).any()
+    for count in (1, 7, 50):
+        s.check(bounds, dspark.select_pages(s.c, 1, bounds, s.q, length, count), count)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scores_that_are_zero_are_equal(cuda, dtype):
+    """Zero queries or bounds of either sign: the lowest pages."""
+    s = Case(dtype, 64, 1, 2, 1, [800], 16, seed=8)
+    bounds = s.bounds()
+    ids = s.c.block_table[0, :50].long()
+    q = s.q
+    for zero in (0.0, -0.0):
+        s.check(bounds, dspark.select_pages(s.c, 1, bounds, q * zero, ints([800]), 7), 7, q=q * 0.0)
+        some = bounds.clone()
+        some[1, ids] = zero
+        some[1, ids[::3]] = 0.0
+        s.check(some, dspark.select_pages(s.c, 1, some, q, ints([800]), 7), 7)
