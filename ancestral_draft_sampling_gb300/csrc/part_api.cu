@@ -50,6 +50,12 @@ dspark_status attention_sizes(int B, int T, int heads, int kv_heads, int D) {
   return DSPARK_OK;
 }
 
+dspark_status prefix_sizes(int B, int T, int heads, int kv_heads, int D) {
+  const dspark_status st = attention_sizes(B, T, heads, kv_heads, D);
+  // rows of results are counted in 32 bits
+  return st == DSPARK_OK && (long long)B * T * heads >= (1LL << 31) ? DSPARK_ERR_UNSUPPORTED : st;
+}
+
 // What the attention needs for units of up to `tokens` tokens, `items` of them:
 // the merge's work, partial results (two a block), the items and their work.
 struct ItemLayout {
@@ -282,7 +288,7 @@ dspark_status dspark_sparse_attention(const dspark_cache* cache, int layer, cons
 }
 
 size_t dspark_prefix_workspace_bytes(int B, int T, int heads, int kv_heads, int head_dim) {
-  if (attention_sizes(B, T, heads, kv_heads, head_dim) != DSPARK_OK) return 0;
+  if (prefix_sizes(B, T, heads, kv_heads, head_dim) != DSPARK_OK) return 0;
   return prefix_layout(B, T, heads, kv_heads, head_dim).total;
 }
 
@@ -294,12 +300,13 @@ dspark_status dspark_prefix_attention(const dspark_cache* cache, int layer, cons
                                       size_t workspace_bytes, cudaStream_t stream) {
   PrefixArgs p{};
   TreeArgs& a = p.shared;
-  const dspark_status st = fill_attention(a, cache, layer, seq, length, token_count, q, mask,
-                                          mask_stride, scale, B, T, heads, out, lse);
+  dspark_status st = fill_attention(a, cache, layer, seq, length, token_count, q, mask,
+                                    mask_stride, scale, B, T, heads, out, lse);
   if (st != DSPARK_OK) return st;
   if (!group_start || !prefix || !is4(group_start) || !is4(prefix) || groups <= 0 || groups > B)
     return DSPARK_ERR_INVALID_ARG;
-  if ((long long)B * T * heads >= (1LL << 31)) return DSPARK_ERR_UNSUPPORTED;
+  st = prefix_sizes(B, T, heads, cache->kv_heads, cache->head_dim);
+  if (st != DSPARK_OK) return st;
   const PrefixLayout L = prefix_layout(B, T, heads, cache->kv_heads, cache->head_dim);
   if (!workspace || workspace_bytes < L.total || !aligned_to(workspace, 256))
     return DSPARK_ERR_WORKSPACE;

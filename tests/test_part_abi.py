@@ -167,3 +167,12 @@ def test_python_refuses_tensors_that_do_not_fit(lib):
     for bad in ((start.long(), one), (start[:1], one), (start, one.long()), (start, start), (start[None], one)):
         with pytest.raises((TypeError, ValueError)):
             dspark.prefix_attention(c, 0, q, one, *bad)
+
+
+def test_prefix_workspace_bytes_goes_by_the_calls_limits(lib):
+    """B * T * heads < 2^31, in the size as in the call."""
+    f = lib.dspark_prefix_workspace_bytes
+    assert f(1024, 64, 32768, 1024, 8) == 0
+    assert f(1023, 64, 32768, 1024, 8) > 0
+    c = ctypes.byref(struct(kv_heads=1024, head_dim=8, max_seqs=1))
+    assert attention(lib, "prefix", c=c, B=1024, T=64, heads=32768, bytes=1 << 62, out=FAKE + (1 << 50)) == UNSUPPORTED
