@@ -1151,22 +1151,21 @@ dim3 score_grid(const SelectArgs& a, int pages, int sms) {
 template <int D>
 cudaError_t launch_score_tc(const SelectArgs& a, int sms, cudaStream_t stream) {
   const int rows = a.T * a.group, N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  const size_t bytes = score_tc_bytes<D>(N);
-  const cudaError_t e =
-      cudaFuncSetAttribute(score_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  // the limit is the kernel's, of all sizes: another thread may set it before the launch
+  const cudaError_t e = cudaFuncSetAttribute(score_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)score_tc_bytes<D>(64));
   if (e != cudaSuccess) return e;
-  return launch_behind(score_tc_kernel<D>, sms, kScoreThreads, bytes, stream, a, N,
+  return launch_behind(score_tc_kernel<D>, sms, kScoreThreads, score_tc_bytes<D>(N), stream, a, N,
                        stall_requested());
 }
 
 template <typename T>
 cudaError_t launch_score_ffma(const SelectArgs& a, int sms, cudaStream_t stream) {
-  const int bytes = score_ffma_bytes<T>(a.c.head_dim);
-  const cudaError_t e =
-      cudaFuncSetAttribute(score_ffma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = cudaFuncSetAttribute(score_ffma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             score_ffma_bytes<T>(256));  // likewise
   if (e != cudaSuccess) return e;
-  return launch_behind(score_ffma_kernel<T>, score_grid(a, kScoreWarps * kReachPages, sms), 32 * kScoreWarps, bytes,
-                       stream, a);
+  return launch_behind(score_ffma_kernel<T>, score_grid(a, kScoreWarps * kReachPages, sms), 32 * kScoreWarps,
+                       score_ffma_bytes<T>(a.c.head_dim), stream, a);
 }
 
 }  // namespace

@@ -1,5 +1,7 @@
 """The bounds of pages and the pages that they select, against 64 bits."""
 import math
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -348,3 +350,38 @@ def test_scores_that_are_zero_are_equal(cuda, dtype):
         some[1, ids] = zero
         some[1, ids[::3]] = 0.0
         s.check(some, dspark.select_pages(s.c, 1, some, q, ints([800]), 7), 7)
+
+
+# (dims, tokens) of two threads' calls: forms of one kernel with different shared memory
+@pytest.mark.parametrize("dtype,sizes", [(BF, [(128, 16), (128, 1)]), (BF, [(64, 16), (64, 1)]), (BF, [(256, 3), (136, 3)]),
+                                         (F32, [(256, 2), (40, 2)])])
+def test_calls_from_two_threads(cuda, dtype, sizes):
+    """Each with a cache, a workspace and a stream of its own, all at once."""
+    some, errors = [], []
+    for D, T in sizes:
+        s = Case(dtype, D, 2, 4, T, [800], 16, seed=D)
+        bounds, ws = s.bounds(), dspark.SelectWorkspace(s.c, 1, T)
+        want = dspark.select_pages(s.c, 1, bounds, s.q, ints([800]), 9, workspace=ws)
+        s.check(bounds, want, 9)
+        some.append((s, bounds, ws, want, ints([800]), torch.empty_like(want), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(some))
+
+    def work(s, bounds, ws, want, length, out, stream):
+        try:
+            start.wait()
+            for _ in range(5000):
+                dspark.select_pages(s.c, 1, bounds, s.q, length, 9, pages=out, workspace=ws, stream=stream)
+        except Exception as e:
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=x) for x in some]
+    every, _ = sys.getswitchinterval(), sys.setswitchinterval(1e-5)
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    sys.setswitchinterval(every)
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for s, _, _, want, _, out, _ in some:
+        assert torch.equal(out, want) and dspark.read_device_error(s.c) == 0
