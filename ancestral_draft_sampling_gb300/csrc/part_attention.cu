@@ -163,13 +163,13 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
     fine = 0 <= from && from <= to && to <= a.B && n >= 0;
     start[tid] = from;
     if (tid + 1 == p.groups) start[p.groups] = to;
-    prefix[tid] = to - from > 1 ? n : 0;
+    prefix[tid] = to > from ? n : 0;
     used[tid] = 0;
   }
   fine = __syncthreads_and(fine);
   if (!fine && tid == 0) cache_error(a.c, kCacheErrGroup);
   long long list = 0;
-  if (fine && tid < p.groups && prefix[tid] > 0) {
+  if (fine && tid < p.groups && prefix[tid] > 0 && start[tid + 1] - start[tid] > 1) {
     const int s = cache_seq(a.c, a.seq, start[tid]), n = prefix[tid];
     list = (long long)s * a.c.max_pages;
     if (s < 0 || n > a.length[start[tid]] || n > (1 << 30) || n > cache_held(a.c, s) * a.c.page_size) {
@@ -182,10 +182,9 @@ __global__ void __launch_bounds__(kItemThreads) prefix_items_kernel(const __grid
   if (fine && q.cnt > 0 && tid >= start[0] && tid < start[p.groups]) {
     g = row_of(start, p.groups, tid);
     hide = prefix[g];
-    if (q.len < hide) {
-      cache_error(a.c, kCacheErrGroup);
-      hide = 0;
-    }
+    const bool less = q.len < hide;
+    if (less) cache_error(a.c, kCacheErrGroup);
+    if (less || start[g + 1] - start[g] == 1) hide = 0;  // a row alone has nobody to share with
     if (hide > 0) used[g] = 1;
   }
   __syncthreads();

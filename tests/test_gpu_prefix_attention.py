@@ -306,3 +306,15 @@ def test_a_wait_that_runs_out_is_reported(cuda, monkeypatch, D, group, T):
     s.run(**a)
     assert torch.equal(a["out"], want[0]) and torch.equal(a["lse"], want[1])
     assert dspark.read_device_error(s.c) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_prefix_that_the_only_row_does_not_have(cuda, dtype):
+    """A group of one row says so too; an empty group's prefix is not looked at."""
+    s = Prefix(dtype, 64, 1, 2, 4, [(100, [5]), (48, [2, 2])], 16, alone=(7,))
+    s.check(*s.run())
+    s.check(*s.run(prefix=[105, 48]))
+    s.check(*s.run(prefix=[106, 48]), error=12)
+    s.check(*s.run(prefix=[2147483647, 48]), error=12)
+    s.check(*s.run(group_start=[0, 0, 0], prefix=[1000, 2147483647]))
+    s.check(*s.run(group_start=[4, 4], prefix=[1000]))
