@@ -6,6 +6,8 @@ import pytest
 import torch
 
 import ancestral_draft_sampling_gb300 as dspark
+from tests.cache_ref import attend_bounds, place, tree_sees
+from tests.test_gpu_tree_units import attend_all
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -114,3 +116,34 @@ def test_more_pages_than_are_counted(cuda):
     dspark.cache_bounds(c, start, length, bounds=bounds, seq=seq)
     assert dspark.read_device_error(c) == 0
     assert torch.equal(bounds[0, 1, 0], c.pool[0, 0, 1, 0].expand(2, -1)) and not bounds[0, 0].any()
+
+
+@pytest.mark.parametrize("dtype,D,kv", [(BF, 128, 2), (BF, 96, 2), (F32, 64, 2)])
+def test_equal_rows_are_right(cuda, dtype, D, kv):
+    """The same: each row's results against 64 bits, over selected pages, behind a
+    prefix and over all."""
+    c, length, _, _, g = small_cache(dtype, 16, D, kv, D)
+    T, heads, count = 3, 4 * kv, 6
+    q = torch.randn(1, T, heads, D, generator=g, device="cuda").to(dtype).expand(4, -1, -1, -1).contiguous()
+    m = length[1]
+    seq, n = ints([1] * 4), ints([m] * 4)
+    bounds = dspark.cache_bounds(c, ints([0] * 4), n, seq=seq)
+    pages = dspark.select_pages(c, 0, bounds, q, n, count, seq=seq)
+    assert (pages == pages[:1]).all()
+    results = {"sparse": dspark.sparse_attention(c, 0, q, n, pages, seq=seq, with_lse=True),
+               "whole": dspark.tree_attention(c, 0, q, n, seq=seq, with_lse=True),
+               "shared": dspark.prefix_attention(c, 0, q, n, ints([0, 4]), ints([500]), seq=seq, with_lse=True)}
+    ids, slots = place(c, 1, m + T)
+    k, v = (c.pool[0, i][ids.cuda(), :, slots.cuda()].transpose(0, 1) for i in (0, 1))
+    sees = tree_sees(m, T, [(2 << t) - 1 for t in range(T)], 0, [0] * T)
+    some = sees[None].repeat(kv, 1, 1)
+    named = torch.zeros(kv, T, m // 16 + 1, dtype=torch.bool)
+    named.scatter_(2, pages[0].cpu().long().transpose(0, 1), True)
+    some[:, :, :m // 16 * 16] = named[:, :, :-1].repeat_interleave(16, dim=2)
+    for name, (out, lse) in results.items():
+        ro, rl, size, reach = attend_all(k, v, q[0], (some[:, None] if name == "sparse" else sees).cuda(), 1 / math.sqrt(D))
+        bo, bl = attend_bounds(size, reach, ro, rl, m + T, D, dtype == BF)
+        for b in range(4):
+            assert ((out[b].double() - ro).abs() <= bo).all(), (name, b)
+            assert ((lse[b].double() - rl).abs() <= bl).all(), (name, b)
+    assert dspark.read_device_error(c) == 0
