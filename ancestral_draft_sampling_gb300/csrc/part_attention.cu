@@ -4,15 +4,16 @@
 // Selected pages: the lists of a sequence's tokens mostly name the same pages.
 // They are made into one list for each key head, each page with a word that says
 // which tokens see it, so that a page is read once for all its tokens' rows
-// together (88 sequences with 8 tokens that choose 32 of 40 pages each: 4.4 GB
-// less than token by token).  Order and repetition in the lists do not matter.
+// together (88 sequences with one to 8 tokens that choose 32 of 40 pages each: 0.9 GB,
+// and 3.3 token by token).  Order and repetition in the lists do not matter.
 //
 // Shared prefixes: softmax(q K^T) V over a sequence's keys is joined from that
 // over its group's prefix and that over what follows, by the maxima m and sums l
 // of both: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  The prefix is one
 // item whose rows are those of all the group's sequences, so its keys are read
-// once for 128 or 256 rows, and its products fill the tensor cores' tiles; prefixes
-// and the rest are one line of tiles, which all blocks share.
+// once for 128 or 256 rows, and its products fill the tensor cores' tiles.  Prefixes
+// and the rest are one line of tiles, which all blocks share, or, where they want
+// different forms of the kernel, a line and a launch each (PrefixArgs::two).
 #include "dspark_common.cuh"
 #include "host_util.cuh"
 #include "part_attention.cuh"
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     const int G = W < l.blocks ? W : l.blocks, q = (int)shares, rest = (int)(shares >> 32);
     const float part = __fdividef(1.0f, (float)G), per = __fdividef((float)G, (float)W);
     // tree_first: rest c < 2^15, so half a unit outweighs float's rounding
+    static_assert(kTreeMaxBlocks * kTreeMaxBlocks < 1 << 15, "rest and c are below the blocks");
     auto first_of = [&](int c) { return q * c + (int)(((float)(rest * c) + 0.5f) * part); };
     // the block of a place, found from beside it
     auto block_of = [&](int at) {

@@ -211,7 +211,7 @@ struct TreeSource<true> {
 // seconds of work, are refused): code comes from memory while a block waits
 // for it, and a 64-bit division is a hundred instructions.
 
-// Where share c of W tiles over G blocks starts: floor(W c / G); c <= G <= 320.
+// Where share c of W tiles over G blocks starts: floor(W c / G); c <= G <= kTreeMaxBlocks.
 __device__ __forceinline__ int tree_first(int W, int G, int c) {
   const uint32_t q = (uint32_t)W / (uint32_t)G, r = (uint32_t)W - q * G;
   return (int)(q * c + r * c / (uint32_t)G);

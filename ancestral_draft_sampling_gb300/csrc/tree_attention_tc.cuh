@@ -61,7 +61,8 @@
 //                to four ahead (walks of their own made each role's code 8 KB
 //                longer, and code comes from memory: 160 KB in all, of which a
 //                unit of a few tiles waited for 9 us); tells the merge what to
-//                do.
+//                do.  (Narrow units of items: warp 0 does this, and writes what
+//                comes of them; warp 2 fills the ring of keys.)
 //   warps 4..7, 8..11  the streams' softmax: rows 32 (w % 4) .. + 31, or keys
 //                32 (w % 4) .. + 31 of all rows of a narrow unit.
 // Tiles that some rows see and others do not (the drafted tokens, a window's
@@ -109,7 +110,7 @@ struct Shape {
   static constexpr uint32_t p_col(uint32_t i) { return apart ? 384 + 64 * i : s_col(i); }
 };
 
-// A unit as warp 2 describes it.
+// A unit as warp 2 (narrow units of items: warp 0) describes it.
 struct SeqUnit {
   int n;            // its tiles here; 0: no more units
   int key;          // first key
@@ -127,7 +128,7 @@ template <bool kItems>
 using Unit = typename std::conditional<kItems, ItemUnit, SeqUnit>::type;
 __device__ __forceinline__ int unit_tokens(const SeqUnit& u) { return u.cnt; }
 __device__ __forceinline__ int unit_tokens(const ItemUnit& u) { return u.tokens; }
-constexpr int kUnits = 4, kUnitReaders = 11;  // warps 0 (2), 1, 3 and the softmax
+constexpr int kUnits = 4, kUnitReaders = 11;  // all warps but the one that describes them
 
 template <bool kItems>
 struct Control {  // shared memory behind the tiles

@@ -710,7 +710,8 @@ DSPARK_API size_t dspark_sparse_workspace_bytes(const dspark_cache* cache, int B
  * All else is as for dspark_tree_attention: q, mask, token_count, scale, out, lse,
  * what a token sees that sees nothing, the workspace, the roundings, the shapes
  * that run on the tensor cores (here with every head_dim up to 128 that is a
- * multiple of 16), and the errors.  Keys and values that a token
+ * multiple of 16: those but 64 and 128 have their weights rounded to bfloat16
+ * here, and not in dspark_tree_attention), and the errors.  Keys and values that a token
  * does not see never reach its result, those of pages that only other tokens'
  * lists name among them.  count * T <= 2^24.  Three launches, graph capturable, no
  * synchronisation.
@@ -741,10 +742,10 @@ DSPARK_API size_t dspark_prefix_workspace_bytes(int B, int T, int heads,
  * A row whose sequence has fewer committed tokens than its group's prefix is
  * attended by itself, as all rows are where group_start is no such list, and a
  * group's where its first row has fewer or does not hold them (error 12).  Results do
- * not depend on it where the pages hold the same tokens, but for the order of the
- * sums.  All else is as for dspark_tree_attention, and the shapes that run on the
- * tensor cores are dspark_sparse_attention's; partial results of both kinds are
- * float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no
+ * not depend on it where the pages hold the same tokens, but for roundings.  All
+ * else is as for dspark_tree_attention, but that the shapes that run on the tensor
+ * cores, with their rounding of the weights, are dspark_sparse_attention's; partial
+ * results of both kinds are float32.  B * T * heads < 2^31.  Three or four launches, graph capturable, no
  * synchronisation.
  */
 DSPARK_API dspark_status dspark_prefix_attention(
